@@ -479,6 +479,100 @@ stof_status stof_oproj_ln_fwd(const void* o, const void* w, const void* bias, co
  * 0 for invalid sizes. */
 size_t stof_oproj_ln_workspace_bytes(int B, int L, int N);
 
+/* ------------------------------------------------------------------ */
+/* Rotary positions                                                     */
+/* ------------------------------------------------------------------ */
+
+/* How a plan's frequencies follow from w_p = theta^(-2 p / rot_dim). */
+typedef enum {
+  STOF_ROPE_PLAIN = 0,    /* w_p */
+  STOF_ROPE_LINEAR = 1,   /* w_p / factor */
+  STOF_ROPE_BY_INDEX = 2, /* w_p for pairs that make at least turns_hi turns in original_length positions, w_p / factor
+                             for those below turns_lo, in between a ramp that is linear in the pair's number: from
+                             low = floor(P(turns_hi)) to high = ceil(P(turns_lo)), P(n) = rot_dim ln(original_length /
+                             (2 pi n)) / (2 ln theta), low clamped to >= 0, high to <= rot_dim - 1 */
+  STOF_ROPE_BY_TURNS = 3  /* the same two ends, with a ramp that is linear in the pair's number of turns */
+} stof_rope_scaling;
+
+/* Rotation of one call, made on the host once and passed to every call
+ * (copied at the call).  step[p] is the angle of pair p per position in
+ * units of 2^-64 turns: position * step[p] modulo 2^64 is then the angle's
+ * fraction of a turn with no rounding at any position. */
+#define STOF_ROPE_MAX_PAIRS 128
+typedef struct {
+  int32_t rot_dim;      /* elements of each head that are turned: the first rot_dim, the rest is copied */
+  int32_t interleaved;  /* pair p is elements (2 p, 2 p + 1) if 1, (p, p + rot_dim / 2) if 0 */
+  float amplitude;      /* factor of the turned elements */
+  int32_t made;         /* set by the functions below; a call refuses a plan without it */
+  uint64_t step[STOF_ROPE_MAX_PAIRS];
+} stof_rope_plan;
+
+/*
+ * Fills *plan.  rot_dim even in [2, 256]; theta > 1; factor > 0 (used unless
+ * STOF_ROPE_PLAIN); original_length >= 1 and 0 < turns_lo < turns_hi (used by
+ * the two ramps); amplitude finite.  Pure host code.
+ */
+stof_status stof_rope_plan_init(stof_rope_plan* plan, int rot_dim, int interleaved, double theta,
+                                stof_rope_scaling scaling, double factor, int64_t original_length, double turns_lo,
+                                double turns_hi, double amplitude);
+
+/* Fills *plan from the caller's own frequencies: HOST array of rot_dim / 2
+ * finite angles per position, in radians. */
+stof_status stof_rope_plan_custom(stof_rope_plan* plan, int rot_dim, int interleaved, const double* frequencies,
+                                  double amplitude);
+
+/* Rows of d contiguous 16-bit elements in device memory: row (b, h, t)
+ * starts at data + b stride_b + h stride_h + t stride_t (elements). */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_h, stride_t;
+} stof_rows;
+
+/*
+ * Rotary positions on the Q and K of B requests of T tokens, moved from the
+ * layout the projection left them in (for instance packed
+ * [B][T][H + 2 Hkv][d]) to the one the attention calls read ([B][H][T][d]),
+ * or into a K/V cache: for every pair (a, c) of a head's first rot_dim
+ * elements
+ *   y[a] = amplitude (x[a] cos phi - x[c] sin phi)
+ *   y[c] = amplitude (x[c] cos phi + x[a] sin phi),   phi = position * frequency of the pair,
+ * in fp32 from an exactly reduced phi, rounded once; the head's other
+ * elements and all of V are copied.
+ *   q, q_out   H heads; both NULL (or H = 0) for none.
+ *   k, k_out   Hkv heads; v, v_out Hkv heads; each pair NULL for none.
+ *              An output may be its input (same data and strides); otherwise
+ *              no output overlaps an input or another output.
+ *   positions  device int32 [B][T], any values; or NULL: token (b, t) has
+ *              position rows[b] + t (t without rows).
+ *   counts     device int32 [B] or NULL (all T): tokens of request b; what
+ *              belongs to later tokens is neither read nor written.
+ *   rows       device int32 [B] or NULL (0): K and V of token (b, t) go to
+ *              row rows[b] + t of k_out and v_out, which have kv_rows rows.
+ *              A row outside [0, kv_rows) is not written and sets
+ *              STOF_DEVERR_BAD_LENGTH in *device_error (device int64 or
+ *              NULL).
+ * rot_dim <= d <= 256, d even.  Any strides and 2-byte aligned data; 16-byte
+ * aligned rows (data, and strides multiples of 8) with d a multiple of 8
+ * and rot_dim of 16 (8 if interleaved) take the wide path.  Asynchronous on
+ * stream; the call needs no workspace.
+ */
+#define STOF_DEVERR_BAD_LENGTH 0x8 /* a length or row from device memory is out of range: skipped */
+stof_status stof_rope_fwd(const stof_rope_plan* plan, const stof_rows* q, const stof_rows* k, const stof_rows* v,
+                          stof_dtype dt, int B, int H, int Hkv, int T, int d, const int32_t* positions,
+                          const int32_t* counts, const int32_t* rows, int kv_rows, const stof_rows* q_out,
+                          const stof_rows* k_out, const stof_rows* v_out, int64_t* device_error, void* stream);
+
+/*
+ * The gradient of stof_rope_fwd() without rows: from the gradients of its
+ * outputs (dq, dk, dv) to those of its inputs, the rotation by -phi with the
+ * same amplitude.  Any strides on both sides: a gradient can go straight into
+ * the packed projection's gradient.  Other arguments as stof_rope_fwd().
+ */
+stof_status stof_rope_bwd(const stof_rope_plan* plan, const stof_rows* dq, const stof_rows* dk, const stof_rows* dv,
+                          stof_dtype dt, int B, int H, int Hkv, int T, int d, const int32_t* positions,
+                          const int32_t* counts, const stof_rows* dq_out, const stof_rows* dk_out,
+                          const stof_rows* dv_out, void* stream);
+
 /*
  * Diagnostic of the failure handling (the paper has no counterpart): every
  * pipeline wait in this library's kernels is bounded in wall time and, when

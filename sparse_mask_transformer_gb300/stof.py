@@ -39,6 +39,13 @@ STOF_KERNEL_BLOCKWISE = 1
 STOF_DEVERR_LOOKBACK_TIMEOUT = 0x1
 STOF_DEVERR_PIPE_TIMEOUT = 0x2
 STOF_DEVERR_BAD_FORMAT = 0x4
+STOF_DEVERR_BAD_LENGTH = 0x8
+
+STOF_ROPE_PLAIN = 0
+STOF_ROPE_LINEAR = 1
+STOF_ROPE_BY_INDEX = 2
+STOF_ROPE_BY_TURNS = 3
+STOF_ROPE_MAX_PAIRS = 128
 
 EXPORTED = ["stof_encode_workspace_bytes", "stof_encode_mask", "stof_format_sync",
             "stof_select_kernel", "stof_mha_fwd", "stof_status_string", "stof_version",
@@ -46,7 +53,7 @@ EXPORTED = ["stof_encode_workspace_bytes", "stof_encode_mask", "stof_format_sync
             "stof_tune_clear", "stof_tune_density_bucket", "stof_encode_mask_bits", "stof_oproj_fwd",
             "stof_encode_rules", "stof_check_bounded_wait", "stof_mha_plan", "stof_mha_fwd_plan",
             "stof_select_kernel_heads", "stof_oproj_ln_fwd", "stof_oproj_ln_workspace_bytes", "stof_ex2_fma",
-            "stof_mha_fwd_cross"]
+            "stof_mha_fwd_cross", "stof_rope_plan_init", "stof_rope_plan_custom", "stof_rope_fwd", "stof_rope_bwd"]
 
 STOF_MAX_RULES = 64
 INT32_MIN, INT32_MAX = -(1 << 31), (1 << 31) - 1
@@ -109,6 +116,16 @@ class stof_plan(ctypes.Structure):
                 ("softmax_warpgroups", ctypes.c_int)]
 
 
+class stof_rope_plan(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("made", ctypes.c_int32), ("step", ctypes.c_uint64 * STOF_ROPE_MAX_PAIRS)]
+
+
+class stof_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64)]
+
+
 _lib = None
 _synth = None
 
@@ -164,6 +181,19 @@ def load_library(path: str = LIB_PATH):
         lib.stof_oproj_ln_fwd.restype = i32
         lib.stof_oproj_ln_workspace_bytes.argtypes = [i32, i32, i32]
         lib.stof_oproj_ln_workspace_bytes.restype = sz
+        lib.stof_rope_plan_init.argtypes = [ctypes.POINTER(stof_rope_plan), i32, i32, ctypes.c_double, i32,
+                                            ctypes.c_double, i64, ctypes.c_double, ctypes.c_double, ctypes.c_double]
+        lib.stof_rope_plan_init.restype = i32
+        lib.stof_rope_plan_custom.argtypes = [ctypes.POINTER(stof_rope_plan), i32, i32, ctypes.POINTER(ctypes.c_double),
+                                              ctypes.c_double]
+        lib.stof_rope_plan_custom.restype = i32
+        R = ctypes.POINTER(stof_rows)
+        lib.stof_rope_fwd.argtypes = [ctypes.POINTER(stof_rope_plan), R, R, R, i32, i32, i32, i32, i32, i32, P, P, P, i32,
+                                      R, R, R, P, P]
+        lib.stof_rope_fwd.restype = i32
+        lib.stof_rope_bwd.argtypes = [ctypes.POINTER(stof_rope_plan), R, R, R, i32, i32, i32, i32, i32, i32, P, P,
+                                      R, R, R, P]
+        lib.stof_rope_bwd.restype = i32
         lib.stof_tune_workspace_bytes.argtypes = [i32, i32]
         lib.stof_tune_workspace_bytes.restype = sz
         lib.stof_tune.argtypes = [P, i32, P, P, P, i32, i32, i32, i32, i32, ctypes.c_float, i64, i64, P, sz, P,
@@ -492,6 +522,125 @@ def stof_oproj_ln_fwd(o: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | Non
         B, H, L, d, N, y.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         ptr(device_error), _stream(stream)), "stof_oproj_ln_fwd")
     return y
+
+
+def _device_of(where: str, tensors: dict) -> torch.device:
+    """The one CUDA device all the given tensors (None: absent) are on."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise StofError(STOF_ERR_INVALID_ARG, f"{where}: {name} must be a CUDA tensor")
+        if device is not None and t.device != device:
+            raise StofError(STOF_ERR_INVALID_ARG, f"{where}: {name} is on another device")
+        device = t.device
+    if device is None:
+        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: no tensor given")
+    return device
+
+
+def _launch(device: torch.device, stream, where: str, call) -> None:
+    """call(stream pointer) with `device` current, on `stream` or that device's current stream."""
+    with torch.cuda.device(device):
+        _check(call(_stream(torch.cuda.current_stream(device) if stream is None else stream)), where)
+
+
+def _int32(where: str, name: str, t: torch.Tensor | None, shape: tuple) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise StofError(STOF_ERR_SHAPE, f"{where}: {name} must be contiguous int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _error_word(where: str, t: torch.Tensor | None) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != torch.int64 or t.numel() != 1:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: device_error must be one int64")
+    return t.data_ptr()
+
+
+def stof_rope_plan_init(rot_dim: int, theta: float = 10000.0, interleaved: bool = False,
+                        scaling: int = STOF_ROPE_PLAIN, factor: float = 1.0, original_length: int = 1,
+                        turns_lo: float = 1.0, turns_hi: float = 32.0, amplitude: float = 1.0) -> stof_rope_plan:
+    """The rotation of the first rot_dim elements of a head, frequencies theta^(-2p/rot_dim) scaled as
+    `scaling` says; pairs are the two halves of those elements, or neighbours if interleaved."""
+    plan = stof_rope_plan()
+    _check(load_library().stof_rope_plan_init(
+        ctypes.byref(plan), int(rot_dim), int(bool(interleaved)), float(theta), int(scaling), float(factor),
+        int(original_length), float(turns_lo), float(turns_hi), float(amplitude)), "stof_rope_plan_init")
+    return plan
+
+
+def stof_rope_plan_custom(frequencies, interleaved: bool = False, amplitude: float = 1.0) -> stof_rope_plan:
+    """The rotation with the caller's own frequencies (radians per position, one per pair)."""
+    f = [float(x) for x in frequencies]
+    plan = stof_rope_plan()
+    _check(load_library().stof_rope_plan_custom(ctypes.byref(plan), 2 * len(f), int(bool(interleaved)),
+                                                (ctypes.c_double * max(1, len(f)))(*f), float(amplitude)),
+           "stof_rope_plan_custom")
+    return plan
+
+
+def _rope(where, plan, x, y, positions, counts, rows, device_error, stream):
+    """x, y: (q, k, v) and their outputs, [B, heads, T, d] with contiguous rows of d, any other strides."""
+    named = dict(zip(("q", "k", "v", "q_out", "k_out", "v_out"), (*x, *y)))
+    device = _device_of(where, {**named, "positions": positions, "counts": counts, "rows": rows,
+                                "device_error": device_error})
+    given = [t for t in x if t is not None]
+    if not given:
+        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: give q or k")
+    for name, t in named.items():
+        if t is not None and (t.dim() != 4 or t.dtype != given[0].dtype or (t.shape[3] > 1 and t.stride(3) != 1)):
+            raise StofError(STOF_ERR_SHAPE, f"{where}: {name} must be [B, heads, T, d], rows contiguous, of one dtype")
+    q, k, v = x
+    B, _, T, d = given[0].shape
+    for a, out in zip(x, y):
+        if (a is None) != (out is None):
+            raise StofError(STOF_ERR_INVALID_ARG, f"{where}: an input needs its output")
+        if a is not None and (tuple(a.shape) != (B, a.shape[1], T, d) or (B, a.shape[1], d) != (out.shape[0], out.shape[1],
+                                                                                                out.shape[3])):
+            raise StofError(STOF_ERR_SHAPE, f"{where}: shapes differ")
+    if v is not None and (k is None or v.shape != k.shape or y[2].shape != y[1].shape):
+        raise StofError(STOF_ERR_SHAPE, f"{where}: v goes with a k of its shape")
+    if q is not None and y[0].shape[2] != T:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q_out must have q's shape")
+    kv_rows = T if k is None else y[1].shape[2]
+    if rows is None and kv_rows < T:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: k_out has fewer rows than k")
+    c = [None if t is None else ctypes.byref(stof_rows(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+         for t in (*x, *y)]
+    head = (ctypes.byref(plan), *c[:3], _dtype_code(given[0]), B, 0 if q is None else q.shape[1],
+            0 if k is None else k.shape[1], T, d, _int32(where, "positions", positions, (B, T)),
+            _int32(where, "counts", counts, (B,)))
+    lib = load_library()
+    if where == "stof_rope_bwd":
+        _launch(device, stream, where, lambda s: lib.stof_rope_bwd(*head, *c[3:], s))
+    else:
+        args = (*head, _int32(where, "rows", rows, (B,)), kv_rows, *c[3:], _error_word(where, device_error))
+        _launch(device, stream, where, lambda s: lib.stof_rope_fwd(*args, s))
+    return y
+
+
+def stof_rope_fwd(plan: stof_rope_plan, q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
+                  q_out: torch.Tensor | None, k_out: torch.Tensor | None, v_out: torch.Tensor | None,
+                  positions: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                  rows: torch.Tensor | None = None, device_error: torch.Tensor | None = None, stream=None):
+    """q [B, H, T, d], k and v [B, Hkv, T, d] (views of a packed projection included) turned by their positions
+    (int32 [B, T]; None: rows[b] + t) and written to q_out [B, H, T, d] and k_out, v_out [B, Hkv, T or more, d],
+    there from row rows[b] (int32 [B]; None: 0) on.  counts (int32 [B]): tokens of each request.  Returns the outputs."""
+    return _rope("stof_rope_fwd", plan, (q, k, v), (q_out, k_out, v_out), positions, counts, rows, device_error, stream)
+
+
+def stof_rope_bwd(plan: stof_rope_plan, dq: torch.Tensor | None, dk: torch.Tensor | None, dv: torch.Tensor | None,
+                  dq_out: torch.Tensor | None, dk_out: torch.Tensor | None, dv_out: torch.Tensor | None,
+                  positions: torch.Tensor | None = None, counts: torch.Tensor | None = None, stream=None):
+    """Gradients of stof_rope_fwd's outputs (no rows) to those of its inputs; any strides on both sides."""
+    if dk_out is not None and dk is not None and dk_out.dim() == 4 and dk.dim() == 4 and dk_out.shape[2] != dk.shape[2]:
+        raise StofError(STOF_ERR_SHAPE, "stof_rope_bwd: dk_out must have dk's shape")
+    return _rope("stof_rope_bwd", plan, (dq, dk, dv), (dq_out, dk_out, dv_out), positions, counts, None, None, stream)
 
 
 def stof_tune_workspace_bytes(n_masks: int, L: int) -> int:
