@@ -238,6 +238,27 @@ typedef struct {
 stof_status stof_encode_rules(const stof_mask_rule* rules, int n_masks, int lq, int lk, int bm, int bn,
                               void* workspace, size_t ws_bytes, stof_format* fmt, void* stream);
 
+/*
+ * Same as stof_encode_mask() for the masks of packed documents: element
+ * (i, j) of a mask is valid iff query i and key j belong to the same document
+ * and the key is not later than the query:
+ *     q_doc[i] == k_doc[j] >= 0  and  k_order[j] <= q_order[i].
+ *   q_doc, q_order   device int32 [n_masks][lq], 4-byte aligned;
+ *   k_doc, k_order   device int32 [n_masks][lk].  A document is any number
+ *                    >= 0; a token with a negative one (padding) sees and is
+ *                    seen by nothing.  The orders are any numbers; both may
+ *                    be NULL: every key of the document is valid.
+ * Examples: causal, the token's index (or position) as both orders; the last
+ * lq tokens of lk as queries, q_order[i] = lk - lq + i; a prefix that its
+ * whole document sees, k_order[j] = INT32_MIN for the prefix's keys; tokens
+ * that see their own chunk and earlier ones, the chunk's number as both.
+ * No mask is read: the encoder computes every IT word from these arrays.
+ * Sizes, workspace and errors as stof_encode_mask().
+ */
+stof_status stof_encode_documents(const int32_t* q_doc, const int32_t* k_doc, const int32_t* q_order,
+                                  const int32_t* k_order, int n_masks, int lq, int lk, int bm, int bn, void* workspace,
+                                  size_t ws_bytes, stof_format* fmt, void* stream);
+
 /* Blocks until the work queued on stream is done, copies the tile counts
  * and the device error word into fmt, and sets fmt->synced.  Returns
  * STOF_ERR_DEVICE if the device error word is non-zero. */
@@ -315,6 +336,35 @@ stof_status stof_mha_fwd(const void* q, const void* k, const void* v, stof_dtype
 stof_status stof_mha_fwd_cross(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Lq,
                                int Lk, int d, float scale, const stof_format* fmt, int64_t mask_stride_b,
                                int64_t mask_stride_h, stof_kernel which, void* o, void* stream);
+
+/* What becomes of a score scale * Q.K before the softmax. */
+typedef struct {
+  float softcap;        /* > 0: score <- softcap * tanh(score / softcap); 0: none */
+  const float* slopes;  /* device fp32 [H] (4-byte aligned) or NULL: then score <- score - slopes[h] * |i + q_start - j|,
+                           finite slopes of either sign */
+  int32_t q_start;      /* position of query row 0 among the keys, in [-2^30, 2^30]; read only with slopes */
+} stof_score;
+
+/*
+ * stof_mha_fwd_cross() with scores that are capped, lowered with the
+ * distance of query and key, or both (in that order), and with K and V heads
+ * shared by groups of query heads:
+ *   q, o      device [B][H][Lq][d];  k, v  device [B][Hkv][Lk][d], H a
+ *             multiple of Hkv; query head h reads K/V head h / (H / Hkv).
+ *   score     HOST struct, copied at the call, or NULL for plain scores.
+ *   which     as stof_mha_fwd(); STOF_KERNEL_AUTO also takes a format that is
+ *             not synced and then runs the block-wise kernel wherever it
+ *             takes the sizes (d 64 or 128, 128 x 64 or 128 x 128 OTs), else
+ *             the row-wise one, so that encoding and attention need no host
+ *             round trip between them.
+ * The scores are capped and lowered in fp32 (the cap to a few 2^-24 of
+ * softcap).  Masked keys take no part whatever their scores; as in
+ * stof_mha_fwd(), K and V rows inside a listed OT have to be finite.  Other
+ * arguments, formats and errors as stof_mha_fwd_cross().
+ */
+stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Hkv, int Lq,
+                               int Lk, int d, float scale, const stof_score* score, const stof_format* fmt,
+                               int64_t mask_stride_b, int64_t mask_stride_h, stof_kernel which, void* o, void* stream);
 
 /* Where a plan's choice came from. */
 #define STOF_PLAN_FORCED 0    /* the caller named the kernel */

@@ -468,6 +468,106 @@ __global__ void __launch_bounds__(kThreads, 7) encode_rules_kernel(const EncodeP
   finish_chunk(p, chunk, g, cs, s_words, local_nnz, tid);
 }
 
+// Phase 1 for a document mask: element (i, j) is valid iff query i and key j
+// are of one document (q_doc[i] == k_doc[j] >= 0) and the key is not later
+// than the query (k_order[j] <= q_order[i]).  The chunk's numbers come to
+// shared memory once; each group of 8 rows or columns is summarised (its one
+// document, if it has one, and its least and greatest order), which settles
+// most ITs of packed documents (other documents: empty; the same document
+// and every key earlier: full) without looking at their 64 elements.
+constexpr int kMaxChunkCols = 1024;  // ct * bn at most (encode_geometry)
+constexpr int kMixed = -3;           // a group of several documents
+
+struct DocChunk {
+  int q_doc[256], q_ord[256];
+  int k_doc[kMaxChunkCols], k_ord[kMaxChunkCols];
+  int4 q_sum[256 / 8], k_sum[kMaxChunkCols / 8];  // document or kMixed, least order, greatest order
+};
+
+__device__ __forceinline__ int4 group_summary(const int* doc, const int* ord) {
+  int d = doc[0], lo = ord[0], hi = ord[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    if (doc[e] != d) d = kMixed;
+    lo = min(lo, ord[e]);
+    hi = max(hi, ord[e]);
+  }
+  return make_int4(d, lo, hi, 0);
+}
+
+__global__ void __launch_bounds__(kThreads) encode_documents_kernel(const EncodeParams p, const DocSet ds) {
+  extern __shared__ uint64_t s_words[];  // [bm/8][nt * bn/8]
+  __shared__ long long s_chunk;
+  __shared__ ChunkState cs;
+  __shared__ DocChunk dc;
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    s_chunk = static_cast<long long>(atomicAdd(p.ticket, 1ull));
+    cs.nnz = 0;
+  }
+  __syncthreads();
+  const long long chunk = s_chunk;
+  if (chunk >= p.n_chunks) return;
+  const ChunkGeom g = chunk_geom(p, chunk);
+  const int i0 = g.I * p.bm, j0 = g.J0 * p.bn, cols = g.itcols * 8;
+  const int32_t* qd = ds.q_doc + static_cast<long long>(g.m) * p.lq;
+  const int32_t* kd = ds.k_doc + static_cast<long long>(g.m) * p.lk;
+  const int32_t* qo = ds.q_order ? ds.q_order + static_cast<long long>(g.m) * p.lq : nullptr;
+  const int32_t* ko = ds.k_order ? ds.k_order + static_cast<long long>(g.m) * p.lk : nullptr;
+  // rows and columns past the mask's sides belong to no document (two
+  // different numbers below 0, and an order that is never the earlier)
+  for (int r = tid; r < p.bm; r += kThreads) {
+    const bool in = i0 + r < p.lq;
+    const int d = in ? __ldg(qd + i0 + r) : -1;
+    dc.q_doc[r] = d < 0 ? -1 : d;
+    dc.q_ord[r] = in && qo ? __ldg(qo + i0 + r) : 0;
+  }
+  for (int c = tid; c < cols; c += kThreads) {
+    const bool in = j0 + c < p.lk;
+    const int d = in ? __ldg(kd + j0 + c) : -2;
+    dc.k_doc[c] = d < 0 ? -2 : d;
+    dc.k_ord[c] = in && ko ? __ldg(ko + j0 + c) : 0;
+  }
+  __syncthreads();
+  for (int e = tid; e < g.bands + g.itcols; e += kThreads) {
+    if (e < g.bands)
+      dc.q_sum[e] = group_summary(dc.q_doc + 8 * e, dc.q_ord + 8 * e);
+    else
+      dc.k_sum[e - g.bands] = group_summary(dc.k_doc + 8 * (e - g.bands), dc.k_ord + 8 * (e - g.bands));
+  }
+  __syncthreads();
+  unsigned long long local_nnz = 0;
+  const int nw = g.bands * g.itcols;
+  for (int w = tid; w < nw; w += kThreads) {
+    const int pb = w / g.itcols, qc = w - pb * g.itcols;
+    const int4 a = dc.q_sum[pb], b = dc.k_sum[qc];
+    uint64_t word = 0;
+    if (a.x != kMixed && b.x != kMixed && (a.x != b.x || b.y > a.z)) {
+      // one document each, and not the same or every key later: empty
+    } else if (a.x != kMixed && a.x == b.x && b.z <= a.y) {
+      word = ~0ull;
+    } else {
+      int kdoc[8], kord[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        kdoc[c] = dc.k_doc[8 * qc + c];
+        kord[c] = dc.k_ord[8 * qc + c];
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int d = dc.q_doc[8 * pb + r], o = dc.q_ord[8 * pb + r];
+        uint32_t bits = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) bits |= (kdoc[c] == d && kord[c] <= o) ? 1u << c : 0u;
+        word |= static_cast<uint64_t>(bits) << (8 * r);
+      }
+    }
+    s_words[w] = word;
+    local_nnz += __popcll(word);
+  }
+  finish_chunk(p, chunk, g, cs, s_words, local_nnz, tid);
+}
+
 // ---------------------------------------------------------------- bit-packed masks
 // A bit-packed mask is an eighth of the dense one, so reading it twice costs
 // less than the single-pass encoder's wait for its predecessors: three short
@@ -801,6 +901,12 @@ cudaError_t launch_encode_rules(const EncodeParams& p_in, const EncodeGeom& g, c
                            static_cast<int>(g.smem_bytes)) != cudaSuccess)
     return cudaGetLastError();
   encode_rules_kernel<<<static_cast<unsigned>(g.n_chunks), kThreads, g.smem_bytes, s>>>(p, rs);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_encode_documents(const EncodeParams& p_in, const EncodeGeom& g, const DocSet& ds, cudaStream_t s) {
+  const EncodeParams p = with_reciprocals(p_in);
+  encode_documents_kernel<<<static_cast<unsigned>(g.n_chunks), kThreads, g.smem_bytes, s>>>(p, ds);
   return cudaGetLastError();
 }
 

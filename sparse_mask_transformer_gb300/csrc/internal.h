@@ -82,6 +82,16 @@ struct RuleSet {
 };
 cudaError_t launch_encode_rules(const EncodeParams& p, const EncodeGeom& g, const RuleSet& rs, cudaStream_t s);
 
+// Document masks (stof_encode_documents): device arrays [n_masks][lq] and
+// [n_masks][lk]; the orders may both be null (every key is early enough).
+struct DocSet {
+  const int32_t* q_doc;
+  const int32_t* k_doc;
+  const int32_t* q_order;
+  const int32_t* k_order;
+};
+cudaError_t launch_encode_documents(const EncodeParams& p, const EncodeGeom& g, const DocSet& ds, cudaStream_t s);
+
 // Scratch of stof_encode_mask_noalloc(): a static device array with room
 // for the ticket and kNoAllocMaxChunks look-back words.  The address is
 // looked up once per device (the current one) and cached.
@@ -115,6 +125,16 @@ struct AttnParams {
   int variant;                     // block-wise: kVariantAuto, kVariantPerTile or kVariantPersistent
   int exp_split;                   // block-wise: 1 = one key pair in eight exponentiated on the FMA pipe
   int softmax_wg;                  // block-wise softmax warpgroups: 2, or 4 (persistent, d = 64); 0 = 2
+};
+// A call whose scores are capped or lowered by distance, or whose K and V
+// heads are shared (stof_mha_fwd_score).  AttnParams' scale_log2 holds the
+// scale times log2(e) as ever.
+struct ScoredParams : AttnParams {
+  int group;               // query heads per K/V head
+  float scale;             // the softmax scale itself
+  float softcap;           // > 0: scores become softcap * tanh(score / softcap)
+  const float* slopes;     // [H] or null: scores are lowered by slopes[h] * |i + q_start - j|
+  int q_start;
 };
 // Block-wise kernel variants: one CTA per query tile, or persistent CTAs
 // (d = 64 only); auto picks by the mean listed OTs per OT row.
@@ -173,6 +193,7 @@ stof_status mha_fwd_choice(const void* q, const void* k, const void* v, stof_dty
                            int d, float scale, const stof_format* fmt, int64_t mask_stride_b, int64_t mask_stride_h,
                            const KernelChoice& c, void* o, void* stream);
 cudaError_t launch_rowwise(const AttnParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_rowwise_scored(const ScoredParams& p, bool bf16, cudaStream_t s);
 // Density bucket of the tuning cache.
 int tune_density_bucket(double density);
 // Returns STOF_OK or an error status (tensor-map encoding / launch).

@@ -29,11 +29,16 @@
 //      merge once at the end.
 // Scores are in the log2 domain (scale * log2 e folded into q); everything
 // after the input loads is fp32.
+// SCORED instances serve stof_mha_fwd_score: K and V heads shared by groups
+// of query heads, scores capped and / or lowered by distance (score.cuh).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "internal.h"
+#include "score.cuh"
 
 namespace stof {
 
@@ -95,13 +100,16 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+template <bool SCORED>
+using RowwiseParams = std::conditional_t<SCORED, ScoredParams, AttnParams>;
+
 // LPR: lanes per query row (32, 16 or 8).  Every loop of the kernel is
 // uniform over the warp (the most OTs, slots or keys of the warp's rows; a
 // row with fewer has its surplus entries masked), so all shuffles are
 // whole-warp operations over LPR-lane segments and no segment waits on a
 // diverged one.
-template <int D, bool BF16, int LPR>
-__global__ void __launch_bounds__(kWarps * 32, 5) rowwise_kernel(const AttnParams p) {
+template <int D, bool BF16, int LPR, bool SCORED>
+__global__ void __launch_bounds__(kWarps * 32, 5) rowwise_kernel(const RowwiseParams<SCORED> p) {
   constexpr int RPW = 32 / LPR;    // query rows per warp
   constexpr int G = D / 16;        // lanes per key
   static_assert(LPR >= G && LPR % G == 0, "a row needs at least one key group");
@@ -140,13 +148,20 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rowwise_kernel(const AttnParam
   const int g = sl / G;            // key group
   const int sub = sl % G;          // 16-dim slice
   const size_t row_bytes = static_cast<size_t>(D) * 2;
-  const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + bh * p.Lk * row_bytes + sub * 32;
-  const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + bh * p.Lk * row_bytes + sub * 32;
+  long long kv = bh;  // K and V head
+  if constexpr (SCORED) kv = static_cast<long long>(b) * (p.H / p.group) + h / p.group;
+  const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + kv * p.Lk * row_bytes + sub * 32;
+  const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + kv * p.Lk * row_bytes + sub * 32;
 
   float qf[16];
   widen16<BF16>(load_raw16(static_cast<const uint8_t*>(p.q) + row * row_bytes + sub * 32), qf);
+  ScoreRow score;  // SCORED: the row's cap and distance terms
+  if constexpr (SCORED) {
+    score = make_score_row(p.scale, p.softcap, p.slopes ? __ldg(p.slopes + h) : 0.f, i + p.q_start);
+  } else {
 #pragma unroll
-  for (int t = 0; t < 16; ++t) qf[t] *= p.scale_log2;
+    for (int t = 0; t < 16; ++t) qf[t] *= p.scale_log2;
+  }
 
   float m_ref = -INFINITY, l = 0.f, o[16];
 #pragma unroll
@@ -176,6 +191,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rowwise_kernel(const AttnParam
       float dot = d0 + d1;
 #pragma unroll
       for (int off = G / 2; off; off >>= 1) dot += __shfl_xor_sync(kAll, dot, off);
+      if constexpr (SCORED) dot = score_of(score, dot, key[u]);
       s[u] = key[u] >= 0 ? dot : -INFINITY;
     }
     float mx = s[0];
@@ -334,39 +350,46 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rowwise_kernel(const AttnParam
   }
 }
 
-template <int D, bool BF16, int LPR>
-cudaError_t launch_rw(const AttnParams& p, cudaStream_t s) {
+template <int D, bool BF16, int LPR, bool SCORED>
+cudaError_t launch_rw(const RowwiseParams<SCORED>& p, cudaStream_t s) {
   const long long rows = static_cast<long long>(p.B) * p.H * p.L;
   const long long rows_per_cta = static_cast<long long>(kWarps) * (32 / LPR);
   const long long blocks = (rows + rows_per_cta - 1) / rows_per_cta;
-  rowwise_kernel<D, BF16, LPR><<<static_cast<unsigned>(blocks), kWarps * 32, 0, s>>>(p);
+  rowwise_kernel<D, BF16, LPR, SCORED><<<static_cast<unsigned>(blocks), kWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, bool BF16>
-cudaError_t launch_rw_d(const AttnParams& p, cudaStream_t s) {
+template <int D, bool BF16, bool SCORED>
+cudaError_t launch_rw_d(const RowwiseParams<SCORED>& p, cudaStream_t s) {
   const int rpw = rowwise_rows_per_warp(static_cast<long long>(p.B) * p.H * p.L, p.keys_per_row,
                                         p.listed128_per_row, p.rows_per_warp);
   // a key needs D / 16 lanes: d = 256 fits 2 rows per warp at most
   if constexpr (D / 16 <= 8) {
-    if (rpw == 4) return launch_rw<D, BF16, 8>(p, s);
+    if (rpw == 4) return launch_rw<D, BF16, 8, SCORED>(p, s);
   } else {
-    if (rpw == 4) return launch_rw<D, BF16, 16>(p, s);
+    if (rpw == 4) return launch_rw<D, BF16, 16, SCORED>(p, s);
   }
-  if (rpw == 2) return launch_rw<D, BF16, 16>(p, s);
-  return launch_rw<D, BF16, 32>(p, s);
+  if (rpw == 2) return launch_rw<D, BF16, 16, SCORED>(p, s);
+  return launch_rw<D, BF16, 32, SCORED>(p, s);
+}
+
+template <bool SCORED>
+cudaError_t launch_rowwise_t(const RowwiseParams<SCORED>& p, bool bf16, cudaStream_t s) {
+  switch (p.d) {
+    case 32: return bf16 ? launch_rw_d<32, true, SCORED>(p, s) : launch_rw_d<32, false, SCORED>(p, s);
+    case 64: return bf16 ? launch_rw_d<64, true, SCORED>(p, s) : launch_rw_d<64, false, SCORED>(p, s);
+    case 128: return bf16 ? launch_rw_d<128, true, SCORED>(p, s) : launch_rw_d<128, false, SCORED>(p, s);
+    case 256: return bf16 ? launch_rw_d<256, true, SCORED>(p, s) : launch_rw_d<256, false, SCORED>(p, s);
+    default: return cudaErrorInvalidValue;  // the host checks d first
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_rowwise(const AttnParams& p, bool bf16, cudaStream_t s) {
-  switch (p.d) {
-    case 32: return bf16 ? launch_rw_d<32, true>(p, s) : launch_rw_d<32, false>(p, s);
-    case 64: return bf16 ? launch_rw_d<64, true>(p, s) : launch_rw_d<64, false>(p, s);
-    case 128: return bf16 ? launch_rw_d<128, true>(p, s) : launch_rw_d<128, false>(p, s);
-    case 256: return bf16 ? launch_rw_d<256, true>(p, s) : launch_rw_d<256, false>(p, s);
-    default: return cudaErrorInvalidValue;  // the host checks d first
-  }
+cudaError_t launch_rowwise(const AttnParams& p, bool bf16, cudaStream_t s) { return launch_rowwise_t<false>(p, bf16, s); }
+
+cudaError_t launch_rowwise_scored(const ScoredParams& p, bool bf16, cudaStream_t s) {
+  return launch_rowwise_t<true>(p, bf16, s);
 }
 
 }  // namespace stof

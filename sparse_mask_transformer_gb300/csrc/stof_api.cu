@@ -82,10 +82,11 @@ size_t stof_encode_workspace_bytes(int n_masks, int lq, int lk, int bm, int bn) 
 }
 
 // Encodes from a dense (bits = 0) or bit-packed (bits = 1) mask, or, with
-// mask = NULL, from the rules in *rules.
-static stof_status encode_impl(const uint8_t* mask, int bits, const RuleSet* rules, int n_masks, int lq, int lk,
-                               int bm, int bn, void* workspace, size_t ws_bytes, stof_format* fmt, void* stream) {
-  if ((!mask && !rules) || !workspace || !fmt) return STOF_ERR_INVALID_ARG;
+// mask = NULL, from the rules in *rules or the documents in *docs.
+static stof_status encode_impl(const uint8_t* mask, int bits, const RuleSet* rules, const DocSet* docs, int n_masks,
+                               int lq, int lk, int bm, int bn, void* workspace, size_t ws_bytes, stof_format* fmt,
+                               void* stream) {
+  if ((!mask && !rules && !docs) || !workspace || !fmt) return STOF_ERR_INVALID_ARG;
   if (n_masks < 1 || lq < 1 || lk < 1 || bm < 1 || bn < 1) return STOF_ERR_INVALID_ARG;
   EncodeGeom g;
   if (!encode_geometry(n_masks, lq, lk, bm, bn, &g)) return STOF_ERR_SHAPE;
@@ -140,7 +141,9 @@ static stof_status encode_impl(const uint8_t* mask, int bits, const RuleSet* rul
   p.status = reinterpret_cast<unsigned long long*>(ws + w.status);
   p.cls = ws + w.cls;
   p.rowcnt = reinterpret_cast<int32_t*>(ws + w.rowcnt);
-  const cudaError_t e = rules ? launch_encode_rules(p, g, *rules, s) : launch_encode(p, g, s);
+  const cudaError_t e = rules  ? launch_encode_rules(p, g, *rules, s)
+                        : docs ? launch_encode_documents(p, g, *docs, s)
+                               : launch_encode(p, g, s);
   if (record_cuda(e) != cudaSuccess) return STOF_ERR_CUDA;
   return STOF_OK;
 }
@@ -148,13 +151,13 @@ static stof_status encode_impl(const uint8_t* mask, int bits, const RuleSet* rul
 stof_status stof_encode_mask(const uint8_t* mask, int n_masks, int lq, int lk, int bm, int bn,
                              void* workspace, size_t ws_bytes, stof_format* fmt, void* stream) {
   if (!mask) return STOF_ERR_INVALID_ARG;
-  return encode_impl(mask, 0, nullptr, n_masks, lq, lk, bm, bn, workspace, ws_bytes, fmt, stream);
+  return encode_impl(mask, 0, nullptr, nullptr, n_masks, lq, lk, bm, bn, workspace, ws_bytes, fmt, stream);
 }
 
 stof_status stof_encode_mask_bits(const uint8_t* mask_bits, int n_masks, int lq, int lk, int bm, int bn,
                                   void* workspace, size_t ws_bytes, stof_format* fmt, void* stream) {
   if (!mask_bits) return STOF_ERR_INVALID_ARG;
-  return encode_impl(mask_bits, 1, nullptr, n_masks, lq, lk, bm, bn, workspace, ws_bytes, fmt, stream);
+  return encode_impl(mask_bits, 1, nullptr, nullptr, n_masks, lq, lk, bm, bn, workspace, ws_bytes, fmt, stream);
 }
 
 stof_status stof_encode_rules(const stof_mask_rule* rules, int n_masks, int lq, int lk, int bm, int bn,
@@ -180,7 +183,17 @@ stof_status stof_encode_rules(const stof_mask_rule* rules, int n_masks, int lq, 
     r.block = u.blocks ? u.block : 8;
     r.nbc = u.blocks ? lk / u.block : 0;
   }
-  return encode_impl(nullptr, 0, &rs, n_masks, lq, lk, bm, bn, workspace, ws_bytes, fmt, stream);
+  return encode_impl(nullptr, 0, &rs, nullptr, n_masks, lq, lk, bm, bn, workspace, ws_bytes, fmt, stream);
+}
+
+stof_status stof_encode_documents(const int32_t* q_doc, const int32_t* k_doc, const int32_t* q_order,
+                                  const int32_t* k_order, int n_masks, int lq, int lk, int bm, int bn, void* workspace,
+                                  size_t ws_bytes, stof_format* fmt, void* stream) {
+  if (!q_doc || !k_doc || !q_order != !k_order) return STOF_ERR_INVALID_ARG;
+  if (!aligned(q_doc, 4) || !aligned(k_doc, 4) || !aligned(q_order, 4) || !aligned(k_order, 4))
+    return STOF_ERR_ALIGNMENT;
+  const DocSet ds{q_doc, k_doc, q_order, k_order};
+  return encode_impl(nullptr, 0, nullptr, &ds, n_masks, lq, lk, bm, bn, workspace, ws_bytes, fmt, stream);
 }
 
 // Variant of stof_encode_mask() that allocates nothing and needs no device
@@ -383,6 +396,17 @@ static stof_status check_call(const void* q, const void* k, const void* v, stof_
   return STOF_OK;
 }
 
+// Score options of a call with this scale.
+static stof_status check_score(const stof_score& s, float scale) {
+  if (!std::isfinite(s.softcap) || s.softcap < 0.f) return STOF_ERR_INVALID_ARG;
+  // 2 log2(e) scale / softcap is a factor of the capped scores
+  if (s.softcap > 0.f && (!std::isfinite(3.f * (scale / s.softcap)) || !std::isfinite(3.f * s.softcap)))
+    return STOF_ERR_INVALID_ARG;
+  if (s.q_start < -(1 << 30) || s.q_start > (1 << 30)) return STOF_ERR_SHAPE;
+  if (!aligned(s.slopes, 4)) return STOF_ERR_ALIGNMENT;
+  return STOF_OK;
+}
+
 // What runs for `which` on this format: a forced kernel, a cached tuning
 // result or the analytic model.
 static stof_status plan_call(const stof_format& f, int B, int H, int L, int Lk, int d, stof_kernel which,
@@ -447,18 +471,10 @@ stof_status stof_mha_plan(const stof_format* fmt, int B, int H, int L, int d, st
 
 namespace stof {
 
-stof_status mha_fwd_choice(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int L, int Lk,
-                           int d,
-                           float scale, const stof_format* fmt, int64_t mask_stride_b, int64_t mask_stride_h,
-                           const KernelChoice& c, void* o, void* stream) {
-  const stof_status st = check_call(q, k, v, dt, B, H, L, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
-  if (st != STOF_OK) return st;
-  if (c.kernel != STOF_KERNEL_ROWWISE && c.kernel != STOF_KERNEL_BLOCKWISE) return STOF_ERR_INVALID_ARG;
-  if (c.kernel == STOF_KERNEL_BLOCKWISE && (!blockwise_tiles(*fmt) || (d != 64 && d != 128)))
-    return STOF_ERR_UNSUPPORTED;
-  if (c.kernel == STOF_KERNEL_ROWWISE && d == 256 && c.rows_per_warp == 4)
-    return STOF_ERR_UNSUPPORTED;  // a d = 256 key needs 16 lanes: 2 rows per warp at most
-  AttnParams p;
+// The kernels' parameters of a checked call.
+static void fill_params(AttnParams& p, const void* q, const void* k, const void* v, int B, int H, int L, int Lk, int d,
+                        float scale, const stof_format* fmt, int64_t mask_stride_b, int64_t mask_stride_h,
+                        const KernelChoice& c, void* o) {
   p.q = q;
   p.k = k;
   p.v = v;
@@ -492,6 +508,21 @@ stof_status mha_fwd_choice(const void* q, const void* k, const void* v, stof_dty
   p.variant = c.variant;
   p.exp_split = c.exp_split;
   p.softmax_wg = c.softmax_wg;
+}
+
+stof_status mha_fwd_choice(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int L, int Lk,
+                           int d,
+                           float scale, const stof_format* fmt, int64_t mask_stride_b, int64_t mask_stride_h,
+                           const KernelChoice& c, void* o, void* stream) {
+  const stof_status st = check_call(q, k, v, dt, B, H, L, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
+  if (st != STOF_OK) return st;
+  if (c.kernel != STOF_KERNEL_ROWWISE && c.kernel != STOF_KERNEL_BLOCKWISE) return STOF_ERR_INVALID_ARG;
+  if (c.kernel == STOF_KERNEL_BLOCKWISE && (!blockwise_tiles(*fmt) || (d != 64 && d != 128)))
+    return STOF_ERR_UNSUPPORTED;
+  if (c.kernel == STOF_KERNEL_ROWWISE && d == 256 && c.rows_per_warp == 4)
+    return STOF_ERR_UNSUPPORTED;  // a d = 256 key needs 16 lanes: 2 rows per warp at most
+  AttnParams p;
+  fill_params(p, q, k, v, B, H, L, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, c, o);
   const bool bf16 = dt == STOF_BF16;
   cudaStream_t s = as_stream(stream);
   if (c.kernel == STOF_KERNEL_ROWWISE)
@@ -545,6 +576,40 @@ stof_status stof_mha_fwd(const void* q, const void* k, const void* v, stof_dtype
                          int64_t mask_stride_b, int64_t mask_stride_h, stof_kernel which, void* o,
                          void* stream) {
   return stof_mha_fwd_cross(q, k, v, dt, B, H, L, L, d, scale, fmt, mask_stride_b, mask_stride_h, which, o, stream);
+}
+
+stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Hkv, int Lq,
+                               int Lk, int d, float scale, const stof_score* score, const stof_format* fmt,
+                               int64_t mask_stride_b, int64_t mask_stride_h, stof_kernel which, void* o, void* stream) {
+  stof_status st = check_call(q, k, v, dt, B, H, Lq, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
+  if (st != STOF_OK) return st;
+  if (Hkv < 1) return STOF_ERR_INVALID_ARG;
+  if (H % Hkv) return STOF_ERR_SHAPE;
+  if (score && (st = check_score(*score, scale)) != STOF_OK) return st;
+  KernelChoice c;
+  int source = 0;
+  if (which == STOF_KERNEL_AUTO && !fmt->synced) {
+    // the tile counts are not on the host: the block-wise kernel, whose time
+    // follows the listed tiles, wherever it takes the sizes
+    const bool blk = blockwise_tiles(*fmt) && (d == 64 || d == 128);
+    c = KernelChoice{blk ? STOF_KERNEL_BLOCKWISE : STOF_KERNEL_ROWWISE, fmt->bn, 0, kVariantAuto, 0, 0, 0};
+  } else {
+    st = plan_call(*fmt, B, H, Lq, Lk, d, which, &c, &source);
+    if (st != STOF_OK) return st;
+  }
+  const bool scored = score && (score->softcap > 0.f || score->slopes);
+  if (!scored && H == Hkv)  // plain scores, a K/V head each
+    return mha_fwd_choice(q, k, v, dt, B, H, Lq, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, c, o, stream);
+  ScoredParams p;
+  c.rows_per_warp = 0;  // a tuned setting was measured on plain scores
+  fill_params(p, q, k, v, B, H, Lq, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, c, o);
+  p.group = H / Hkv;
+  p.scale = scale;
+  p.softcap = score ? score->softcap : 0.f;
+  p.slopes = score ? score->slopes : nullptr;
+  p.q_start = score ? score->q_start : 0;
+  cudaStream_t s = as_stream(stream);
+  return record_cuda(launch_rowwise_scored(p, dt == STOF_BF16, s)) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -53,7 +53,8 @@ EXPORTED = ["stof_encode_workspace_bytes", "stof_encode_mask", "stof_format_sync
             "stof_tune_clear", "stof_tune_density_bucket", "stof_encode_mask_bits", "stof_oproj_fwd",
             "stof_encode_rules", "stof_check_bounded_wait", "stof_mha_plan", "stof_mha_fwd_plan",
             "stof_select_kernel_heads", "stof_oproj_ln_fwd", "stof_oproj_ln_workspace_bytes", "stof_ex2_fma",
-            "stof_mha_fwd_cross", "stof_rope_plan_init", "stof_rope_plan_custom", "stof_rope_fwd", "stof_rope_bwd"]
+            "stof_mha_fwd_cross", "stof_rope_plan_init", "stof_rope_plan_custom", "stof_rope_fwd", "stof_rope_bwd",
+            "stof_encode_documents", "stof_mha_fwd_score"]
 
 STOF_MAX_RULES = 64
 INT32_MIN, INT32_MAX = -(1 << 31), (1 << 31) - 1
@@ -114,6 +115,10 @@ class stof_plan(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("stages", ctypes.c_int), ("persistent", ctypes.c_int),
                 ("source", ctypes.c_int), ("rows_per_warp", ctypes.c_int), ("exp_split", ctypes.c_int),
                 ("softmax_warpgroups", ctypes.c_int)]
+
+
+class stof_score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("q_start", ctypes.c_int32)]
 
 
 class stof_rope_plan(ctypes.Structure):
@@ -181,6 +186,11 @@ def load_library(path: str = LIB_PATH):
         lib.stof_oproj_ln_fwd.restype = i32
         lib.stof_oproj_ln_workspace_bytes.argtypes = [i32, i32, i32]
         lib.stof_oproj_ln_workspace_bytes.restype = sz
+        lib.stof_encode_documents.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, P, sz, ctypes.POINTER(stof_format), P]
+        lib.stof_encode_documents.restype = i32
+        lib.stof_mha_fwd_score.argtypes = [P, P, P, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float,
+                                           ctypes.POINTER(stof_score), ctypes.POINTER(stof_format), i64, i64, i32, P, P]
+        lib.stof_mha_fwd_score.restype = i32
         lib.stof_rope_plan_init.argtypes = [ctypes.POINTER(stof_rope_plan), i32, i32, ctypes.c_double, i32,
                                             ctypes.c_double, i64, ctypes.c_double, ctypes.c_double, ctypes.c_double]
         lib.stof_rope_plan_init.restype = i32
@@ -314,6 +324,24 @@ def stof_encode_rules(rules: list, lq: int, lk: int, bm: int, bn: int, workspace
     return fmt
 
 
+def stof_encode_documents(q_doc: torch.Tensor, k_doc: torch.Tensor, q_order: torch.Tensor | None,
+                          k_order: torch.Tensor | None, bm: int, bn: int, workspace: torch.Tensor,
+                          fmt: stof_format | None = None, stream=None) -> stof_format:
+    """q_doc, q_order: int32 [n_masks, lq]; k_doc, k_order: int32 [n_masks, lk] (orders both None: no order).
+    Query i sees key j iff q_doc[i] == k_doc[j] >= 0 and k_order[j] <= q_order[i]."""
+    where = "stof_encode_documents"
+    device = _device_of(where, dict(q_doc=q_doc, k_doc=k_doc, q_order=q_order, k_order=k_order, workspace=workspace))
+    if q_doc.dim() != 2 or k_doc.dim() != 2 or q_doc.shape[0] != k_doc.shape[0]:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q_doc must be [n_masks, lq] and k_doc [n_masks, lk]")
+    (n, lq), (_, lk) = q_doc.shape, k_doc.shape
+    fmt = fmt if fmt is not None else stof_format()
+    args = (_int32(where, "q_doc", q_doc, (n, lq)), _int32(where, "k_doc", k_doc, (n, lk)),
+            _int32(where, "q_order", q_order, (n, lq)), _int32(where, "k_order", k_order, (n, lk)), n, lq, lk, bm, bn,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), ctypes.byref(fmt))
+    _launch(device, stream, where, lambda s: load_library().stof_encode_documents(*args, s))
+    return fmt
+
+
 def stof_check_bounded_wait(device_error: torch.Tensor, seconds: float, stream=None) -> None:
     """device_error: device int64 tensor of one element; the call ORs
     STOF_DEVERR_PIPE_TIMEOUT into it after `seconds` of a wait that never ends."""
@@ -375,6 +403,41 @@ def stof_mha_fwd_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, fmt: s
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Lq, Lk, d, float(scale),
         ctypes.byref(fmt), int(mask_stride_b), int(mask_stride_h), int(which), o.data_ptr(),
         _stream(stream)), "stof_mha_fwd_cross")
+    return o
+
+
+class Score:
+    """What becomes of the scores before the softmax: capped at `softcap` by a tanh (0: not), then lowered by
+    slopes[h] * |i + q_start - j| (slopes: fp32 [H] on the device, or None; q_start: position of query row 0)."""
+
+    def __init__(self, softcap: float = 0.0, slopes: torch.Tensor | None = None, q_start: int = 0):
+        self.softcap, self.slopes, self.q_start = float(softcap), slopes, int(q_start)
+
+    def as_c(self, where: str, heads: int) -> stof_score:
+        s = self.slopes
+        if s is not None and (s.dtype != torch.float32 or s.shape != (heads,) or not s.is_contiguous()):
+            raise StofError(STOF_ERR_SHAPE, f"{where}: slopes must be contiguous fp32 [H]")
+        return stof_score(self.softcap, None if s is None else s.data_ptr(), self.q_start)
+
+
+def stof_mha_fwd_score(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, fmt: stof_format, scale: float,
+                       score: Score | None, mask_stride_b: int, mask_stride_h: int, which: int, o: torch.Tensor,
+                       stream=None) -> torch.Tensor:
+    """q, o: device [B, H, Lq, d]; k, v: device [B, Hkv, Lk, d], H a multiple of Hkv; fp16/bf16, contiguous.
+    STOF_KERNEL_AUTO needs no synced format here."""
+    where = "stof_mha_fwd_score"
+    device = _device_of(where, dict(q=q, k=k, v=v, o=o, slopes=score.slopes if score is not None else None))
+    if q.dim() != 4 or k.dim() != 4:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q, k must be [B, heads, L, d]")
+    B, H, Lq, d = q.shape
+    Hkv, Lk = k.shape[1], k.shape[2]
+    if (o.shape != q.shape or k.shape != (B, Hkv, Lk, d) or v.shape != k.shape
+            or any(t.dtype != q.dtype or not t.is_contiguous() for t in (q, k, v, o))):
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, Lq, d] and k, v [B, Hkv, Lk, d], contiguous")
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Hkv, Lq, Lk, d, float(scale),
+            None if score is None else ctypes.byref(score.as_c(where, H)), ctypes.byref(fmt), int(mask_stride_b),
+            int(mask_stride_h), int(which), o.data_ptr())
+    _launch(device, stream, where, lambda s: load_library().stof_mha_fwd_score(*args, s))
     return o
 
 
