@@ -366,6 +366,49 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
                                int Lk, int d, float scale, const stof_score* score, const stof_format* fmt,
                                int64_t mask_stride_b, int64_t mask_stride_h, stof_kernel which, void* o, void* stream);
 
+/*
+ * Attention of drafted tokens over a K/V cache, for the steps of a decoder
+ * that check a tree of T drafted tokens per request at once, or decode one
+ * token (T = 1):
+ *   O[b,h,t,:] = sum_{j visible} softmax_j(score(scale * Q[b,h,t,:].K[b,g,j,:])) V[b,g,j,:],  g = h / (H / Hkv),
+ * where row j of request b's cache is a committed token for j < lens[b] and
+ * drafted token u = j - lens[b] for the counts[b] rows after them (the
+ * drafted tokens' own K and V, for instance by stof_rope_fwd() with rows =
+ * lens); drafted token t sees every committed row and the drafted rows u
+ * whose bit is set in its tree row.
+ *   q, o       device [B][H][T][d], dt; o is written.
+ *   k, v       device [B][Hkv][cap][d], dt; H a multiple of Hkv.  Rows from
+ *              lens[b] + counts[b] on are not used, whatever they hold.
+ *   lens       device int32 [B]; counts device int32 [B] or NULL (all T).
+ *              Needs lens[b] >= 0, 0 <= counts[b] <= T and lens[b] +
+ *              counts[b] <= cap; a request that breaks this is skipped and
+ *              sets STOF_DEVERR_BAD_LENGTH.  Rows t >= counts[b] of o are
+ *              left as they are.
+ *   tree       device bitset [B][T][ceil(T / 32)] of uint32 words (bit u of
+ *              row t: u % 32 of word u / 32), or NULL: token t sees u <= t.
+ *              A token that is to see itself has its own bit set; bits from
+ *              counts[b] on are ignored.
+ *   positions  device int32 [B][T] or NULL (lens[b] + t): the drafted
+ *              tokens' positions, read only with slopes; row j < lens[b] has
+ *              position j.  (score->q_start is not read.)
+ *   workspace  device, >= stof_tree_attn_workspace_bytes(...) bytes, 16-byte
+ *              aligned; scratch of one call: calls that share it must not
+ *              overlap on the GPU.  Nothing is kept in it from call to call.
+ *   device_error  device int64 or NULL; the call ORs its error bits into it.
+ * d is 64 or 128 (else STOF_ERR_UNSUPPORTED), T in [1, 1024], pointers of q,
+ * k, v and o 16-byte aligned.  A row that sees nothing gives 0.  Scores and
+ * precision as stof_mha_fwd_score().  Asynchronous on stream; the lengths are
+ * read on the device only, so a captured call follows them.
+ */
+#define STOF_TREE_MAX_TOKENS 1024
+stof_status stof_tree_attn_fwd(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Hkv, int T,
+                               int d, int cap, const int32_t* lens, const int32_t* counts, const uint32_t* tree,
+                               const int32_t* positions, float scale, const stof_score* score, void* o,
+                               void* workspace, size_t ws_bytes, int64_t* device_error, void* stream);
+
+/* Workspace bytes of stof_tree_attn_fwd(); 0 for invalid sizes. */
+size_t stof_tree_attn_workspace_bytes(int B, int H, int Hkv, int T, int d);
+
 /* Where a plan's choice came from. */
 #define STOF_PLAN_FORCED 0    /* the caller named the kernel */
 #define STOF_PLAN_ANALYTIC 1  /* stof_select_kernel() on the format's density [SEL] */

@@ -136,6 +136,8 @@ struct ScoredParams : AttnParams {
   const float* slopes;     // [H] or null: scores are lowered by slopes[h] * |i + q_start - j|
   int q_start;
 };
+// STOF_OK, or what is wrong with a call's score options at this scale.
+stof_status check_score(const stof_score& s, float scale);
 // Block-wise kernel variants: one CTA per query tile, or persistent CTAs
 // (d = 64 only); auto picks by the mean listed OTs per OT row.
 constexpr int kVariantAuto = 0, kVariantPerTile = 1, kVariantPersistent = 2;

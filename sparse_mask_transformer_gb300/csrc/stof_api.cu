@@ -51,6 +51,17 @@ bool once_per_device(const void* key, bool (*prepare)(const void*), const void* 
   return true;
 }
 
+// Score options of a call with this scale.
+stof_status check_score(const stof_score& s, float scale) {
+  if (!std::isfinite(s.softcap) || s.softcap < 0.f) return STOF_ERR_INVALID_ARG;
+  // 2 log2(e) scale / softcap is a factor of the capped scores
+  if (s.softcap > 0.f && (!std::isfinite(3.f * (scale / s.softcap)) || !std::isfinite(3.f * s.softcap)))
+    return STOF_ERR_INVALID_ARG;
+  if (s.q_start < -(1 << 30) || s.q_start > (1 << 30)) return STOF_ERR_SHAPE;
+  if (!aligned(s.slopes, 4)) return STOF_ERR_ALIGNMENT;
+  return STOF_OK;
+}
+
 }  // namespace stof
 
 extern "C" {
@@ -393,17 +404,6 @@ static stof_status check_call(const void* q, const void* k, const void* v, stof_
   if (max_mask >= fmt->n_masks) return STOF_ERR_SHAPE;
   if (static_cast<long double>(B) * H * (L > Lk ? L : Lk) >= 2147483647.0L * 8) return STOF_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16)) return STOF_ERR_ALIGNMENT;
-  return STOF_OK;
-}
-
-// Score options of a call with this scale.
-static stof_status check_score(const stof_score& s, float scale) {
-  if (!std::isfinite(s.softcap) || s.softcap < 0.f) return STOF_ERR_INVALID_ARG;
-  // 2 log2(e) scale / softcap is a factor of the capped scores
-  if (s.softcap > 0.f && (!std::isfinite(3.f * (scale / s.softcap)) || !std::isfinite(3.f * s.softcap)))
-    return STOF_ERR_INVALID_ARG;
-  if (s.q_start < -(1 << 30) || s.q_start > (1 << 30)) return STOF_ERR_SHAPE;
-  if (!aligned(s.slopes, 4)) return STOF_ERR_ALIGNMENT;
   return STOF_OK;
 }
 

@@ -54,7 +54,7 @@ EXPORTED = ["stof_encode_workspace_bytes", "stof_encode_mask", "stof_format_sync
             "stof_encode_rules", "stof_check_bounded_wait", "stof_mha_plan", "stof_mha_fwd_plan",
             "stof_select_kernel_heads", "stof_oproj_ln_fwd", "stof_oproj_ln_workspace_bytes", "stof_ex2_fma",
             "stof_mha_fwd_cross", "stof_rope_plan_init", "stof_rope_plan_custom", "stof_rope_fwd", "stof_rope_bwd",
-            "stof_encode_documents", "stof_mha_fwd_score"]
+            "stof_encode_documents", "stof_mha_fwd_score", "stof_tree_attn_fwd", "stof_tree_attn_workspace_bytes"]
 
 STOF_MAX_RULES = 64
 INT32_MIN, INT32_MAX = -(1 << 31), (1 << 31) - 1
@@ -191,6 +191,11 @@ def load_library(path: str = LIB_PATH):
         lib.stof_mha_fwd_score.argtypes = [P, P, P, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float,
                                            ctypes.POINTER(stof_score), ctypes.POINTER(stof_format), i64, i64, i32, P, P]
         lib.stof_mha_fwd_score.restype = i32
+        lib.stof_tree_attn_fwd.argtypes = [P, P, P, i32, i32, i32, i32, i32, i32, i32, P, P, P, P, ctypes.c_float,
+                                           ctypes.POINTER(stof_score), P, P, sz, P, P]
+        lib.stof_tree_attn_fwd.restype = i32
+        lib.stof_tree_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        lib.stof_tree_attn_workspace_bytes.restype = sz
         lib.stof_rope_plan_init.argtypes = [ctypes.POINTER(stof_rope_plan), i32, i32, ctypes.c_double, i32,
                                             ctypes.c_double, i64, ctypes.c_double, ctypes.c_double, ctypes.c_double]
         lib.stof_rope_plan_init.restype = i32
@@ -438,6 +443,36 @@ def stof_mha_fwd_score(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, fmt: s
             None if score is None else ctypes.byref(score.as_c(where, H)), ctypes.byref(fmt), int(mask_stride_b),
             int(mask_stride_h), int(which), o.data_ptr())
     _launch(device, stream, where, lambda s: load_library().stof_mha_fwd_score(*args, s))
+    return o
+
+
+def stof_tree_attn_workspace_bytes(B: int, H: int, Hkv: int, T: int, d: int) -> int:
+    return int(load_library().stof_tree_attn_workspace_bytes(int(B), int(H), int(Hkv), int(T), int(d)))
+
+
+def stof_tree_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor, scale: float,
+                       o: torch.Tensor, workspace: torch.Tensor, tree: torch.Tensor | None = None,
+                       counts: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                       score: Score | None = None, device_error: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q, o: device [B, H, T, d]; k, v: the caches [B, Hkv, cap, d]; lens, counts: int32 [B]; tree: int32
+    [B, T, ceil(T / 32)] ancestor bits (None: token t sees drafted tokens 0..t); positions: int32 [B, T]."""
+    where = "stof_tree_attn_fwd"
+    slopes = score.slopes if score is not None else None
+    device = _device_of(where, dict(q=q, k=k, v=v, o=o, lens=lens, workspace=workspace, tree=tree, counts=counts,
+                                    positions=positions, slopes=slopes, device_error=device_error))
+    if q.dim() != 4 or k.dim() != 4:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q, k must be [B, heads, rows, d]")
+    B, H, T, d = q.shape
+    Hkv, cap = k.shape[1], k.shape[2]
+    if (o.shape != q.shape or k.shape != (B, Hkv, cap, d) or v.shape != k.shape
+            or any(t.dtype != q.dtype or not t.is_contiguous() for t in (q, k, v, o))):
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, T, d] and k, v [B, Hkv, cap, d], contiguous")
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Hkv, T, d, cap,
+            _int32(where, "lens", lens, (B,)), _int32(where, "counts", counts, (B,)),
+            _int32(where, "tree", tree, (B, T, (T + 31) // 32)), _int32(where, "positions", positions, (B, T)),
+            float(scale), None if score is None else ctypes.byref(score.as_c(where, H)), o.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _error_word(where, device_error))
+    _launch(device, stream, where, lambda s: load_library().stof_tree_attn_fwd(*args, s))
     return o
 
 
