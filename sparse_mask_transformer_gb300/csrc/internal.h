@@ -196,6 +196,7 @@ stof_status mha_fwd_choice(const void* q, const void* k, const void* v, stof_dty
                            const KernelChoice& c, void* o, void* stream);
 cudaError_t launch_rowwise(const AttnParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_rowwise_scored(const ScoredParams& p, bool bf16, cudaStream_t s);
+stof_status launch_blockwise_scored(const ScoredParams& p, bool bf16, cudaStream_t s);
 // Density bucket of the tuning cache.
 int tune_density_bucket(double density);
 // Returns STOF_OK or an error status (tensor-map encoding / launch).

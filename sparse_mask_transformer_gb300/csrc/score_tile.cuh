@@ -1,0 +1,191 @@
+// Capped and distance-lowered scores of a block-wise tile, on the 128 scores
+// of one query row that a softmax thread holds in registers (see score.cuh
+// for the formulas).
+//
+// The cap.  A tile whose products all stay within half the cap (scaled), as
+// they do in trained models (caps of 30 to 50, scores of a few units), takes
+//   log2 e cap tanh(scale s / cap) = s (k1 + t (k3 + t (k5 + t k7))),  t = s^2,
+// the odd polynomial of csrc/tanh_poly.py (within 1.3e-7 of the tanh), on the
+// FMA pipe in packed pairs: four instructions a pair, the last product folded
+// into the subtraction of the running max.  Any other tile takes the exact
+// formula with an exponential and a reciprocal of the special-function unit
+// for every score, which beside the softmax's own exponential would be the
+// kernel's bound for every tile.
+// The distance.  Row at position pos, keys of the tile at j0 + i: while no
+// key is past the row, -slope |pos - j| is linear in i and takes a packed
+// addition a pair; else one subtraction and one multiply-add per score.
+#pragma once
+#include "blockwise_common.cuh"
+#include "score.cuh"
+
+namespace stof {
+namespace bw {
+
+constexpr float kTanhLimit = 0.5f;  // |scale s / cap| the polynomial is made for
+constexpr float kTanh1 = 0x1.ffffb2p-1f, kTanh3 = -0x1.55341ap-2f, kTanh5 = 0x1.0d366cp-3f, kTanh7 = -0x1.634eb0p-5f;
+
+// The call's score constants, in log2 units.
+struct ScoreConst {
+  float c;               // scale log2 e (no cap)
+  float k1, k3, k5, k7;  // the polynomial in s
+  float lim;             // |s| up to which it holds; negative: never
+  float a, two_a, b;     // the exact form: a + two_a u, u = -1 / (1 + 2^(b s))
+  int cap;
+};
+
+inline ScoreConst make_score_const(float scale, float softcap) {
+  ScoreConst r{};
+  const double log2e = 1.4426950408889634;
+  r.c = static_cast<float>(scale * log2e);
+  r.cap = softcap > 0.f;
+  r.lim = -1.f;
+  if (r.cap) {
+    const double x = static_cast<double>(scale) / softcap, a = softcap * log2e;  // y = x s
+    r.a = static_cast<float>(a);
+    r.two_a = static_cast<float>(2.0 * a);
+    r.b = static_cast<float>(2.0 * log2e * x);
+    const double m = x < 0 ? -x : x;
+    if (m > 1e-4 && m < 1e4 && a < 1e5) {  // the powers of x stay well inside fp32
+      r.k1 = static_cast<float>(a * kTanh1 * x);
+      r.k3 = static_cast<float>(a * kTanh3 * x * x * x);
+      r.k5 = static_cast<float>(a * kTanh5 * x * x * x * x * x);
+      r.k7 = static_cast<float>(a * kTanh7 * x * x * x * x * x * x * x);
+      r.lim = static_cast<float>(kTanhLimit / m);
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.ftz.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// The polynomial's bracket for two products: P(s^2), to be multiplied by s.
+__device__ __forceinline__ void cap_bracket(const ScoreConst& k, float s0, float s1, float& p0, float& p1) {
+  float t0, t1;
+  fmul2(t0, t1, s0, s1, s0, s1);
+  ffma2(p0, p1, t0, t1, k.k7, k.k7, k.k5, k.k5);
+  ffma2(p0, p1, p0, p1, t0, t1, k.k3, k.k3);
+  ffma2(p0, p1, p0, p1, t0, t1, k.k1, k.k1);
+}
+__device__ __forceinline__ float cap_poly(const ScoreConst& k, float s) {
+  const float t = s * s;
+  return s * fmaf(fmaf(fmaf(k.k7, t, k.k5), t, k.k3), t, k.k1);
+}
+__device__ __forceinline__ float cap_exact(const ScoreConst& k, float s) {
+  return fmaf(k.two_a, score_rcp(-1.f - score_ex2(k.b * s)), k.a);
+}
+
+// Whether every product of the row is within the polynomial's range.  (A NaN
+// does not count: it stays NaN either way, until a mask drops it.)
+template <int CHUNKS>
+__device__ __forceinline__ bool row_within(const uint32_t (&sr)[CHUNKS][32], float lim) {
+  float m[CHUNKS];
+#pragma unroll
+  for (int cc = 0; cc < CHUNKS; ++cc) {
+    m[cc] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      m[cc] = max3(m[cc], fabsf(__uint_as_float(sr[cc][i])), fabsf(__uint_as_float(sr[cc][i + 1])));
+  }
+  float x = m[0];
+#pragma unroll
+  for (int cc = 1; cc < CHUNKS; ++cc) x = fmaxf(x, m[cc]);
+  return x <= lim;
+}
+
+// Capped scores (log2 units) in place.
+template <int CHUNKS>
+__device__ __forceinline__ void cap_scores(uint32_t (&sr)[CHUNKS][32], const ScoreConst& k, bool within) {
+  if (within) {
+#pragma unroll
+    for (int cc = 0; cc < CHUNKS; ++cc)
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float s0 = __uint_as_float(sr[cc][i]), s1 = __uint_as_float(sr[cc][i + 1]);
+        float p0, p1;
+        cap_bracket(k, s0, s1, p0, p1);
+        fmul2(p0, p1, p0, p1, s0, s1);
+        sr[cc][i] = __float_as_uint(p0);
+        sr[cc][i + 1] = __float_as_uint(p1);
+      }
+  } else {
+#pragma unroll
+    for (int cc = 0; cc < CHUNKS; ++cc)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sr[cc][i] = __float_as_uint(cap_exact(k, __uint_as_float(sr[cc][i])));
+  }
+}
+
+// sr <- c sr - slope |pos - (j0 + i)|, rel = pos - j0.  `before`: no key is
+// past the row (rel >= 32 CHUNKS - 1 in every row of the warp).
+template <int CHUNKS>
+__device__ __forceinline__ void lower_by_distance(uint32_t (&sr)[CHUNKS][32], float c, float slope, float rel, bool before) {
+  if (before) {
+    const float base = -slope * rel;  // -slope (rel - i) = base + slope i
+#pragma unroll
+    for (int cc = 0; cc < CHUNKS; ++cc)
+#pragma unroll
+      for (int i0 = 0; i0 < 32; i0 += 8) {
+        float b0 = fmaf(slope, static_cast<float>(cc * 32 + i0), base), b1 = b0 + slope;
+        const float two = 2.f * slope;
+#pragma unroll
+        for (int i = i0; i < i0 + 8; i += 2) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(sr[cc][i]), __uint_as_float(sr[cc][i + 1]), c, c, b0, b1);
+          sr[cc][i] = __float_as_uint(x0);
+          sr[cc][i + 1] = __float_as_uint(x1);
+          fadd2(b0, b1, two, two);
+        }
+      }
+  } else {
+#pragma unroll
+    for (int cc = 0; cc < CHUNKS; ++cc)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float d = fabsf(rel - static_cast<float>(cc * 32 + i));
+        sr[cc][i] = __float_as_uint(fmaf(__uint_as_float(sr[cc][i]), c, -slope * d));
+      }
+  }
+}
+
+// The same with the keys' own positions: lane x holds at[i] = position of key
+// 32 i + x, minus j0.  A warp-wide call.
+template <int CHUNKS>
+__device__ __forceinline__ void lower_by_positions(uint32_t (&sr)[CHUNKS][32], float c, float slope, float rel,
+                                                   const float (&at)[CHUNKS]) {
+#pragma unroll
+  for (int cc = 0; cc < CHUNKS; ++cc)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float d = fabsf(rel - __shfl_sync(0xffffffffu, at[cc], i));
+      sr[cc][i] = __float_as_uint(fmaf(__uint_as_float(sr[cc][i]), c, -slope * d));
+    }
+}
+
+// exp_pack of capped scores straight from the products: P = 2^(s P(s^2) + nmu).
+template <int CHUNKS, bool BF16>
+__device__ __forceinline__ float exp_pack_capped(const uint32_t (&sr)[CHUNKS][32], const ScoreConst& k, float nmu,
+                                                 uint32_t (&pk)[CHUNKS][16]) {
+  float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int cc = 0; cc < CHUNKS; ++cc)
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float s0 = __uint_as_float(sr[cc][i]), s1 = __uint_as_float(sr[cc][i + 1]);
+      float x0, x1;
+      cap_bracket(k, s0, s1, x0, x1);
+      ffma2(x0, x1, x0, x1, s0, s1, nmu, nmu);
+      const float e0 = ex2(x0), e1 = ex2(x1);
+      fadd2(ls[((i >> 1) & 1) * 2], ls[((i >> 1) & 1) * 2 + 1], e0, e1);
+      pk[cc][i / 2] = pack2<BF16>(e0, e1);
+    }
+  return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+}
+
+}  // namespace bw
+}  // namespace stof

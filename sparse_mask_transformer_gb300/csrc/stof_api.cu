@@ -609,6 +609,7 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
   p.slopes = score ? score->slopes : nullptr;
   p.q_start = score ? score->q_start : 0;
   cudaStream_t s = as_stream(stream);
+  if (c.kernel == STOF_KERNEL_BLOCKWISE && fmt->bn == 128) return launch_blockwise_scored(p, dt == STOF_BF16, s);
   return record_cuda(launch_rowwise_scored(p, dt == STOF_BF16, s)) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
 
