@@ -6,14 +6,14 @@
 // row has to be read once (4 d bytes), and 128 rows cost the tensor cores
 // half of the time that 128 keys take to arrive.  So the work is cut by keys:
 // all (request, K/V head, row tile) items in order, each a run of 128-key
-// tiles, are one long sequence of tiles, of which each of kTreeCtas CTAs
-// takes an equal share (the lengths are read on the device, so the shares
-// follow them).  A CTA streams its share through scored_kernel.cuh, a
-// segment per item it touches; an item that lies in one share is finished
-// there, the others leave partial rows (O relative to the rows' max, max and
-// sum) in the workspace, which combine_kernel merges in the order of the
-// keys: the result does not depend on timing.  A CTA has at most one item
-// that began before its share and one that goes on after it: two slots.
+// tiles and kItemCost more for its start and end, are one long line, of which
+// each of kWorkers workers (two per SM, scored_kernel.cuh) takes an equal
+// share (the lengths are read on the device, so the shares follow them).  An
+// item whose tiles lie in one share is finished there; the others leave
+// partial rows (O relative to the rows' max, max and sum) in the workspace,
+// which combine_kernel merges in the order of the keys: the result does not
+// depend on timing.  A worker has at most one item that began before its
+// share and one that goes on after it: two slots.
 #include <cmath>
 
 #include "scored_kernel.cuh"
@@ -23,7 +23,9 @@ namespace {
 
 using namespace scored;
 
-constexpr int kTreeCtas = 152;  // one CTA per SM
+constexpr int kTreeCtas = 152;             // one CTA per SM
+constexpr int kWorkers = 2 * kTreeCtas;
+constexpr int kItemCost = 2;               // an item's start and end, in tiles
 
 struct TreeParams : CommonParams {
   int B, Hkv, T, d, cap, words;
@@ -34,8 +36,9 @@ struct TreeParams : CommonParams {
   const int32_t* counts;
   const uint32_t* tree;
   const int32_t* positions;
-  float* slots;    // [2 kTreeCtas][slot_rows][d] partial O
-  float2* stats;   // [2 kTreeCtas][slot_rows] (max, sum)
+  float* slots;    // [2 kWorkers][slot_rows][d] partial O
+  float2* stats;   // [2 kWorkers][slot_rows] (max, sum)
+  int32_t* line;   // [B + 1] place of each request on the line, its length
 };
 
 // Committed and drafted tokens of request b; false for a request that breaks
@@ -45,9 +48,10 @@ __device__ __forceinline__ bool request(const TreeParams& p, int b, int& ctx, in
   count = p.counts ? __ldg(p.counts + b) : p.T;
   return ctx >= 0 && count >= 1 && count <= p.T && ctx <= p.cap - count;
 }
-__device__ __forceinline__ int tiles_of(const TreeParams& p, int b) {
+// Length of a request's items on the line (0: none).
+__device__ __forceinline__ int item_length(const TreeParams& p, int b) {
   int ctx, count;
-  return request(p, b, ctx, count) ? (ctx + count + 127) >> 7 : 0;
+  return request(p, b, ctx, count) ? ((ctx + count + 127) >> 7) + kItemCost : 0;
 }
 
 // Exclusive prefix of v over the block's threads and the total (all threads
@@ -72,234 +76,276 @@ __device__ __forceinline__ int block_prefix(int v, int* sums, int& total) {
   return before + x - v;
 }
 
-// All tiles of the call.
-__device__ __forceinline__ int total_tiles(const TreeParams& p, int* sums) {
-  int all = 0;
-  for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    int total;
-    block_prefix(b < p.B ? tiles_of(p, b) * p.Hkv * p.row_tiles : 0, sums, total);
-    all += total;
-  }
-  return all;
-}
-
-// Tiles per CTA.
-__device__ __forceinline__ int share_of(int all) { return max(1, (all + kTreeCtas - 1) / kTreeCtas); }
+// A worker's share of a line of this length.
+__device__ __forceinline__ int share_of(int all) { return max(1, (all + kWorkers - 1) / kWorkers); }
 
 struct CacheSource {
   using Params = TreeParams;
   static constexpr bool kClearsV = true;
+  struct Item {
+    int b, hk, rt;     // request, K/V head, row tile
+    int ctx, count;    // committed and drafted tokens
+    int t0;            // first tile of the segment
+    bool whole;        // the segment is the whole item
+  };
+  struct Shared {
+    int sums[kThreads / 32];
+    int begin[2], end[2];  // the workers' shares
+    int b[2], base[2];     // request that holds a share's begin, its place on the line
+  };
   struct Row {
     int head, t, pos;
     size_t out;
     const uint32_t* tree;  // the row's bits, or null
   };
-  struct Tile {
-    bool partial;   // not every key is visible to every row
-    bool drafted;   // it has drafted keys
-    int j0;
-    int end;        // keys of the tile that the request has
-  };
 
-  const Params& p;
-  int w, w_end;            // next tile of the share, its end
-  int b, base, nt;         // request, the number of its first tile, tiles per item
-  int ctx, count;
-  int t0, hk, rt;          // the segment: first tile of the item, K/V head, row tile
-  bool whole_;
-
-  __device__ explicit CacheSource(const Params& params) : p(params) {
-    __shared__ int sums[kThreads / 32];
-    __shared__ int s_b, s_base;
-    const int all = total_tiles(p, sums), share = share_of(all);
-    w = min(static_cast<int>(blockIdx.x) * share, all);
-    w_end = min(w + share, all);
-    if (threadIdx.x == 0) s_b = p.B;
-    int base0 = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {  // the request that holds tile w
-      const int bb = b0 + threadIdx.x;
-      const int v = bb < p.B ? tiles_of(p, bb) * p.Hkv * p.row_tiles : 0;
-      if (blockIdx.x == 0 && p.err && bb < p.B && v == 0) {
+  static __device__ void init(Shared&) {}
+  // Finds the requests at the workers' begins; CTA 0 reports bad requests and
+  // leaves the line for combine_kernel.
+  static __device__ void prologue(const Params& p, Shared& s) {
+    const int per = p.Hkv * p.row_tiles;
+    int all = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      int total;
+      const int v = b < p.B ? item_length(p, b) * per : 0;
+      const int at = all + block_prefix(v, s.sums, total);
+      if (blockIdx.x == 0 && b < p.B) {
+        p.line[b] = at;
         int c, n;
-        if (!request(p, bb, c, n) && !(n == 0 && c >= 0 && c <= p.cap))
+        if (p.err && v == 0 && !request(p, b, c, n) && !(n == 0 && c >= 0 && c <= p.cap))
           raise_error(p.err, STOF_DEVERR_BAD_LENGTH);
       }
+      all += total;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.line[p.B] = all;
+    const int share = share_of(all);
+    const int w0 = min(static_cast<int>(blockIdx.x) * 2 * share, all), w1 = min(w0 + share, all);
+    if (threadIdx.x == 0) {
+      s.begin[0] = w0;
+      s.end[0] = s.begin[1] = w1;
+      s.end[1] = min(w1 + share, all);
+    }
+    int base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
       int total;
-      const int first = base0 + block_prefix(v, sums, total);
-      if (v > 0 && first <= w && w < first + v) {
-        s_b = bb;
-        s_base = first;
+      const int v = b < p.B ? item_length(p, b) * per : 0;
+      const int at = base + block_prefix(v, s.sums, total);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int w = g == 0 ? w0 : w1;
+        if (at <= w && w < at + v) {
+          s.b[g] = b;
+          s.base[g] = at;
+        }
       }
-      base0 += total;
+      base += total;
     }
-    __syncthreads();
-    b = s_b;
-    base = s_base;
-    if (w < w_end) load_request();
   }
-  __device__ void load_request() {
-    nt = request(p, b, ctx, count) ? (ctx + count + 127) >> 7 : 0;
-  }
-  __device__ bool next(Segment& seg) {
-    if (w >= w_end) return false;
-    while (w >= base + nt * p.Hkv * p.row_tiles) {  // on to the next request with tiles
-      base += nt * p.Hkv * p.row_tiles;
-      ++b;
-      load_request();
+  struct Lead {
+    __device__ Lead(const Params&, Shared&, const volatile int*) {}
+    __device__ void drain() {}
+  };
+
+  // A worker's segments, the same in every warp.
+  template <int WHO>
+  struct Feed {
+    const Params& p;
+    int w, end;             // place on the line, end of the share
+    int b, base, len;       // request, its place, length of its items
+    int ctx, count;
+    static constexpr bool ok = true;
+    __device__ Feed(const Params& params, Shared& s, int g, const volatile int*, Lead*) : p(params) {
+      w = s.begin[g];
+      end = s.end[g];
+      b = s.b[g];
+      base = s.base[g];
+      if (w < end) load();
     }
-    const int off = w - base, item = off / nt;
-    t0 = off - item * nt;
-    hk = item / p.row_tiles;
-    rt = item - hk * p.row_tiles;
-    seg.q_plane = seg.kv_plane = b * p.Hkv + hk;
-    seg.q_row = rt * 128;
-    seg.n = min(nt - t0, w_end - w);
-    whole_ = seg.n == nt;
-    w += seg.n;
-    return true;
-  }
-  __device__ int tile_key(int t) const { return (t0 + t) * 128; }
-  __device__ bool begin_row(Row& row, const Segment&, int r) const {
-    const int rr = rt * 128 + r;
-    const int gq = rr / p.T;
+    __device__ void load() { len = request(p, b, ctx, count) ? ((ctx + count + 127) >> 7) + kItemCost : 0; }
+    __device__ bool next(Segment<Item>& seg) {
+      const int per = p.Hkv * p.row_tiles;
+      while (w < end) {
+        while (w >= base + len * per) {  // on to the next request on the line
+          base += len * per;
+          ++b;
+          load();
+        }
+        const int off = w - base, item = off / len, at = off - item * len;
+        const int to = min(end, base + (item + 1) * len) - (base + item * len);  // the share's part: [at, to)
+        w += to - at;
+        const int t0 = max(0, at - kItemCost), t1 = max(0, to - kItemCost);
+        if (t1 <= t0) continue;  // the share ends before the item's first tile
+        const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
+        seg.q_plane = seg.kv_plane = b * p.Hkv + hk;
+        seg.q_row = rt * 128;
+        seg.n = t1 - t0;
+        seg.item = Item{b, hk, rt, ctx, count, t0, t1 - t0 == len - kItemCost};
+        return true;
+      }
+      return false;
+    }
+  };
+
+  static __device__ int tile_key(const Params&, const Item& x, int t) { return (x.t0 + t) * 128; }
+  static __device__ int tile_end(const Item& x, int t) { return min(128, x.ctx + x.count - (x.t0 + t) * 128); }
+  static __device__ bool begin_row(const Params& p, Row& row, const Item& x, int r) {
+    const int rr = x.rt * 128 + r, gq = rr / p.T;
     row.t = rr - gq * p.T;
-    row.head = hk * p.group + gq;
-    const bool live = rr < p.rows && row.t < count;
-    const size_t token = static_cast<size_t>(b) * p.T + row.t;
-    row.pos = live && p.positions ? __ldg(p.positions + token) : ctx + row.t;
-    row.out = (static_cast<size_t>(b) * p.H + row.head) * p.T + row.t;
+    row.head = x.hk * p.group + gq;
+    const bool live = rr < p.rows && row.t < x.count;
+    const size_t token = static_cast<size_t>(x.b) * p.T + row.t;
+    row.pos = live && p.positions ? __ldg(p.positions + token) : x.ctx + row.t;
+    row.out = (static_cast<size_t>(x.b) * p.H + row.head) * p.T + row.t;
     row.tree = live && p.tree ? p.tree + token * p.words : nullptr;
     return live;
   }
-  __device__ void prefetch(Row&, const Segment&, int) const {}
-  __device__ Tile tile(const Row&, const Segment&, int t) const {
-    Tile x;
-    x.j0 = (t0 + t) * 128;
-    x.end = min(128, ctx + count - x.j0);
-    x.drafted = x.j0 + 128 > ctx;
-    x.partial = x.drafted;
-    return x;
-  }
+  static __device__ void prefetch(const Params&, Row&, const Item&, int, int) {}
+  static __device__ bool partial(const Item& x, int t) { return (x.t0 + t + 1) * 128 > x.ctx; }  // it has drafted keys
   // Bits of drafted tokens 32 x .. 32 x + 31 that the row sees.
-  __device__ uint32_t seen(const Row& row, int x) const {
-    if (x < 0 || 32 * x >= count) return 0u;
-    uint32_t word;
+  static __device__ uint32_t seen(const Params& p, const Row& row, const Item& x, int word) {
+    if (32 * word >= x.count) return 0u;
+    uint32_t bits;
     if (p.tree)
-      word = row.tree ? __ldg(row.tree + x) : 0u;
+      bits = row.tree ? __ldg(row.tree + word) : 0u;
     else
-      word = row.t >= 32 * x + 31 ? ~0u : (row.t < 32 * x ? 0u : (2u << (row.t - 32 * x)) - 1u);
-    const int left = count - 32 * x;
-    return left >= 32 ? word : word & ((1u << left) - 1u);
+      bits = row.t >= 32 * word + 31 ? ~0u : (row.t < 32 * word ? 0u : (2u << (row.t - 32 * word)) - 1u);
+    const int left = x.count - 32 * word;
+    return left >= 32 ? bits : bits & ((1u << left) - 1u);
   }
-  __device__ void bits(const Row& row, const Segment&, int t, uint32_t (&out)[4]) const {
+  static __device__ void bits(const Params& p, const Row& row, const Item& x, int t, uint32_t (&out)[4]) {
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
-      const int u0 = (t0 + t) * 128 + 32 * cc - ctx;  // drafted token of the chunk's first key
-      if (u0 <= -32) {
+      const int u0 = (x.t0 + t) * 128 + 32 * cc - x.ctx;  // drafted token of the chunk's first key
+      if (u0 <= -32)
         out[cc] = ~0u;
-      } else if (u0 < 0) {
-        out[cc] = ((1u << -u0) - 1u) | (seen(row, 0) << -u0);
-      } else {
-        const int x = u0 >> 5, sh = u0 & 31;
-        out[cc] = __funnelshift_r(seen(row, x), seen(row, x + 1), sh);
-      }
+      else if (u0 < 0)
+        out[cc] = ((1u << -u0) - 1u) | (seen(p, row, x, 0) << -u0);
+      else
+        out[cc] = __funnelshift_r(seen(p, row, x, u0 >> 5), seen(p, row, x, (u0 >> 5) + 1), u0 & 31);
     }
   }
-  __device__ void lower(const Row& row, const Tile& t, uint32_t (&sr)[4][32], float c, float slope) const {
-    const long long rel = static_cast<long long>(row.pos) - t.j0;
-    if (t.drafted && p.positions) {
+  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, uint32_t (&sr)[4][32], float c,
+                               float slope) {
+    const int j0 = (x.t0 + t) * 128;
+    const long long rel = static_cast<long long>(row.pos) - j0;
+    if (p.positions && partial(x, t)) {
       float at[4];  // position of key 32 i + lane of the tile
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int key = 32 * i + static_cast<int>(threadIdx.x & 31), u = t.j0 + key - ctx;
-        long long x = key;
-        if (u >= 0) x = u < count ? static_cast<long long>(__ldg(p.positions + static_cast<size_t>(b) * p.T + u)) - t.j0 : 0;
-        at[i] = static_cast<float>(x);
+        const int key = 32 * i + static_cast<int>(threadIdx.x & 31), u = j0 + key - x.ctx;
+        long long pos = key;
+        if (u >= 0) pos = u < x.count ? static_cast<long long>(__ldg(p.positions + static_cast<size_t>(x.b) * p.T + u)) - j0 : 0;
+        at[i] = static_cast<float>(pos);
       }
       lower_by_positions(sr, c, slope, static_cast<float>(rel), at);
     } else {
       lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= 127));
     }
   }
-  __device__ bool whole(const Segment&) const { return whole_; }
-  __device__ size_t out_row(const Row& row) const { return row.out; }
-  // A segment that begins its item goes on in the next CTA's share: slot 2 c + 1; else slot 2 c.
-  __device__ size_t slot_row(int r) const {
-    return static_cast<size_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * p.slot_rows + r;
+  static __device__ bool whole(const Item& x) { return x.whole; }
+  static __device__ size_t out_row(const Params&, const Row& row, const Item&) { return row.out; }
+  // A segment that begins its item goes on in a later share: slot 2 w + 1 of
+  // worker w; one that does not: slot 2 w.
+  static __device__ size_t slot_row(const Params& p, const Item& x, int g, int r) {
+    return static_cast<size_t>(2 * (2 * blockIdx.x + g) + (x.t0 == 0 ? 1 : 0)) * p.slot_rows + r;
   }
-  __device__ float* partial_o(const Segment&, int r) const { return p.slots + slot_row(r) * p.d; }
-  __device__ void put_stats(const Segment&, int r, float m, float l) const { p.stats[slot_row(r)] = make_float2(m, l); }
+  static __device__ float* partial_o(const Params& p, const Item& x, int g, int r, int d) {
+    return p.slots + slot_row(p, x, g, r) * d;
+  }
+  static __device__ void put_stats(const Params& p, const Item& x, int g, int r, float m, float l) {
+    p.stats[slot_row(p, x, g, r)] = make_float2(m, l);
+  }
 };
 
-// Merges the partial rows of the items that lie in several CTAs' shares, a
-// warp per query row: O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
+// Merges the partial rows of the items that lie in several workers' shares:
+// O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, a block per query row,
+// warp x the parts x, x + 4, ..., eight of them in flight.
+constexpr int kMergeWarps = 4;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) combine_kernel(const __grid_constant__ TreeParams p) {
   constexpr int E = D / 32;
-  __shared__ int sums[8];
-  __shared__ int s_base;
+  __shared__ float s_o[kMergeWarps][D], s_m[kMergeWarps], s_l[kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = p.Hkv * p.row_tiles;
   const int b = static_cast<int>(blockIdx.x) / per, item = static_cast<int>(blockIdx.x) - b * per;
-  int all = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 256) {
-    const int bb = b0 + threadIdx.x;
-    int total;
-    const int first = all + block_prefix(bb < p.B ? tiles_of(p, bb) * per : 0, sums, total);
-    if (bb == b) s_base = first;
-    all += total;
-  }
-  __syncthreads();
+  const int all = p.line[p.B], line = p.line[b];
   int ctx, count;
   if (!request(p, b, ctx, count)) return;
-  const int nt = (ctx + count + 127) >> 7, share = share_of(all), w0 = s_base + item * nt;
-  const int c0 = w0 / share, c1 = (w0 + nt - 1) / share;
-  if (c0 == c1) return;  // finished by its one CTA
+  const int len = ((ctx + count + 127) >> 7) + kItemCost, share = share_of(all), at = line + item * len;
+  const int w0 = (at + kItemCost) / share, w1 = (at + len - 1) / share;  // workers of its first and last tile
+  if (w0 == w1) return;                                                  // finished by its one worker
   const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
-  const int r = static_cast<int>(blockIdx.y) * 8 + warp, rr = rt * 128 + r, gq = rr / p.T, t = rr - gq * p.T;
-  if (r >= p.slot_rows || rr >= p.rows || t >= count) return;
-  // the first CTA's part is its last segment, the others' their first
-  auto slot = [&](int c) { return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * p.slot_rows + r; };
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.stats[slot(c)].x);
-#pragma unroll
-  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  float l = 0.f, o[E];
+  const int r = static_cast<int>(blockIdx.y), rr = rt * 128 + r, gq = rr / p.T, t = rr - gq * p.T;
+  if (rr >= p.rows || t >= count) return;
+  // the first worker's part is its last segment, the others' their first
+  auto slot = [&](int w) { return static_cast<size_t>(2 * w + (w == w0 ? 1 : 0)) * p.slot_rows + r; };
+  float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int i0 = c0; i0 <= c1; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane <= c1) {
-      const float2 st = p.stats[slot(i0 + lane)];
-      w = st.x == -INFINITY ? 0.f : ex2(st.x - m);
-      l = fmaf(w, st.y, l);
-    }
-    const int n = min(32, c1 - i0 + 1);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.slots + slot(i0 + i) * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        o[0] = fmaf(wi, x.x, o[0]);
-        o[1] = fmaf(wi, x.y, o[1]);
-        o[2] = fmaf(wi, x.z, o[2]);
-        o[3] = fmaf(wi, x.w, o[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        o[0] = fmaf(wi, x.x, o[0]);
-        o[1] = fmaf(wi, x.y, o[1]);
+  constexpr int kBatch = 8;
+  for (int i0 = w0 + warp; i0 <= w1; i0 += kMergeWarps * kBatch) {
+    float2 st[kBatch];
+    float x[kBatch][E];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int w = i0 + i * kMergeWarps;
+      st[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+      if (w <= w1) {
+        st[i] = p.stats[slot(w)];
+        const float* src = p.slots + slot(w) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src + e);
+          x[i][e] = y.x;
+          x[i][e + 1] = y.y;
+        }
       }
     }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, st[i].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref);
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= a;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float w = ex2(st[i].x - ref);
+      l = fmaf(w, st[i].y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[i][e], o[e]);
+    }
+    m = mn;
   }
 #pragma unroll
-  for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint32_t* out = static_cast<uint32_t*>(p.o) +
-                  ((((static_cast<size_t>(b) * p.H + hk * p.group + gq) * p.T + t) * D + lane * E) >> 1);
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  float mm = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; e += 2) out[e / 2] = pack2<BF16>(o[e] * inv, o[e + 1] * inv);
+  for (int w = 0; w < kMergeWarps; ++w) mm = fmaxf(mm, s_m[w]);
+  if (mm == -INFINITY) mm = 0.f;
+  const int c = 2 * threadIdx.x;  // two columns a thread
+  if (c >= D) return;
+  float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float a = ex2(s_m[w] - mm);
+    sum = fmaf(a, s_l[w], sum);
+    y0 = fmaf(a, s_o[w][c], y0);
+    y1 = fmaf(a, s_o[w][c + 1], y1);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t* out = static_cast<uint32_t*>(p.o) +
+                  ((((static_cast<size_t>(b) * p.H + hk * p.group + gq) * p.T + t) * D + c) >> 1);
+  *out = pack2<BF16>(y0 * inv, y1 * inv);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -311,16 +357,15 @@ stof_status launch_tree(const void* q, const void* k, const void* v, const TreeP
   if (!make_bw_map(&mq, q, planes, p.rows, D, kBM, BF16) || !make_bw_map(&mk, k, planes, p.cap, D, 128, BF16) ||
       !make_bw_map(&mv, v, planes, p.cap, D, 128, BF16))
     return STOF_ERR_CUDA;
-  constexpr int ST = D == 128 ? 3 : 6;  // 32 or 16 KB a stage: about 200 KB of K and V in flight or in use
   stof_status st;
   switch (mode) {
-    case MODE_PLAIN: st = launch_scored<CacheSource, D, BF16, MODE_PLAIN, ST>(mq, mk, mv, p, kTreeCtas, s); break;
-    case MODE_CAP: st = launch_scored<CacheSource, D, BF16, MODE_CAP, ST>(mq, mk, mv, p, kTreeCtas, s); break;
-    default: st = launch_scored<CacheSource, D, BF16, MODE_DISTANCE, ST>(mq, mk, mv, p, kTreeCtas, s); break;
+    case MODE_PLAIN: st = launch_scored<CacheSource, D, BF16, MODE_PLAIN>(mq, mk, mv, p, kTreeCtas, s); break;
+    case MODE_CAP: st = launch_scored<CacheSource, D, BF16, MODE_CAP>(mq, mk, mv, p, kTreeCtas, s); break;
+    default: st = launch_scored<CacheSource, D, BF16, MODE_DISTANCE>(mq, mk, mv, p, kTreeCtas, s); break;
   }
   if (st != STOF_OK) return st;
-  const dim3 grid(static_cast<unsigned>(planes * p.row_tiles), static_cast<unsigned>((p.slot_rows + 7) / 8));
-  combine_kernel<D, BF16><<<grid, 256, 0, s>>>(p);
+  const dim3 grid(static_cast<unsigned>(planes * p.row_tiles), static_cast<unsigned>(p.slot_rows));
+  combine_kernel<D, BF16><<<grid, 32 * kMergeWarps, 0, s>>>(p);
   return record_cuda(cudaGetLastError()) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
 
@@ -332,8 +377,8 @@ using namespace stof;
 extern "C" size_t stof_tree_attn_workspace_bytes(int B, int H, int Hkv, int T, int d) {
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || T < 1 || T > STOF_TREE_MAX_TOKENS || (d != 64 && d != 128)) return 0;
   const long long rows = static_cast<long long>(H / Hkv) * T;
-  const size_t slots = static_cast<size_t>(2 * kTreeCtas) * (rows < 128 ? rows : 128);
-  return up256(slots * d * sizeof(float)) + slots * sizeof(float2);
+  const size_t slots = static_cast<size_t>(2 * kWorkers) * (rows < 128 ? rows : 128);
+  return up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + (static_cast<size_t>(B) + 1) * sizeof(int32_t);
 }
 
 extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H,
@@ -347,9 +392,9 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   if (d != 64 && d != 128) return STOF_ERR_UNSUPPORTED;
   if (H % Hkv || T > STOF_TREE_MAX_TOKENS) return STOF_ERR_SHAPE;
   const long long rows = static_cast<long long>(H / Hkv) * T, row_tiles = (rows + 127) / 128;
-  // tiles of the call and query rows are counted in 32 bits
+  // the line of the call's tiles and its query rows are counted in 32 bits
   if (static_cast<long long>(B) * H * T >= (1ll << 31) || static_cast<long long>(B) * Hkv >= (1ll << 31) ||
-      static_cast<long double>(B) * Hkv * row_tiles * ((static_cast<long long>(cap) + 127) / 128) >= 2147483000.0L)
+      static_cast<long double>(B) * Hkv * row_tiles * ((static_cast<long long>(cap) + 127) / 128 + kItemCost) >= 2147480000.0L)
     return STOF_ERR_SHAPE;
   if (score) {
     stof_score s = *score;
@@ -385,8 +430,10 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   p.tree = tree;
   p.positions = p.slopes ? positions : nullptr;
   p.slots = static_cast<float*>(workspace);
-  const size_t slots = static_cast<size_t>(2 * kTreeCtas) * p.slot_rows;
-  p.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + up256(slots * d * sizeof(float)));
+  const size_t slots = static_cast<size_t>(2 * kWorkers) * p.slot_rows;
+  uint8_t* ws = static_cast<uint8_t*>(workspace) + up256(slots * d * sizeof(float));
+  p.stats = reinterpret_cast<float2*>(ws);
+  p.line = reinterpret_cast<int32_t*>(ws + up256(slots * sizeof(float2)));
   const int mode = mode_of(scale, softcap, p.slopes != nullptr);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
