@@ -11,8 +11,7 @@
 // started yet (clusterlaunchcontrol.try_cancel: the hardware hands out the
 // pending CTA's index instead of launching it) and gives them to its two
 // workers, so items are handed out as workers come free, with no counter in
-// memory that calls would share.  The K producer takes them; an item and its
-// list bounds reach the other warps through a ring in shared memory.
+// memory that calls would share.  The first item of worker 0 is the CTA's own.
 #include "scored_kernel.cuh"
 
 namespace stof {
@@ -22,6 +21,7 @@ using namespace scored;
 
 struct FormatParams : CommonParams {
   int L, n_tr, n_tc, q_start;
+  int per_ot;  // tiles per OT: 128 / BN
   int64_t stride_b, stride_h;
   const int32_t* full_row_ptr;
   const int32_t* full_col_idx;
@@ -33,183 +33,157 @@ struct FormatParams : CommonParams {
 struct FormatSource {
   using Params = FormatParams;
   static constexpr bool kClearsV = false;
-  static constexpr int kRing = 4;       // items in flight per worker
-  static constexpr int kReaders = 7;    // V producer, score and PV issuers, four softmax warps
   struct Item {
-    int id;      // query tile, head-major; negative: no more
-    int f0, nf;  // its full OTs in the lists
+    int head;
+    int f0, nf;  // its first full OT in the list, tiles of its full OTs
     int p0;      // its first partial OT
-  };
-  struct Slot {
-    Item item;
-    int n;
+    int per_ot;  // tiles per OT: 128 / BN
   };
   struct Shared {
-    alignas(16) uint4 answer;           // of try_cancel
+    alignas(16) uint4 answer;  // of try_cancel
     uint64_t answered;
-    uint64_t full[2][kRing], free_[2][kRing];
-    Slot ring[2][kRing];
+    int lock;                  // the producer that handles the answer
+    int asked;                 // requests so far; under the lock
+    int done;                  // a request was refused: none follows
   };
   struct Row {
     int head;
     int pos;                 // the row's position among the keys
     int i;                   // query row of the head
+    size_t out;              // row of O
     const uint8_t* bits;     // the row's byte of IT column 0 in a partial tile's bitmaps
     uint32_t nb[16];         // its bytes of the next partial tile, loaded a tile ahead
   };
 
   static __device__ void init(Shared& s) {
     mbar_init(&s.answered, 1);
-    for (int g = 0; g < 2; ++g)
-      for (int i = 0; i < kRing; ++i) {
-        mbar_init(&s.full[g][i], 1);
-        mbar_init(&s.free_[g][i], kReaders);
-      }
+    s.lock = s.asked = s.done = 0;
   }
   static __device__ void prologue(const Params&, Shared&) {}
 
-  // The K producer's hold on the items: this CTA's own first, then those of
-  // CTAs that have not started.  One request is always in flight until one
-  // is refused; none follows a refusal.
+  // A producer's way to its items.  One request to the hardware is in flight
+  // at a time; either producer takes the answer and makes the next request,
+  // until one is refused (after which none may follow).
   struct Lead {
-    const Params& p;
-    Shared& s;
-    const volatile int* abort_flag;
-    int asked = 0;
-    bool own = true, done = false, waiting = false;
-    __device__ Lead(const Params& params, Shared& sh, const volatile int* abort) : p(params), s(sh), abort_flag(abort) { ask(); }
-    __device__ void ask() {
+    int g;
+    bool first = true, ended = false;
+    __device__ Lead(const Params&, Shared& s, int worker) : g(worker) {
+      if (g == 0) ask(s);
+    }
+    static __device__ void ask(Shared& s) {
       mbar_arrive_expect_tx(&s.answered, 16);
       asm volatile(
           "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
               smem_u32(&s.answer)),
           "r"(smem_u32(&s.answered))
           : "memory");
-      waiting = true;
-      ++asked;
+      *static_cast<volatile int*>(&s.asked) = *static_cast<volatile int*>(&s.asked) + 1;
     }
-    // Next item, -1: no more, -2: the wait ran out.
-    __device__ int take() {
-      if (own) {
-        own = false;
+    // Next item, -1: no more, -2: a wait ran out.
+    __device__ int take(Shared& s, const volatile int* abort_flag) {
+      if (g == 0 && first) {
+        first = false;
         return static_cast<int>(blockIdx.x);
       }
-      if (done) return -1;
-      if (!mbar_wait(&s.answered, (asked - 1) & 1, abort_flag, kWaitNs)) return -2;
-      waiting = false;
-      uint32_t got, id;
-      asm volatile(
-          "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
-          "ld.shared.b128 h, [%2];\n\t"
-          "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t"
-          "mov.u32 %1, 0;\n\t"
-          "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-          : "=r"(got), "=r"(id)
-          : "r"(smem_u32(&s.answer))
-          : "memory");
-      if (!got) {
-        done = true;
-        return -1;
-      }
-      fence_proxy_async_smem();  // the answer is read before it is overwritten
-      ask();
-      return static_cast<int>(id);
-    }
-    __device__ void drain() {  // no copy into this CTA's memory outlives it
-      if (waiting) mbar_wait_timeout(&s.answered, (asked - 1) & 1, kWaitNs);
-    }
-  };
-
-  // A worker's items.
-  template <int WHO>
-  struct Feed {
-    const Params& p;
-    Shared& s;
-    const volatile int* abort_flag;
-    Lead* lead;
-    int g, k = 0;
-    bool ok = true;
-    __device__ Feed(const Params& params, Shared& sh, int worker, const volatile int* abort, Lead* l)
-        : p(params), s(sh), abort_flag(abort), lead(l), g(worker) {}
-    __device__ bool next(Segment<Item>& seg) {
-      if (!ok) return false;
-      const int slot = k % kRing, ph = (k / kRing) & 1;
-      Slot& x = s.ring[g][slot];
-      if constexpr (WHO == FEED_LEAD) {
-        const int id = lead->take();
-        Item item{id, 0, 0, 0};
-        int n = 0;
-        if (id >= 0) {
-          const int bh = id / p.n_tr, I = p.n_tr - 1 - (id - bh * p.n_tr);
-          const long long mrow = ((bh / p.H) * p.stride_b + (bh % p.H) * p.stride_h) * p.n_tr + I;
-          item.f0 = __ldg(p.full_row_ptr + mrow);
-          item.p0 = __ldg(p.part_row_ptr + mrow);
-          item.nf = __ldg(p.full_row_ptr + mrow + 1) - item.f0;
-          n = item.nf + __ldg(p.part_row_ptr + mrow + 1) - item.p0;
+      const uint64_t t0 = globaltimer_ns();
+      while (atomicCAS_block(&s.lock, 0, 1) != 0)
+        if (*abort_flag || globaltimer_ns() - t0 > kWaitNs) return -2;
+      __threadfence_block();
+      int id = -1;
+      if (!*static_cast<volatile int*>(&s.done)) {
+        // worker 0 makes the first request as it starts
+        while (*static_cast<volatile int*>(&s.asked) == 0)
+          if (*abort_flag || globaltimer_ns() - t0 > kWaitNs) return -2;
+        if (!mbar_wait(&s.answered, (*static_cast<volatile int*>(&s.asked) - 1) & 1, abort_flag, kWaitNs)) return -2;
+        uint32_t got, x;
+        asm volatile(
+            "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+            "ld.shared.b128 h, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t"
+            "mov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+            : "=r"(got), "=r"(x)
+            : "r"(smem_u32(&s.answer))
+            : "memory");
+        if (got) {
+          id = static_cast<int>(x);
+          fence_proxy_async_smem();  // the answer is read before it is overwritten
+          ask(s);
+        } else {
+          *static_cast<volatile int*>(&s.done) = 1;
         }
-        if (k >= kRing && !mbar_wait(&s.free_[g][slot], ph ^ 1, abort_flag, kWaitNs)) return ok = false;
-        x.item = item;
-        x.n = n;
-        mbar_arrive(&s.full[g][slot]);
-        if (id == -2) return ok = false;
-        fill(seg, item, n);
-      } else {
-        ok = WHO == FEED_WARP ? warp_wait(&s.full[g][slot], ph, abort_flag)
-                              : mbar_wait(&s.full[g][slot], ph, abort_flag, kWaitNs);
-        if (!ok) return false;
-        fill(seg, x.item, x.n);
-        if (WHO == FEED_WARP) __syncwarp();  // every lane has read the slot
-        if (WHO == FEED_THREAD || (threadIdx.x & 31) == 0) mbar_arrive(&s.free_[g][slot]);
       }
-      ++k;
-      return seg.item.id >= 0;
+      __threadfence_block();
+      atomicExch_block(&s.lock, 0);
+      return id;
     }
-    __device__ void fill(Segment<Item>& seg, const Item& item, int n) {
-      const int bh = item.id / p.n_tr;
-      seg.item = item;
+    __device__ Next next(const Params& p, Shared& s, const volatile int* abort_flag, Segment<Item>& seg) {
+      const int id = take(s, abort_flag);
+      if (id < 0) {
+        ended = id == -1;
+        return ended ? Next::none : Next::lost;
+      }
+      const int bh = id / p.n_tr, I = p.n_tr - 1 - (id - bh * p.n_tr), b = bh / p.H, h = bh - b * p.H;
+      const long long mrow = (b * p.stride_b + h * p.stride_h) * p.n_tr + I;
+      const int f0 = __ldg(p.full_row_ptr + mrow), f1 = __ldg(p.full_row_ptr + mrow + 1);
+      const int p0 = __ldg(p.part_row_ptr + mrow), p1 = __ldg(p.part_row_ptr + mrow + 1);
       seg.q_plane = bh;
-      seg.q_row = (p.n_tr - 1 - (item.id - bh * p.n_tr)) * kBM;
-      seg.kv_plane = (bh / p.H) * (p.H / p.group) + (bh % p.H) / p.group;
-      seg.n = n;
+      seg.q_row = I * kBM;
+      seg.kv_plane = b * (p.H / p.group) + h / p.group;
+      seg.n = (f1 - f0 + p1 - p0) * p.per_ot;
+      seg.item = Item{h, f0, (f1 - f0) * p.per_ot, p0, p.per_ot};
+      return Next::segment;
+    }
+    // Nothing is written to this CTA's memory after its end: a refusal is the
+    // last answer; without one a request may still be in flight.
+    __device__ void drain(Shared& s) {
+      const int asked = *static_cast<volatile int*>(&s.asked);
+      if (!ended && asked > 0) mbar_wait_timeout(&s.answered, (asked - 1) & 1, kWaitNs);
     }
   };
 
-  // first key of the t-th listed OT (full ones first)
+  // first key of tile t (the OTs' tiles in list order, full ones first)
   static __device__ int tile_key(const Params& p, const Item& x, int t) {
-    int J = t >= x.nf ? p.part_col_idx[x.p0 + (t - x.nf)] : p.full_col_idx[x.f0 + t];
+    const int two = x.per_ot - 1;  // tile t is half t & two of OT t >> two
+    int J = t >= x.nf ? p.part_col_idx[x.p0 + ((t - x.nf) >> two)] : p.full_col_idx[x.f0 + (t >> two)];
     if (J < 0 || J >= p.n_tc) {
       raise_error(p.err, STOF_DEVERR_BAD_FORMAT);
       J = 0;
     }
-    return J * 128;
+    return J * 128 + 64 * (t & two);
   }
-  static __device__ bool begin_row(const Params& p, Row& row, const Item& x, int r) {
-    const int bh = x.id / p.n_tr;
-    row.head = bh % p.H;
-    row.i = (p.n_tr - 1 - (x.id - bh * p.n_tr)) * kBM + r;
+  static __device__ bool begin_row(const Params& p, Row& row, const Segment<Item>& seg, int r) {
+    row.head = seg.item.head;
+    row.i = seg.q_row + r;
     row.pos = row.i + p.q_start;
+    row.out = static_cast<size_t>(seg.q_plane) * p.L + row.i;
     row.bits = reinterpret_cast<const uint8_t*>(p.bitmaps) + (r >> 3) * 128 + (r & 7);
     return row.i < p.L;
   }
+  template <int BN>
   static __device__ void prefetch(const Params&, Row& row, const Item& x, int t, int n) {
     if (t < n && t >= x.nf) {
-      const uint8_t* src = row.bits + static_cast<long long>(x.p0 + (t - x.nf)) * 2048;
+      const int u = t - x.nf;
+      const uint8_t* src = row.bits + static_cast<long long>(x.p0 + (BN == 64 ? u >> 1 : u)) * 2048 + (BN == 64 ? (u & 1) * 64 : 0);
 #pragma unroll
-      for (int w = 0; w < 16; ++w) row.nb[w] = __ldg(src + w * 8);
+      for (int w = 0; w < BN / 8; ++w) row.nb[w] = __ldg(src + w * 8);
     }
   }
   static __device__ bool partial(const Item& x, int t) { return t >= x.nf; }
-  static __device__ void bits(const Params&, const Row& row, const Item&, int, uint32_t (&b)[4]) { assemble_bits<4>(row.nb, b); }
-  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, uint32_t (&sr)[4][32], float c,
+  template <int BN>
+  static __device__ void bits(const Params&, const Row& row, const Item&, int, uint32_t (&b)[BN / 32]) {
+#pragma unroll
+    for (int cc = 0; cc < BN / 32; ++cc)
+      b[cc] = row.nb[4 * cc] | (row.nb[4 * cc + 1] << 8) | (row.nb[4 * cc + 2] << 16) | (row.nb[4 * cc + 3] << 24);
+  }
+  template <int CHUNKS>
+  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, uint32_t (&sr)[CHUNKS][32], float c,
                                float slope) {
     const int rel = row.pos - tile_key(p, x, t);
-    lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= 127));
+    lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= CHUNKS * 32 - 1));
   }
   static __device__ bool whole(const Item&) { return true; }
-  static __device__ size_t out_row(const Params& p, const Row& row, const Item& x) {
-    return static_cast<size_t>(x.id / p.n_tr) * p.L + row.i;
-  }
   static __device__ float* partial_o(const Params&, const Item&, int, int, int) { return nullptr; }
   static __device__ void put_stats(const Params&, const Item&, int, int, float, float) {}
 };
@@ -218,8 +192,8 @@ template <int D, bool BF16>
 stof_status launch_d(const ScoredParams& a, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   const uint64_t heads = static_cast<uint64_t>(a.B) * a.H, kv = heads / a.group;
-  if (!make_bw_map(&mq, a.q, heads, a.L, D, kBM, BF16) || !make_bw_map(&mk, a.k, kv, a.Lk, D, 128, BF16) ||
-      !make_bw_map(&mv, a.v, kv, a.Lk, D, 128, BF16))
+  if (!make_bw_map(&mq, a.q, heads, a.L, D, kBM, BF16) || !make_bw_map(&mk, a.k, kv, a.Lk, D, Shape<D>::BN, BF16) ||
+      !make_bw_map(&mv, a.v, kv, a.Lk, D, Shape<D>::BN, BF16))
     return STOF_ERR_CUDA;
   FormatParams p;
   p.k = make_score_const(a.scale, a.softcap);
@@ -232,6 +206,7 @@ stof_status launch_d(const ScoredParams& a, cudaStream_t s) {
   p.n_tr = a.n_tr;
   p.n_tc = a.n_tc;
   p.q_start = a.q_start;
+  p.per_ot = 128 / Shape<D>::BN;
   p.stride_b = a.stride_b;
   p.stride_h = a.stride_h;
   p.full_row_ptr = a.full_row_ptr;

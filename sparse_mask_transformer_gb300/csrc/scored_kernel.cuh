@@ -2,35 +2,34 @@
 // shared by its two sources of tiles:
 //   FormatSource  the listed outer tiles of the query tiles of a mask format
 //                 (blockwise_score.cu, stof_mha_fwd_score);
-//   CacheSource   the 128-key tiles of the requests' K/V caches (tree_attn.cu,
+//   CacheSource   the tiles of the requests' K/V caches (tree_attn.cu,
 //                 stof_tree_attn_fwd).
-// A segment is a run of K/V tiles of 128 keys for one tile of 128 query
-// rows; its online softmax gives the rows' O, or a partial O with the rows'
-// max and sum where other workers hold the rest.
+// A segment is a run of K/V tiles of BN keys for one tile of 128 query rows;
+// its online softmax gives the rows' O, or a partial O with the rows' max and
+// sum where other workers hold the rest.
 //
-// A CTA runs two workers, softmax warpgroups g = 0 and 1, each with segments
-// of its own (its Q tile in shared memory, its P and O in TMEM, its running
-// max and sum in registers), one after the other.  While one worker loads Q,
-// starts or finishes a segment, the tensor cores, the copies and the other
-// worker go on, so that short segments (a few tiles, as packed documents and
-// short caches give) cost little more than their tiles.  (Both warpgroups on
-// the tiles of one segment, merged at its end, took 88 us instead of
-// @DOCS@ us on 4096 tokens of five documents, 32 heads of 128, and 6 us for
-// every one-tile segment of a cache.)
-//   warp 0      K producer (TMA ring);
-//   warp 1      V producer (TMA ring) and the workers' Q tiles;
-//   warp 2      TMEM, score MMAs S = Q_g K^T;
-//   warp 3      PV MMAs O_g += P_g V, P read from TMEM;
-//   warps 4-7, 8-11  the workers' softmax, a thread per query row.
-// The workers' tiles take turns (g = 0, 1, 0, 1, ...; when one has no more
-// segments, the other goes on alone), in the same order in warps 0 to 3, so
-// the rings need no labels.  A softmax warp whose 32 query rows are all past
-// the tile's last one only keeps the barriers' step: a decode step of four
-// query rows runs one warp in four.
-// TMEM columns, d = 128: S [0,128), one buffer that a worker hands on as
-// soon as its scores are in registers; P_g [128 + 64 g, +64); O_g [256 +
-// 128 g, +128).  d = 64: S_g [128 g, +128), P_g [256 + 64 g, +64), O_g [384 +
-// 64 g, +64).
+// A CTA runs two workers g = 0, 1 that share nothing but the SM's units: each
+// has segments of its own, one after the other, a Q tile and K and V rings
+// in shared memory, S, P and O in TMEM, and its own warps:
+//   warp g          producer (one thread): takes segments, copies Q, K, V (TMA);
+//   warp 2 + g      score MMAs S = Q K^T and PV MMAs O += P V (P read from
+//                   TMEM), the scores of the next tile before the PV of this;
+//   warps 4 + 4 g ..  softmax, a thread per query row.
+// While one worker loads Q, starts or finishes a segment or waits for a tile,
+// the other one's tiles go on, so that short segments (a few tiles, as
+// packed documents and short caches give) cost little more than their tiles.
+// Both workers run the same code: what bounds this kernel besides the units
+// themselves is the instruction cache, whose 32 KB the softmax's
+// straight-line code for a tile must share with the other warps' loops.
+// (With K, V, score and PV warps that served both workers in turn the loops
+// took 32 KB, and 92% of the instruction fetch bandwidth behind the cache:
+// 723 us instead of @CAUSAL@ us for 8192 causal tokens, 32 heads of 128.)
+// A softmax warp whose 32 query rows are all past the tile's last one only
+// keeps the barriers' step: a decode step of four query rows runs one warp
+// in four.
+// BN is 128 for d = 64 and 64 for d = 128: S, P and O of both workers then fit
+// the 512 TMEM columns, and a ring stage is 16 KB.  TMEM columns: S_g [BN g,
+// +BN), P_g [2 BN + BN / 2 g, +BN / 2), O_g [512 - 2 d + d g, +d).
 // Every wait is bounded; on timeout the CTA raises STOF_DEVERR_PIPE_TIMEOUT
 // (where there is an error word), drains its copies and MMAs, frees TMEM and
 // exits.
@@ -74,68 +73,97 @@ struct Segment {
   ITEM item;
 };
 
-// Ring depths: K tiles leave early (their MMA comes first), V tiles a softmax
-// later; 160 KB in both at d = 64 and 128.
+// Tile width and ring depths (per worker): 16 KB a stage.  K tiles leave
+// early (their MMA comes first), V tiles a softmax later.
 template <int D>
-struct Depth {
-  static constexpr int K = D == 128 ? 3 : 5, V = D == 128 ? 2 : 5;
+struct Shape {
+  static constexpr int BN = D == 128 ? 64 : 128;
+  static constexpr int K = 3, V = D == 128 ? 2 : 3;
+  static constexpr int STAGE = BN * D * 2;
+  static constexpr int ATOM = BN * 128;  // bytes of a 64-column swizzle atom of a K or V tile
+};
+
+// A worker's producer takes its segments from the source and hands them to
+// the worker's other warps through a ring in shared memory.
+constexpr int kRing = 4;     // segments in flight
+constexpr int kReaders = 5;  // the MMA warp, four softmax warps
+enum class Next { segment, none, lost };  // lost: a wait ran out
+
+// What one worker has in shared memory.
+template <class SRC, int D>
+struct Worker {
+  uint64_t q_full, q_done;  // Q is in place; the segment's score MMAs are done
+  uint64_t k_full[Shape<D>::K], k_free[Shape<D>::K], v_full[Shape<D>::V], v_free[Shape<D>::V];
+  uint64_t s_full, s_free, p_full, pv_done, drain;
+  uint64_t ring_full[kRing], ring_free[kRing];
+  Segment<typename SRC::Item> ring[kRing];  // n < 0: no more segments
 };
 
 template <class SRC, int D>
 struct alignas(1024) Smem {
-  uint8_t q[2][kBM * D * 2];  // per worker
-  uint8_t k[Depth<D>::K][128 * D * 2];
-  uint8_t v[Depth<D>::V][128 * D * 2];
-  uint64_t q_full[2], q_done[2];  // per worker: Q is in place; its segment's score MMAs are done
-  uint64_t k_full[Depth<D>::K], k_free[Depth<D>::K], v_full[Depth<D>::V], v_free[Depth<D>::V];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
-  uint64_t drain, drain_qk;
+  uint8_t q[2][kBM * D * 2];
+  uint8_t k[2][Shape<D>::K][Shape<D>::STAGE];
+  uint8_t v[2][Shape<D>::V][Shape<D>::STAGE];
+  Worker<SRC, D> w[2];
   uint32_t tmem_base;
   int abort_flag;
   typename SRC::Shared src;
 };
-
-// Who reads a worker's segments: the K producer (which takes them from the
-// source), one thread, or a whole warp.
-constexpr int FEED_LEAD = 0, FEED_THREAD = 1, FEED_WARP = 2;
 
 // A wait that gives the same answer in every lane of the warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitNs));
 }
 
+// O row (d fp32 columns at tOr) *= alpha, in TMEM; a loop, being rare.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t tOr, float alpha) {
+#pragma unroll 1
+  for (int cc = 0; cc < D / 32; ++cc) {
+    uint32_t o[32];
+    tmem_ld32(tOr + cc * 32, o);
+    tmem_ld_wait(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st32(tOr + cc * 32, o);
+  }
+}
+
 template <class SRC, int D, bool BF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ typename SRC::Params p) {
-  constexpr int REGIONS = D / 64, ATOM = 128 * 128, KV_BYTES = 128 * D * 2, CHUNKS = 4;
-  constexpr int STK = Depth<D>::K, STV = Depth<D>::V;
-  using Seg = Segment<typename SRC::Item>;
-  extern __shared__ uint8_t smem_raw[];
+  using Sh = Shape<D>;
+  constexpr int BN = Sh::BN, REGIONS = D / 64, Q_ATOM = kBM * 128, CHUNKS = BN / 32;
   using Shared = Smem<SRC, D>;
+  extern __shared__ uint8_t smem_raw[];
   Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < STK; ++i) {
-      mbar_init(&s.k_full[i], 1);
-      mbar_init(&s.k_free[i], 1);
+  if (threadIdx.x < 2) {
+    Worker<SRC, D>& w = s.w[threadIdx.x];
+    mbar_init(&w.q_full, 1);
+    mbar_init(&w.q_done, 1);
+    for (int i = 0; i < Sh::K; ++i) {
+      mbar_init(&w.k_full[i], 1);
+      mbar_init(&w.k_free[i], 1);
     }
-    for (int i = 0; i < STV; ++i) {
-      mbar_init(&s.v_full[i], 1);
-      mbar_init(&s.v_free[i], 1);
+    for (int i = 0; i < Sh::V; ++i) {
+      mbar_init(&w.v_full[i], 1);
+      mbar_init(&w.v_free[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.q_full[i], 1);
-      mbar_init(&s.q_done[i], 1);
-      mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.s_free[i], 128);
-      mbar_init(&s.p_full[i], 128);
-      mbar_init(&s.pv_done[i], 1);
+    mbar_init(&w.s_full, 1);
+    mbar_init(&w.s_free, 128);
+    mbar_init(&w.p_full, 128);
+    mbar_init(&w.pv_done, 1);
+    mbar_init(&w.drain, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&w.ring_full[i], 1);
+      mbar_init(&w.ring_free[i], kReaders);
     }
-    mbar_init(&s.drain, 1);
-    mbar_init(&s.drain_qk, 1);
-    s.abort_flag = 0;
-    SRC::init(s.src);
+    if (threadIdx.x == 0) {
+      s.abort_flag = 0;
+      SRC::init(s.src);
+    }
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -146,238 +174,221 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = s.tmem_base;
-  constexpr uint32_t kP = D == 128 ? 128 : 256, kO = D == 128 ? 256 : 384;
-  auto s_at = [&](int g) { return D == 128 ? tbase : tbase + 128 * g; };
+  const int g = warp < 4 ? warp & 1 : (warp - 4) >> 2;  // the warp's worker
+  Worker<SRC, D>& w = s.w[g];
+  const uint32_t tS = s.tmem_base + BN * g, tP = s.tmem_base + 2 * BN + BN / 2 * g, tO = s.tmem_base + 512 - 2 * D + D * g;
   volatile int* abort_flag = &s.abort_flag;
   auto fail = [&]() {
     *abort_flag = 1;
     if (p.err) raise_error(p.err, STOF_DEVERR_PIPE_TIMEOUT);
   };
-  // The two workers' tiles in turn: begin(g) at each new segment with tiles,
-  // tile(g) for every tile (false: give up), until both have no more.
-  auto turns = [&](auto& feed0, auto& feed1, Seg (&seg)[2], int (&t)[2], auto&& begin, auto&& tile) {
-    bool has[2], ok = true;
-    auto advance = [&](auto gc, auto& feed) {
-      constexpr int G = decltype(gc)::value;
-      do has[G] = feed.next(seg[G]);
-      while (has[G] && seg[G].n == 0);
-      t[G] = 0;
-      if (has[G]) ok = begin(gc) && ok;
-    };
-    auto step = [&](auto gc, auto& feed) {
-      constexpr int G = decltype(gc)::value;
-      ok = tile(gc);
-      if (ok && ++t[G] == seg[G].n) advance(gc, feed);
-    };
-    std::integral_constant<int, 0> w0;
-    std::integral_constant<int, 1> w1;
-    advance(w0, feed0);
-    advance(w1, feed1);
-    while (ok && (has[0] || has[1])) {
-      if (has[0]) step(w0, feed0);
-      if (ok && has[1]) step(w1, feed1);
-    }
-    return ok && feed0.ok && feed1.ok;
+  // the worker's segment number `handed`, out of its ring (a whole warp)
+  auto read_ring = [&](int handed, Segment<typename SRC::Item>& seg) {
+    const int slot = handed % kRing;
+    if (!warp_wait(&w.ring_full[slot], (handed / kRing) & 1, abort_flag)) return Next::lost;
+    seg = w.ring[slot];
+    __syncwarp();  // every lane has read it
+    if (lane == 0) mbar_arrive(&w.ring_free[slot]);
+    return seg.n >= 0 ? Next::segment : Next::none;
   };
+  Segment<typename SRC::Item> seg;
+  bool ok = true;
 
-  if (warp < 4) {
+  if (warp < 4)
     regs_dec<kProducerRegs>();
-    Seg seg[2];
-    int t[2] = {0, 0};
-    if (warp == 0) {
-      // ------------------------------------------------------------ K producer
-      if (lane == 0) {
-        prefetch_tmap(&tmK);
-        typename SRC::Lead lead(p, s.src, abort_flag);
-        typename SRC::template Feed<FEED_LEAD> f0(p, s.src, 0, abort_flag, &lead), f1(p, s.src, 1, abort_flag, &lead);
-        int it = 0, st = 0, ph = 0;
-        const bool ok = turns(f0, f1, seg, t, [&](auto) { return true; }, [&](auto gc) {
-          constexpr int G = decltype(gc)::value;
-          if (it >= STK && !mbar_wait(&s.k_free[st], ph ^ 1, abort_flag, kWaitNs)) return false;
-          const int row = SRC::tile_key(p, seg[G].item, t[G]);
-          mbar_arrive_expect_tx(&s.k_full[st], KV_BYTES);
+  else
+    regs_inc<kSoftmaxRegs>();
+  if (warp < 2) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      typename SRC::Lead lead(p, s.src, g);
+      int ik = 0, iv = 0, nq = 0;  // K, V and Q tiles so far
+      int sk = 0, pk = 0, sv = 0, pv = 0;
+      // one K or V tile of the segment; K runs one tile ahead of V
+      auto copy = [&](bool is_k, int t) {
+        int& i = is_k ? ik : iv;
+        int& st = is_k ? sk : sv;
+        int& ph = is_k ? pk : pv;
+        const int depth = is_k ? Sh::K : Sh::V;
+        uint64_t* full = (is_k ? w.k_full : w.v_full) + st;
+        const int row = SRC::tile_key(p, seg.item, t);
+        if (i >= depth && !mbar_wait((is_k ? w.k_free : w.v_free) + st, ph ^ 1, abort_flag, kWaitNs)) return false;
+        uint8_t* to = is_k ? s.k[g][st] : s.v[g][st];
+        const CUtensorMap* map = is_k ? &tmK : &tmV;
+        mbar_arrive_expect_tx(full, Sh::STAGE);
 #pragma unroll
-          for (int r = 0; r < REGIONS; ++r)
-            tma_load_3d(s.k[st] + r * ATOM, &tmK, &s.k_full[st], 64 * r, row, seg[G].kv_plane);
-          ++it;
-          if (++st == STK) {
-            st = 0;
-            ph ^= 1;
-          }
-          return true;
-        });
-        if (!ok) fail();
-        lead.drain();
-        if (*abort_flag) {  // let every copy this thread started land before exit
-          for (int i = it - STK < 0 ? 0 : it - STK; i < it; ++i) mbar_wait_timeout(&s.k_full[i % STK], (i / STK) & 1, kWaitNs);
-        }
-      }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ Q tiles, V producer
-      if (lane == 0) {
-        prefetch_tmap(&tmQ);
-        prefetch_tmap(&tmV);
-        typename SRC::template Feed<FEED_THREAD> f0(p, s.src, 0, abort_flag, nullptr), f1(p, s.src, 1, abort_flag, nullptr);
-        int it = 0, st = 0, ph = 0, nq[2] = {0, 0};
-        const bool ok = turns(f0, f1, seg, t, [&](auto gc) {
-          constexpr int G = decltype(gc)::value;
-          // the worker's Q is overwritten once its last segment's score MMAs are done
-          if (nq[G] > 0 && !mbar_wait(&s.q_done[G], (nq[G] - 1) & 1, abort_flag, kWaitNs)) return false;
-          ++nq[G];
-          mbar_arrive_expect_tx(&s.q_full[G], kBM * D * 2);
-#pragma unroll
-          for (int r = 0; r < REGIONS; ++r)
-            tma_load_3d(s.q[G] + r * ATOM, &tmQ, &s.q_full[G], 64 * r, seg[G].q_row, seg[G].q_plane);
-          return true;
-        }, [&](auto gc) {
-          constexpr int G = decltype(gc)::value;
-          if (it >= STV && !mbar_wait(&s.v_free[st], ph ^ 1, abort_flag, kWaitNs)) return false;
-          const int row = SRC::tile_key(p, seg[G].item, t[G]);
-          mbar_arrive_expect_tx(&s.v_full[st], KV_BYTES);
-#pragma unroll
-          for (int r = 0; r < REGIONS; ++r)
-            tma_load_3d(s.v[st] + r * ATOM, &tmV, &s.v_full[st], 64 * r, row, seg[G].kv_plane);
-          ++it;
-          if (++st == STV) {
-            st = 0;
-            ph ^= 1;
-          }
-          return true;
-        });
-        if (!ok) fail();
-        if (*abort_flag) {
-          for (int g = 0; g < 2; ++g)
-            if (nq[g] > 0) mbar_wait_timeout(&s.q_full[g], (nq[g] - 1) & 1, kWaitNs);
-          for (int i = it - STV < 0 ? 0 : it - STV; i < it; ++i) mbar_wait_timeout(&s.v_full[i % STV], (i / STV) & 1, kWaitNs);
-        }
-      }
-    } else if (warp == 2) {
-      // ------------------------------------------------------------ score MMAs
-      constexpr uint32_t idesc_qk = idesc_f16(BF16 ? 1 : 0, 0, kBM, 128);
-      const uint64_t qdesc0 = smem_desc_sw128(smem_u32(s.q[0]), 16, 1024);
-      const uint64_t kdesc0 = smem_desc_sw128(smem_u32(s.k[0]), 16, 1024);
-      typename SRC::template Feed<FEED_WARP> f0(p, s.src, 0, abort_flag, nullptr), f1(p, s.src, 1, abort_flag, nullptr);
-      int st = 0, ph = 0, nq[2] = {0, 0}, j[2] = {0, 0};
-      int prev_g = -1, prev_j = 0;  // the tile issued last
-      const bool ok = turns(f0, f1, seg, t, [&](auto) { return true; }, [&](auto gc) {
-        constexpr int G = decltype(gc)::value;
-        if (t[G] == 0) {
-          if (!warp_wait(&s.q_full[G], nq[G] & 1, abort_flag)) return false;
-          ++nq[G];
-        }
-        if (!warp_wait(&s.k_full[st], ph, abort_flag)) return false;
-        if constexpr (D == 128) {  // one S: the tile before this one has been loaded
-          if (prev_g >= 0 && !warp_wait(&s.s_free[prev_g], prev_j & 1, abort_flag)) return false;
-          prev_g = G;
-          prev_j = j[G];
-        } else {
-          if (j[G] > 0 && !warp_wait(&s.s_free[G], (j[G] - 1) & 1, abort_flag)) return false;
-        }
-        tc_fence_after();
-        const uint64_t qd = qdesc0 + static_cast<uint64_t>(G) * (kBM * D * 2 / 16);
-        const uint64_t kd = kdesc0 + static_cast<uint64_t>(st) * (KV_BYTES / 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (kk >> 2) * (ATOM / 16) + (kk & 3) * 2;
-            mma_f16_ss(s_at(G), qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&s.s_full[G]);
-          mma_commit(&s.k_free[st]);
-          if (t[G] == seg[G].n - 1) mma_commit(&s.q_done[G]);
-        }
-        __syncwarp();
-        ++j[G];
-        if (++st == STK) {
+        for (int r = 0; r < REGIONS; ++r) tma_load_3d(to + r * Sh::ATOM, map, full, 64 * r, row, seg.kv_plane);
+        ++i;
+        if (++st == depth) {
           st = 0;
           ph ^= 1;
         }
         return true;
-      });
-      if (elect_one()) {  // the lane that issued the MMAs
-        if (!ok) fail();
-        mma_commit(&s.drain_qk);
-        mbar_wait_timeout(&s.drain_qk, 0, kWaitNs);
-      }
-    } else {
-      // ------------------------------------------------------------ PV MMAs
-      constexpr uint32_t idesc_pv = idesc_f16(BF16 ? 1 : 0, 1, kBM, D);
-      const uint64_t vdesc0 = smem_desc_sw128(smem_u32(s.v[0]), ATOM, 1024);
-      typename SRC::template Feed<FEED_WARP> f0(p, s.src, 0, abort_flag, nullptr), f1(p, s.src, 1, abort_flag, nullptr);
-      int st = 0, ph = 0, j[2] = {0, 0};
-      const bool ok = turns(f0, f1, seg, t, [&](auto) { return true; }, [&](auto gc) {
-        constexpr int G = decltype(gc)::value;
-        if (!warp_wait(&s.v_full[st], ph, abort_flag)) return false;
-        if constexpr (SRC::kClearsV) {
-          // V rows behind the request's last token may hold anything, and
-          // 0 * NaN is NaN: clear them before the MMA reads the tile
-          const int end = SRC::tile_end(seg[G].item, t[G]);
-          if (end < 128) {
-            for (int x = lane; x < (128 - end) * 8 * REGIONS; x += 32) {
-              const int region = x / ((128 - end) * 8), y = x - region * (128 - end) * 8;
-              *reinterpret_cast<uint4*>(s.v[st] + region * ATOM + end * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+      };
+#pragma unroll 1
+      for (int handed = 0; ok; ++handed) {
+        const Next got = lead.next(p, s.src, abort_flag, seg);
+        const int slot = handed % kRing;
+        if (got == Next::lost ||
+            (handed >= kRing && !mbar_wait(&w.ring_free[slot], (handed / kRing - 1) & 1, abort_flag, kWaitNs))) {
+          ok = false;
+          break;
         }
-        if (!warp_wait(&s.p_full[G], j[G] & 1, abort_flag)) return false;
-        tc_fence_after();
-        const uint64_t vd = vdesc0 + static_cast<uint64_t>(st) * (KV_BYTES / 16);
-        if (elect_one()) {
+        if (got == Next::none) seg.n = -1;
+        w.ring[slot] = seg;
+        mbar_arrive(&w.ring_full[slot]);
+        if (got == Next::none) break;
+        if (seg.n == 0) continue;  // a query tile without listed tiles
+        // Q is overwritten once the last segment's score MMAs are done
+        if (nq > 0 && !mbar_wait(&w.q_done, (nq - 1) & 1, abort_flag, kWaitNs)) {
+          ok = false;
+          break;
+        }
+        ++nq;
+        mbar_arrive_expect_tx(&w.q_full, kBM * D * 2);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // the segment's first tile overwrites O_g
-            mma_f16_ts(tbase + kO + G * D, tbase + kP + G * 64 + kk * 8, vd + kk * 128, idesc_pv,
-                       (t[G] > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&s.pv_done[G]);
-          mma_commit(&s.v_free[st]);
+        for (int r = 0; r < REGIONS; ++r)
+          tma_load_3d(s.q[g] + r * Q_ATOM, &tmQ, &w.q_full, 64 * r, seg.q_row, seg.q_plane);
+        // K_0, K_1, V_0, K_2, V_1, ...
+#pragma unroll 1
+        for (int x = 0; ok && x < 2 * seg.n; ++x) {
+          const bool is_k = x == 0 || (x & 1 && x < 2 * seg.n - 1);
+          ok = copy(is_k, is_k ? (x + 1) >> 1 : (x - 1) >> 1);
         }
-        __syncwarp();
-        ++j[G];
-        if (++st == STV) {
-          st = 0;
-          ph ^= 1;
-        }
-        return true;
-      });
-      if (elect_one()) {
-        if (!ok) fail();
-        mma_commit(&s.drain);
-        mbar_wait_timeout(&s.drain, 0, kWaitNs);
+      }
+      if (!ok) fail();
+      lead.drain(s.src);
+      if (*abort_flag) {  // let every copy this thread started land before exit
+        if (nq > 0) mbar_wait_timeout(&w.q_full, (nq - 1) & 1, kWaitNs);
+        for (int i = ik - Sh::K < 0 ? 0 : ik - Sh::K; i < ik; ++i) mbar_wait_timeout(&w.k_full[i % Sh::K], (i / Sh::K) & 1, kWaitNs);
+        for (int i = iv - Sh::V < 0 ? 0 : iv - Sh::V; i < iv; ++i) mbar_wait_timeout(&w.v_full[i % Sh::V], (i / Sh::V) & 1, kWaitNs);
       }
     }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ MMAs
+    constexpr uint32_t idesc_qk = idesc_f16(BF16 ? 1 : 0, 0, kBM, BN);
+    constexpr uint32_t idesc_pv = idesc_f16(BF16 ? 1 : 0, 1, kBM, D);
+    const uint64_t qdesc = smem_desc_sw128(smem_u32(s.q[g]), 16, 1024);
+    const uint64_t kdesc0 = smem_desc_sw128(smem_u32(s.k[g][0]), 16, 1024);
+    const uint64_t vdesc0 = smem_desc_sw128(smem_u32(s.v[g][0]), Sh::ATOM, 1024);
+    int j = 0, i = 0;  // tiles scored, tiles accumulated so far
+    int sk = 0, pk = 0, sv = 0, pv = 0, nq = 0;
+    // S = Q K_t^T
+    auto score = [&](int t) {
+      if (!warp_wait(&w.k_full[sk], pk, abort_flag)) return false;
+      if (j > 0 && !warp_wait(&w.s_free, (j - 1) & 1, abort_flag)) return false;  // S has been loaded
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t kd = kdesc0 + static_cast<uint64_t>(sk) * (Sh::STAGE / 16);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)  // 32 B per K step inside an atom
+          mma_f16_ss(tS, qdesc + (kk >> 2) * (Q_ATOM / 16) + (kk & 3) * 2, kd + (kk >> 2) * (Sh::ATOM / 16) + (kk & 3) * 2,
+                     idesc_qk, kk > 0 ? 1u : 0u);
+        mma_commit(&w.s_full);
+        mma_commit(&w.k_free[sk]);
+        if (t == seg.n - 1) mma_commit(&w.q_done);
+      }
+      __syncwarp();
+      ++j;
+      if (++sk == Sh::K) {
+        sk = 0;
+        pk ^= 1;
+      }
+      return true;
+    };
+    // O += P V_t
+    auto accumulate = [&](int t) {
+      if (!warp_wait(&w.v_full[sv], pv, abort_flag)) return false;
+      if constexpr (SRC::kClearsV) {
+        // V rows behind the request's last token may hold anything, and
+        // 0 * NaN is NaN: clear them before the MMA reads the tile
+        const int end = SRC::tile_end(seg.item, t);
+        if (end < BN) {
+#pragma unroll 1
+          for (int x = lane + end * 8; x < BN * 8; x += 32)
+#pragma unroll
+            for (int r = 0; r < REGIONS; ++r)
+              *reinterpret_cast<uint4*>(s.v[g][sv] + r * Sh::ATOM + x * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
+      if (!warp_wait(&w.p_full, i & 1, abort_flag)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t vd = vdesc0 + static_cast<uint64_t>(sv) * (Sh::STAGE / 16);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys a K step; the segment's first tile overwrites O
+          mma_f16_ts(tO, tP + kk * 8, vd + kk * 128, idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&w.pv_done);
+        mma_commit(&w.v_free[sv]);
+      }
+      __syncwarp();
+      ++i;
+      if (++sv == Sh::V) {
+        sv = 0;
+        pv ^= 1;
+      }
+      return true;
+    };
+#pragma unroll 1
+    for (int handed = 0; ok; ++handed) {
+      const Next got = read_ring(handed, seg);
+      if (got == Next::none) break;
+      ok = got == Next::segment;
+      if (!ok || seg.n == 0) continue;
+      ok = warp_wait(&w.q_full, nq & 1, abort_flag);
+      ++nq;
+      // S_0, S_1, O_0, S_2, O_1, ...
+#pragma unroll 1
+      for (int t = -1; ok && t < seg.n; ++t) {
+        if (t + 1 < seg.n) ok = score(t + 1);
+        if (ok && t >= 0) ok = accumulate(t);
+      }
+    }
+    if (elect_one()) {  // the lane that issued the MMAs
+      if (!ok) fail();
+      mma_commit(&w.drain);
+      mbar_wait_timeout(&w.drain, 0, kWaitNs);
+    }
+    __syncwarp();
   } else {
-    regs_inc<kSoftmaxRegs>();
     // ------------------------------------------------------------ softmax
-    const int quarter = warp & 3, g = (warp - 4) >> 2;
+    const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // query row in the tile == TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tSr = s_at(g) + lane_off, tP = tbase + kP + g * 64 + lane_off, tO = tbase + kO + g * D + lane_off;
-    typename SRC::template Feed<FEED_WARP> feed(p, s.src, g, abort_flag, nullptr);
+    const uint32_t tSr = tS + lane_off, tPr = tP + lane_off, tOr = tO + lane_off;
     typename SRC::Row row;
-    Seg seg;
-    int j = 0;  // this worker's tile count
-    bool ok = true;
-    while (ok && feed.next(seg)) {
-      const bool live = SRC::begin_row(p, row, seg.item, r);  // the row is one of the call's
-      const bool alive = __any_sync(0xffffffffu, live);       // the warp has such a row
+    int j = 0;  // tiles so far
+#pragma unroll 1
+    for (int handed = 0;; ++handed) {
+      const Next got = read_ring(handed, seg);
+      if (got != Next::segment) {
+        ok = got == Next::none;
+        break;
+      }
+      const bool live = SRC::begin_row(p, row, seg, r);   // the row is one of the call's
+      const bool alive = __any_sync(0xffffffffu, live);   // the warp has such a row
       float slope = 0.f;
       if (MODE == MODE_DISTANCE && p.slopes && live) slope = __ldg(p.slopes + row.head) * kLog2e;
       float m_ref = -INFINITY, l = 0.f;
-      SRC::prefetch(p, row, seg.item, 0, seg.n);
+      SRC::template prefetch<BN>(p, row, seg.item, 0, seg.n);
+#pragma unroll 1
       for (int t = 0; t < seg.n; ++t, ++j) {
-        if (!warp_wait(&s.s_full[g], j & 1, abort_flag)) { ok = false; break; }
+        if (!warp_wait(&w.s_full, j & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         if (alive) {
           uint32_t sr[CHUNKS][32];
           load_scores(tSr, sr);
           tc_fence_before();
-          mbar_arrive(&s.s_free[g]);
+          mbar_arrive(&w.s_free);  // the scores are in registers: S may be overwritten
           const bool partial = SRC::partial(seg.item, t);
           uint32_t bits[CHUNKS] = {};
-          if (partial) SRC::bits(p, row, seg.item, t, bits);
-          SRC::prefetch(p, row, seg.item, t + 1, seg.n);
+          if (partial) SRC::template bits<BN>(p, row, seg.item, t, bits);
+          SRC::template prefetch<BN>(p, row, seg.item, t + 1, seg.n);
           uint32_t pk[CHUNKS][16];
           float alpha = 1.f;
           // the max mt of the tile's scores (log2 units) becomes the
@@ -418,42 +429,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += exp_pack<CHUNKS, BF16>(sr, 1.f, nmu, pk);
           }
           if (t > 0) {
-            // P_g is rewritten and O_g rescaled once the PV of the tile before is done
-            if (!warp_wait(&s.pv_done[g], (j - 1) & 1, abort_flag)) { ok = false; break; }
+            // P is rewritten and O rescaled once the PV of the tile before is done
+            if (!warp_wait(&w.pv_done, (j - 1) & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o<D>(tO, alpha);
+            if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_row<D>(tOr, alpha);
           }
-          store_p(tP, pk);
+          store_p(tPr, pk);
         } else {  // no row of the call: keep the barriers' step
-          mbar_arrive(&s.s_free[g]);
-          if (t > 0 && !warp_wait(&s.pv_done[g], (j - 1) & 1, abort_flag)) { ok = false; break; }
+          mbar_arrive(&w.s_free);
+          if (t > 0 && !warp_wait(&w.pv_done, (j - 1) & 1, abort_flag)) { ok = false; break; }
         }
         tc_fence_before();
-        mbar_arrive(&s.p_full[g]);
+        mbar_arrive(&w.p_full);
       }
       // ---- the segment's end
-      if (!ok || (seg.n > 0 && !warp_wait(&s.pv_done[g], (j - 1) & 1, abort_flag))) {
+      if (!ok || (seg.n > 0 && !warp_wait(&w.pv_done, (j - 1) & 1, abort_flag))) {
         ok = false;
         break;
       }
       if (!alive) continue;
       tc_fence_after();
       const bool whole = SRC::whole(seg.item);
-      const float w = whole ? 1.f / l : 1.f;
-#pragma unroll
+      const float scale = whole ? 1.f / l : 1.f;
+#pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
         float x[32];
         if (seg.n > 0) {
-          tmem_ld32(tO + cc * 32, o);
+          tmem_ld32(tOr + cc * 32, o);
           tmem_ld_wait(o);
         }
         // a row that has seen no key gives 0 (its O is a sum of zeros, or unset)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : w * __uint_as_float(o[i]);
+        for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : scale * __uint_as_float(o[i]);
         if (live) {
           if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + SRC::out_row(p, row, seg.item) * D + cc * 32);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row.out * D + cc * 32);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               dst[i] = make_uint4(pack2<BF16>(x[8 * i], x[8 * i + 1]), pack2<BF16>(x[8 * i + 2], x[8 * i + 3]),
@@ -466,15 +477,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (live && !whole) SRC::put_stats(p, seg.item, g, r, m_ref, l);
-      tc_fence_before();  // O_g is read before the next segment's first p_full lets it be overwritten
+      tc_fence_before();  // O is read before the next segment's first p_full lets it be overwritten
     }
-    if (!(ok && feed.ok) && lane == 0) fail();
+    if (!ok && lane == 0) fail();
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(s.tmem_base, 512);
   }
 }
 

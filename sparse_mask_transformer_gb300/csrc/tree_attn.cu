@@ -29,6 +29,7 @@ constexpr int kItemCost = 2;               // an item's start and end, in tiles
 
 struct TreeParams : CommonParams {
   int B, Hkv, T, d, cap, words;
+  int tile;        // keys per tile: 128 (d = 64) or 64 (d = 128)
   int rows;        // group * T: query rows per K/V head
   int row_tiles;   // ceil(rows / 128)
   int slot_rows;   // rows of a partial result: min(rows, 128)
@@ -48,10 +49,13 @@ __device__ __forceinline__ bool request(const TreeParams& p, int b, int& ctx, in
   count = p.counts ? __ldg(p.counts + b) : p.T;
   return ctx >= 0 && count >= 1 && count <= p.T && ctx <= p.cap - count;
 }
+__device__ __forceinline__ int tiles_of(const TreeParams& p, int keys) {
+  return p.tile == 128 ? (keys + 127) >> 7 : (keys + 63) >> 6;
+}
 // Length of a request's items on the line (0: none).
 __device__ __forceinline__ int item_length(const TreeParams& p, int b) {
   int ctx, count;
-  return request(p, b, ctx, count) ? ((ctx + count + 127) >> 7) + kItemCost : 0;
+  return request(p, b, ctx, count) ? tiles_of(p, ctx + count) + kItemCost : 0;
 }
 
 // Exclusive prefix of v over the block's threads and the total (all threads
@@ -83,9 +87,10 @@ struct CacheSource {
   using Params = TreeParams;
   static constexpr bool kClearsV = true;
   struct Item {
-    int b, hk, rt;     // request, K/V head, row tile
+    int b, hk;         // request, K/V head
     int ctx, count;    // committed and drafted tokens
     int t0;            // first tile of the segment
+    int tile;          // keys per tile
     bool whole;        // the segment is the whole item
   };
   struct Shared {
@@ -143,37 +148,33 @@ struct CacheSource {
       base += total;
     }
   }
+  // A worker's place on the line.
   struct Lead {
-    __device__ Lead(const Params&, Shared&, const volatile int*) {}
-    __device__ void drain() {}
-  };
-
-  // A worker's segments, the same in every warp.
-  template <int WHO>
-  struct Feed {
-    const Params& p;
-    int w, end;             // place on the line, end of the share
-    int b, base, len;       // request, its place, length of its items
-    int ctx, count;
-    static constexpr bool ok = true;
-    __device__ Feed(const Params& params, Shared& s, int g, const volatile int*, Lead*) : p(params) {
+    int w, end;                      // place, end of the share
+    int b = 0, base = 0, len = 0;    // request, its place, length of its items
+    int ctx = 0, count = 0;
+    __device__ Lead(const Params& p, Shared& s, int g) {
       w = s.begin[g];
       end = s.end[g];
-      b = s.b[g];
-      base = s.base[g];
-      if (w < end) load();
+      if (w < end) {
+        b = s.b[g];
+        base = s.base[g];
+        load(p);
+      }
     }
-    __device__ void load() { len = request(p, b, ctx, count) ? ((ctx + count + 127) >> 7) + kItemCost : 0; }
-    __device__ bool next(Segment<Item>& seg) {
+    __device__ void load(const Params& p) { len = request(p, b, ctx, count) ? tiles_of(p, ctx + count) + kItemCost : 0; }
+    __device__ Next next(const Params& p, Shared&, const volatile int*, Segment<Item>& seg) {
       const int per = p.Hkv * p.row_tiles;
+#pragma unroll 1
       while (w < end) {
+#pragma unroll 1
         while (w >= base + len * per) {  // on to the next request on the line
           base += len * per;
           ++b;
-          load();
+          load(p);
         }
         const int off = w - base, item = off / len, at = off - item * len;
-        const int to = min(end, base + (item + 1) * len) - (base + item * len);  // the share's part: [at, to)
+        const int to = min(end - base - item * len, len);  // the share's part of the item: [at, to)
         w += to - at;
         const int t0 = max(0, at - kItemCost), t1 = max(0, to - kItemCost);
         if (t1 <= t0) continue;  // the share ends before the item's first tile
@@ -181,17 +182,19 @@ struct CacheSource {
         seg.q_plane = seg.kv_plane = b * p.Hkv + hk;
         seg.q_row = rt * 128;
         seg.n = t1 - t0;
-        seg.item = Item{b, hk, rt, ctx, count, t0, t1 - t0 == len - kItemCost};
-        return true;
+        seg.item = Item{b, hk, ctx, count, t0, p.tile, t1 - t0 == len - kItemCost};
+        return Next::segment;
       }
-      return false;
+      return Next::none;
     }
+    __device__ void drain(Shared&) {}
   };
 
-  static __device__ int tile_key(const Params&, const Item& x, int t) { return (x.t0 + t) * 128; }
-  static __device__ int tile_end(const Item& x, int t) { return min(128, x.ctx + x.count - (x.t0 + t) * 128); }
-  static __device__ bool begin_row(const Params& p, Row& row, const Item& x, int r) {
-    const int rr = x.rt * 128 + r, gq = rr / p.T;
+  static __device__ int tile_key(const Params&, const Item& x, int t) { return (x.t0 + t) * x.tile; }
+  static __device__ int tile_end(const Item& x, int t) { return min(x.tile, x.ctx + x.count - (x.t0 + t) * x.tile); }
+  static __device__ bool begin_row(const Params& p, Row& row, const Segment<Item>& seg, int r) {
+    const Item& x = seg.item;
+    const int rr = seg.q_row + r, gq = rr / p.T;
     row.t = rr - gq * p.T;
     row.head = x.hk * p.group + gq;
     const bool live = rr < p.rows && row.t < x.count;
@@ -201,8 +204,9 @@ struct CacheSource {
     row.tree = live && p.tree ? p.tree + token * p.words : nullptr;
     return live;
   }
+  template <int BN>
   static __device__ void prefetch(const Params&, Row&, const Item&, int, int) {}
-  static __device__ bool partial(const Item& x, int t) { return (x.t0 + t + 1) * 128 > x.ctx; }  // it has drafted keys
+  static __device__ bool partial(const Item& x, int t) { return (x.t0 + t + 1) * x.tile > x.ctx; }  // it has drafted keys
   // Bits of drafted tokens 32 x .. 32 x + 31 that the row sees.
   static __device__ uint32_t seen(const Params& p, const Row& row, const Item& x, int word) {
     if (32 * word >= x.count) return 0u;
@@ -214,10 +218,11 @@ struct CacheSource {
     const int left = x.count - 32 * word;
     return left >= 32 ? bits : bits & ((1u << left) - 1u);
   }
-  static __device__ void bits(const Params& p, const Row& row, const Item& x, int t, uint32_t (&out)[4]) {
+  template <int BN>
+  static __device__ void bits(const Params& p, const Row& row, const Item& x, int t, uint32_t (&out)[BN / 32]) {
 #pragma unroll
-    for (int cc = 0; cc < 4; ++cc) {
-      const int u0 = (x.t0 + t) * 128 + 32 * cc - x.ctx;  // drafted token of the chunk's first key
+    for (int cc = 0; cc < BN / 32; ++cc) {
+      const int u0 = (x.t0 + t) * BN + 32 * cc - x.ctx;  // drafted token of the chunk's first key
       if (u0 <= -32)
         out[cc] = ~0u;
       else if (u0 < 0)
@@ -226,14 +231,15 @@ struct CacheSource {
         out[cc] = __funnelshift_r(seen(p, row, x, u0 >> 5), seen(p, row, x, (u0 >> 5) + 1), u0 & 31);
     }
   }
-  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, uint32_t (&sr)[4][32], float c,
+  template <int CHUNKS>
+  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, uint32_t (&sr)[CHUNKS][32], float c,
                                float slope) {
-    const int j0 = (x.t0 + t) * 128;
+    const int j0 = (x.t0 + t) * CHUNKS * 32;
     const long long rel = static_cast<long long>(row.pos) - j0;
     if (p.positions && partial(x, t)) {
-      float at[4];  // position of key 32 i + lane of the tile
+      float at[CHUNKS];  // position of key 32 i + lane of the tile
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < CHUNKS; ++i) {
         const int key = 32 * i + static_cast<int>(threadIdx.x & 31), u = j0 + key - x.ctx;
         long long pos = key;
         if (u >= 0) pos = u < x.count ? static_cast<long long>(__ldg(p.positions + static_cast<size_t>(x.b) * p.T + u)) - j0 : 0;
@@ -241,11 +247,10 @@ struct CacheSource {
       }
       lower_by_positions(sr, c, slope, static_cast<float>(rel), at);
     } else {
-      lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= 127));
+      lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= CHUNKS * 32 - 1));
     }
   }
   static __device__ bool whole(const Item& x) { return x.whole; }
-  static __device__ size_t out_row(const Params&, const Row& row, const Item&) { return row.out; }
   // A segment that begins its item goes on in a later share: slot 2 w + 1 of
   // worker w; one that does not: slot 2 w.
   static __device__ size_t slot_row(const Params& p, const Item& x, int g, int r) {
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) combine_kernel(const __grid_
   const int all = p.line[p.B], line = p.line[b];
   int ctx, count;
   if (!request(p, b, ctx, count)) return;
-  const int len = ((ctx + count + 127) >> 7) + kItemCost, share = share_of(all), at = line + item * len;
+  const int len = tiles_of(p, ctx + count) + kItemCost, share = share_of(all), at = line + item * len;
   const int w0 = (at + kItemCost) / share, w1 = (at + len - 1) / share;  // workers of its first and last tile
   if (w0 == w1) return;                                                  // finished by its one worker
   const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
@@ -354,8 +359,8 @@ template <int D, bool BF16>
 stof_status launch_tree(const void* q, const void* k, const void* v, const TreeParams& p, int mode, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   const uint64_t planes = static_cast<uint64_t>(p.B) * p.Hkv;
-  if (!make_bw_map(&mq, q, planes, p.rows, D, kBM, BF16) || !make_bw_map(&mk, k, planes, p.cap, D, 128, BF16) ||
-      !make_bw_map(&mv, v, planes, p.cap, D, 128, BF16))
+  if (!make_bw_map(&mq, q, planes, p.rows, D, kBM, BF16) || !make_bw_map(&mk, k, planes, p.cap, D, Shape<D>::BN, BF16) ||
+      !make_bw_map(&mv, v, planes, p.cap, D, Shape<D>::BN, BF16))
     return STOF_ERR_CUDA;
   stof_status st;
   switch (mode) {
@@ -394,7 +399,7 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   const long long rows = static_cast<long long>(H / Hkv) * T, row_tiles = (rows + 127) / 128;
   // the line of the call's tiles and its query rows are counted in 32 bits
   if (static_cast<long long>(B) * H * T >= (1ll << 31) || static_cast<long long>(B) * Hkv >= (1ll << 31) ||
-      static_cast<long double>(B) * Hkv * row_tiles * ((static_cast<long long>(cap) + 127) / 128 + kItemCost) >= 2147480000.0L)
+      static_cast<long double>(B) * Hkv * row_tiles * ((static_cast<long long>(cap) + 63) / 64 + kItemCost) >= 2147480000.0L)
     return STOF_ERR_SHAPE;
   if (score) {
     stof_score s = *score;
@@ -421,6 +426,7 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   p.T = T;
   p.d = d;
   p.cap = cap;
+  p.tile = d == 64 ? Shape<64>::BN : Shape<128>::BN;
   p.words = (T + 31) / 32;
   p.rows = static_cast<int>(rows);
   p.row_tiles = static_cast<int>(row_tiles);
