@@ -135,10 +135,10 @@ __device__ __forceinline__ void classify(const uint64_t* words, const ChunkGeom&
   }
 }
 
-// Phase 3 (one warp): ranks inside the chunk and the chained prefix sum.
-__device__ __forceinline__ void rank_and_lookback(const EncodeParams& p, long long chunk, const ChunkGeom& g,
-                                                  ChunkState& cs, int lane) {
-  int nf = 0, np = 0;
+// Ranks of the chunk's listed OTs among its full and partial ones, and their
+// numbers (one warp).
+__device__ __forceinline__ void rank_tiles(const ChunkGeom& g, ChunkState& cs, int lane, int& nf, int& np) {
+  nf = np = 0;
   for (int t0 = 0; t0 < g.nt; t0 += 32) {
     const int t = t0 + lane;
     const int cls = t < g.nt ? cs.cls[t] : 0;
@@ -154,6 +154,13 @@ __device__ __forceinline__ void rank_and_lookback(const EncodeParams& p, long lo
     nf += __popc(bf);
     np += __popc(bp);
   }
+}
+
+// Phase 3 (one warp): ranks inside the chunk and the chained prefix sum.
+__device__ __forceinline__ void rank_and_lookback(const EncodeParams& p, long long chunk, const ChunkGeom& g,
+                                                  ChunkState& cs, int lane) {
+  int nf, np;
+  rank_tiles(g, cs, lane, nf, np);
   const unsigned long long agg = (static_cast<unsigned long long>(nf) << 31) | static_cast<unsigned long long>(np);
   unsigned long long excl = 0;
   if (chunk == 0) {
@@ -495,20 +502,9 @@ __device__ __forceinline__ int4 group_summary(const int* doc, const int* ord) {
   return make_int4(d, lo, hi, 0);
 }
 
-__global__ void __launch_bounds__(kThreads) encode_documents_kernel(const EncodeParams p, const DocSet ds) {
-  extern __shared__ uint64_t s_words[];  // [bm/8][nt * bn/8]
-  __shared__ long long s_chunk;
-  __shared__ ChunkState cs;
-  __shared__ DocChunk dc;
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    s_chunk = static_cast<long long>(atomicAdd(p.ticket, 1ull));
-    cs.nnz = 0;
-  }
-  __syncthreads();
-  const long long chunk = s_chunk;
-  if (chunk >= p.n_chunks) return;
-  const ChunkGeom g = chunk_geom(p, chunk);
+// The chunk's IT words; returns this thread's valid elements.
+__device__ __forceinline__ unsigned long long document_words(const EncodeParams& p, const DocSet& ds, const ChunkGeom& g,
+                                                             DocChunk& dc, uint64_t* words, int tid) {
   const int i0 = g.I * p.bm, j0 = g.J0 * p.bn, cols = g.itcols * 8;
   const int32_t* qd = ds.q_doc + static_cast<long long>(g.m) * p.lq;
   const int32_t* kd = ds.k_doc + static_cast<long long>(g.m) * p.lk;
@@ -536,7 +532,7 @@ __global__ void __launch_bounds__(kThreads) encode_documents_kernel(const Encode
       dc.k_sum[e - g.bands] = group_summary(dc.k_doc + 8 * (e - g.bands), dc.k_ord + 8 * (e - g.bands));
   }
   __syncthreads();
-  unsigned long long local_nnz = 0;
+  unsigned long long nnz = 0;
   const int nw = g.bands * g.itcols;
   for (int w = tid; w < nw; w += kThreads) {
     const int pb = w / g.itcols, qc = w - pb * g.itcols;
@@ -562,10 +558,120 @@ __global__ void __launch_bounds__(kThreads) encode_documents_kernel(const Encode
         word |= static_cast<uint64_t>(bits) << (8 * r);
       }
     }
-    s_words[w] = word;
-    local_nnz += __popcll(word);
+    words[w] = word;
+    nnz += __popcll(word);
   }
+  return nnz;
+}
+
+// Single-pass encoder (many chunks): offsets by look-back, as for the other sources.
+__global__ void __launch_bounds__(kThreads) encode_documents_kernel(const EncodeParams p, const DocSet ds) {
+  extern __shared__ uint64_t s_words[];  // [bm/8][nt * bn/8]
+  __shared__ long long s_chunk;
+  __shared__ ChunkState cs;
+  __shared__ DocChunk dc;
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    s_chunk = static_cast<long long>(atomicAdd(p.ticket, 1ull));
+    cs.nnz = 0;
+  }
+  __syncthreads();
+  const long long chunk = s_chunk;
+  if (chunk >= p.n_chunks) return;
+  const ChunkGeom g = chunk_geom(p, chunk);
+  const unsigned long long local_nnz = document_words(p, ds, g, dc, s_words, tid);
   finish_chunk(p, chunk, g, cs, s_words, local_nnz, tid);
+}
+
+// Up to kDirectChunks chunks: two kernels of the same grid, neither waiting
+// on a CTA of its own.  The first leaves each chunk's counts in its status
+// word, the second adds up the words before its chunk and writes.  Their
+// words are computed in both, the second's while the first still runs
+// (programmatic dependent launch), and no memory has to be cleared first.
+constexpr int kDirectChunks = 4096;
+
+// valid elements (2^18 at most) | full OTs | partial OTs of a chunk
+__device__ __forceinline__ unsigned long long pack_counts(unsigned long long nnz, int nf, int np) {
+  return nnz << 32 | static_cast<unsigned long long>(nf) << 16 | static_cast<unsigned long long>(np);
+}
+
+__global__ void __launch_bounds__(kThreads) documents_count_kernel(const EncodeParams p, const DocSet ds) {
+  extern __shared__ uint64_t s_words[];
+  __shared__ ChunkState cs;
+  __shared__ DocChunk dc;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long chunk = blockIdx.x;
+  if (tid == 0) cs.nnz = 0;
+  if (chunk == 0 && tid < 8) p.counts[tid] = 0;  // the workspace's header: counts, error word, the attention kernel's counters
+  const ChunkGeom g = chunk_geom(p, chunk);
+  unsigned long long nnz = document_words(p, ds, g, dc, s_words, tid);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) nnz += __shfl_xor_sync(0xffffffffu, nnz, off);
+  if (lane == 0 && nnz) atomicAdd(&cs.nnz, nnz);
+  __syncthreads();
+  classify(s_words, g, cs, warp, lane, kThreads / 32);
+  __syncthreads();
+  if (warp == 0) {
+    int nf = 0, np = 0;
+    for (int t = lane; t < g.nt; t += 32) {
+      nf += cs.cls[t] == 1;
+      np += cs.cls[t] == 2;
+    }
+    nf = __reduce_add_sync(0xffffffffu, nf);
+    np = __reduce_add_sync(0xffffffffu, np);
+    if (lane == 0) p.status[chunk] = pack_counts(cs.nnz, nf, np);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) documents_write_kernel(const EncodeParams p, const DocSet ds) {
+  extern __shared__ uint64_t s_words[];
+  __shared__ ChunkState cs;
+  __shared__ DocChunk dc;
+  __shared__ unsigned long long s_before[kThreads / 32], s_nnz[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long chunk = blockIdx.x;
+  const ChunkGeom g = chunk_geom(p, chunk);
+  document_words(p, ds, g, dc, s_words, tid);
+  __syncthreads();
+  classify(s_words, g, cs, warp, lane, kThreads / 32);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel has ended
+  // full << 31 | partial OTs before the chunk; the last chunk also adds up all valid elements
+  const bool last = chunk == p.n_chunks - 1;
+  unsigned long long before = 0, nnz = 0;
+  for (long long c = tid; c < chunk + (last ? 1 : 0); c += kThreads) {
+    const unsigned long long v = __ldcg(p.status + c);
+    if (c < chunk) before += (v >> 16 & 0xFFFFull) << 31 | (v & 0xFFFFull);
+    nnz += v >> 32;
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+    nnz += __shfl_xor_sync(0xffffffffu, nnz, off);
+  }
+  if (lane == 0) {
+    s_before[warp] = before;
+    s_nnz[warp] = nnz;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    unsigned long long excl = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      excl += s_before[w];
+      all += s_nnz[w];
+    }
+    int nf, np;
+    rank_tiles(g, cs, lane, nf, np);
+    if (lane == 0) {
+      cs.excl = excl;
+      cs.nf = nf;
+      cs.np = np;
+      if (last) p.counts[2] = static_cast<int64_t>(all);
+    }
+  }
+  __syncthreads();
+  write_outputs(p, chunk, s_words, g, cs, tid, kThreads);
 }
 
 // ---------------------------------------------------------------- bit-packed masks
@@ -904,10 +1010,28 @@ cudaError_t launch_encode_rules(const EncodeParams& p_in, const EncodeGeom& g, c
   return cudaGetLastError();
 }
 
+bool documents_direct(const EncodeGeom& g) { return g.n_chunks <= kDirectChunks; }
+
 cudaError_t launch_encode_documents(const EncodeParams& p_in, const EncodeGeom& g, const DocSet& ds, cudaStream_t s) {
   const EncodeParams p = with_reciprocals(p_in);
-  encode_documents_kernel<<<static_cast<unsigned>(g.n_chunks), kThreads, g.smem_bytes, s>>>(p, ds);
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>(g.n_chunks);
+  if (!documents_direct(g)) {
+    encode_documents_kernel<<<grid, kThreads, g.smem_bytes, s>>>(p, ds);
+    return cudaGetLastError();
+  }
+  documents_count_kernel<<<grid, kThreads, g.smem_bytes, s>>>(p, ds);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = g.smem_bytes;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, documents_write_kernel, p, ds);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // ------------------------------------------------------------------------

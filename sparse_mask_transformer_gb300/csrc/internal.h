@@ -91,6 +91,8 @@ struct DocSet {
   const int32_t* k_order;
 };
 cudaError_t launch_encode_documents(const EncodeParams& p, const EncodeGeom& g, const DocSet& ds, cudaStream_t s);
+// Whether that launch needs nothing cleared beforehand.
+bool documents_direct(const EncodeGeom& g);
 
 // Scratch of stof_encode_mask_noalloc(): a static device array with room
 // for the ticket and kNoAllocMaxChunks look-back words.  The address is

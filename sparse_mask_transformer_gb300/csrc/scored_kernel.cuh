@@ -52,9 +52,11 @@ namespace scored {
 using namespace ptx;
 using namespace bw;
 
-// What becomes of the products: MODE_PLAIN scale > 0 only; MODE_CAP a cap
-// only; MODE_DISTANCE distance, with or without a cap, and any scale.
+// What becomes of the products: MODE_PLAIN scale > 0 only; MODE_CAP a cap of
+// at most kMaxCapOnly only; MODE_DISTANCE anything.
 constexpr int MODE_PLAIN = 0, MODE_CAP = 1, MODE_DISTANCE = 2;
+// 60 log2 e = 87: sums of 2^31 keys of 2^87 times |V| below 2^8 stay in fp32.
+constexpr float kMaxCapOnly = 60.f;
 
 struct CommonParams {
   ScoreConst k;
@@ -405,6 +407,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (partial) mask_scores(sr, bits);
             const float nmu = raise_ref(row_max(sr) * p.k.c);
             l += exp_pack<CHUNKS, BF16>(sr, p.k.c, nmu, pk);
+          } else if constexpr (MODE == MODE_CAP && BF16) {
+            // Capped scores lie within a of 0 (log2 units; the host sends a
+            // larger cap to MODE_DISTANCE), and bf16 and fp32 hold 2^-a to
+            // 2^a: no running max, the reference is 0 throughout.
+            m_ref = 0.f;
+            bool within = true;
+            if (CHUNKS > 2 || partial) within = __all_sync(0xffffffffu, row_within(sr, p.k.lim));
+            if (!partial && CHUNKS > 2 && within) {
+              l += exp_pack_capped<CHUNKS, BF16>(sr, p.k, 0.f, pk);
+            } else if (!partial && CHUNKS == 2) {
+              // the polynomial for all, while its range is being checked (the
+              // scores stay: registers for 64 of them, not for 128)
+              const float sum = exp_pack_capped<CHUNKS, BF16>(sr, p.k, 0.f, pk);
+              if (__all_sync(0xffffffffu, row_within(sr, p.k.lim))) {
+                l += sum;
+              } else {
+                cap_scores(sr, p.k, false);
+                l += exp_pack<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
+              }
+            } else {
+              cap_scores(sr, p.k, within);
+              if (partial) mask_scores(sr, bits);
+              l += exp_pack<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
+            }
           } else if constexpr (MODE == MODE_CAP) {
             const bool within = __all_sync(0xffffffffu, row_within(sr, p.k.lim));
             if (within && !partial && p.k.k1 > 0.f) {
@@ -520,7 +546,7 @@ stof_status launch_scored(const CUtensorMap& mq, const CUtensorMap& mk, const CU
 
 // The mode a call's score options need.
 inline int mode_of(float scale, float softcap, bool slopes) {
-  if (slopes || (softcap <= 0.f && !(scale > 0.f))) return MODE_DISTANCE;
+  if (slopes || softcap > kMaxCapOnly || (softcap <= 0.f && !(scale > 0.f))) return MODE_DISTANCE;
   return softcap > 0.f ? MODE_CAP : MODE_PLAIN;
 }
 

@@ -128,7 +128,8 @@ static stof_status encode_impl(const uint8_t* mask, int bits, const RuleSet* rul
 
   cudaStream_t s = as_stream(stream);
   // counts, ticket and look-back state start at zero
-  if (record_cuda(cudaMemsetAsync(ws + w.counts, 0, w.zero_bytes, s)) != cudaSuccess) return STOF_ERR_CUDA;
+  if (!(docs && documents_direct(g)) &&
+      record_cuda(cudaMemsetAsync(ws + w.counts, 0, w.zero_bytes, s)) != cudaSuccess) return STOF_ERR_CUDA;
   EncodeParams p;
   p.mask = mask;
   p.bits = bits;

@@ -202,7 +202,7 @@ def load_library(path: str = LIB_PATH):
         lib.stof_rope_plan_custom.argtypes = [ctypes.POINTER(stof_rope_plan), i32, i32, ctypes.POINTER(ctypes.c_double),
                                               ctypes.c_double]
         lib.stof_rope_plan_custom.restype = i32
-        R = ctypes.POINTER(stof_rows)
+        R = P  # stof_rows
         lib.stof_rope_fwd.argtypes = [ctypes.POINTER(stof_rope_plan), R, R, R, i32, i32, i32, i32, i32, i32, P, P, P, i32,
                                       R, R, R, P, P]
         lib.stof_rope_fwd.restype = i32
@@ -335,15 +335,15 @@ def stof_encode_documents(q_doc: torch.Tensor, k_doc: torch.Tensor, q_order: tor
     """q_doc, q_order: int32 [n_masks, lq]; k_doc, k_order: int32 [n_masks, lk] (orders both None: no order).
     Query i sees key j iff q_doc[i] == k_doc[j] >= 0 and k_order[j] <= q_order[i]."""
     where = "stof_encode_documents"
-    device = _device_of(where, dict(q_doc=q_doc, k_doc=k_doc, q_order=q_order, k_order=k_order, workspace=workspace))
+    device = _device_of(where, q_doc, k_doc, q_order, k_order, workspace)
     if q_doc.dim() != 2 or k_doc.dim() != 2 or q_doc.shape[0] != k_doc.shape[0]:
         raise StofError(STOF_ERR_SHAPE, f"{where}: q_doc must be [n_masks, lq] and k_doc [n_masks, lk]")
     (n, lq), (_, lk) = q_doc.shape, k_doc.shape
     fmt = fmt if fmt is not None else stof_format()
-    args = (_int32(where, "q_doc", q_doc, (n, lq)), _int32(where, "k_doc", k_doc, (n, lk)),
-            _int32(where, "q_order", q_order, (n, lq)), _int32(where, "k_order", k_order, (n, lk)), n, lq, lk, bm, bn,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), ctypes.byref(fmt))
-    _launch(device, stream, where, lambda s: load_library().stof_encode_documents(*args, s))
+    _launch(where, device, stream, load_library().stof_encode_documents, _int32(where, "q_doc", q_doc, (n, lq)),
+            _int32(where, "k_doc", k_doc, (n, lk)), _int32(where, "q_order", q_order, (n, lq)),
+            _int32(where, "k_order", k_order, (n, lk)), n, lq, lk, bm, bn, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), ctypes.byref(fmt))
     return fmt
 
 
@@ -431,7 +431,7 @@ def stof_mha_fwd_score(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, fmt: s
     """q, o: device [B, H, Lq, d]; k, v: device [B, Hkv, Lk, d], H a multiple of Hkv; fp16/bf16, contiguous.
     STOF_KERNEL_AUTO needs no synced format here."""
     where = "stof_mha_fwd_score"
-    device = _device_of(where, dict(q=q, k=k, v=v, o=o, slopes=score.slopes if score is not None else None))
+    device = _device_of(where, q, k, v, o, score.slopes if score is not None else None)
     if q.dim() != 4 or k.dim() != 4:
         raise StofError(STOF_ERR_SHAPE, f"{where}: q, k must be [B, heads, L, d]")
     B, H, Lq, d = q.shape
@@ -439,10 +439,9 @@ def stof_mha_fwd_score(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, fmt: s
     if (o.shape != q.shape or k.shape != (B, Hkv, Lk, d) or v.shape != k.shape
             or any(t.dtype != q.dtype or not t.is_contiguous() for t in (q, k, v, o))):
         raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, Lq, d] and k, v [B, Hkv, Lk, d], contiguous")
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Hkv, Lq, Lk, d, float(scale),
-            None if score is None else ctypes.byref(score.as_c(where, H)), ctypes.byref(fmt), int(mask_stride_b),
-            int(mask_stride_h), int(which), o.data_ptr())
-    _launch(device, stream, where, lambda s: load_library().stof_mha_fwd_score(*args, s))
+    _launch(where, device, stream, load_library().stof_mha_fwd_score, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            _dtype_code(q), B, H, Hkv, Lq, Lk, d, float(scale), None if score is None else ctypes.byref(score.as_c(where, H)),
+            ctypes.byref(fmt), mask_stride_b, mask_stride_h, which, o.data_ptr())
     return o
 
 
@@ -458,8 +457,7 @@ def stof_tree_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens: 
     [B, T, ceil(T / 32)] ancestor bits (None: token t sees drafted tokens 0..t); positions: int32 [B, T]."""
     where = "stof_tree_attn_fwd"
     slopes = score.slopes if score is not None else None
-    device = _device_of(where, dict(q=q, k=k, v=v, o=o, lens=lens, workspace=workspace, tree=tree, counts=counts,
-                                    positions=positions, slopes=slopes, device_error=device_error))
+    device = _device_of(where, q, k, v, o, lens, workspace, tree, counts, positions, slopes, device_error)
     if q.dim() != 4 or k.dim() != 4:
         raise StofError(STOF_ERR_SHAPE, f"{where}: q, k must be [B, heads, rows, d]")
     B, H, T, d = q.shape
@@ -467,12 +465,11 @@ def stof_tree_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens: 
     if (o.shape != q.shape or k.shape != (B, Hkv, cap, d) or v.shape != k.shape
             or any(t.dtype != q.dtype or not t.is_contiguous() for t in (q, k, v, o))):
         raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, T, d] and k, v [B, Hkv, cap, d], contiguous")
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), B, H, Hkv, T, d, cap,
-            _int32(where, "lens", lens, (B,)), _int32(where, "counts", counts, (B,)),
-            _int32(where, "tree", tree, (B, T, (T + 31) // 32)), _int32(where, "positions", positions, (B, T)),
-            float(scale), None if score is None else ctypes.byref(score.as_c(where, H)), o.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _error_word(where, device_error))
-    _launch(device, stream, where, lambda s: load_library().stof_tree_attn_fwd(*args, s))
+    _launch(where, device, stream, load_library().stof_tree_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            _dtype_code(q), B, H, Hkv, T, d, cap, _int32(where, "lens", lens, (B,)), _int32(where, "counts", counts, (B,)),
+            _int32(where, "tree", tree, (B, T, (T + 31) // 32)), _int32(where, "positions", positions, (B, T)), float(scale),
+            None if score is None else ctypes.byref(score.as_c(where, H)), o.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _error_word(where, device_error))
     return o
 
 
@@ -622,32 +619,40 @@ def stof_oproj_ln_fwd(o: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | Non
     return y
 
 
-def _device_of(where: str, tensors: dict) -> torch.device:
-    """The one CUDA device all the given tensors (None: absent) are on."""
-    device = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise StofError(STOF_ERR_INVALID_ARG, f"{where}: {name} must be a CUDA tensor")
-        if device is not None and t.device != device:
-            raise StofError(STOF_ERR_INVALID_ARG, f"{where}: {name} is on another device")
-        device = t.device
-    if device is None:
+def _device_of(where: str, *tensors) -> int:
+    """Index of the one CUDA device all the given tensors (None: absent) are on."""
+    device = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise StofError(STOF_ERR_INVALID_ARG, f"{where}: every tensor must be on a CUDA device")
+            if device >= 0 and d != device:
+                raise StofError(STOF_ERR_INVALID_ARG, f"{where}: the tensors are on different devices")
+            device = d
+    if device < 0:
         raise StofError(STOF_ERR_INVALID_ARG, f"{where}: no tensor given")
     return device
 
 
-def _launch(device: torch.device, stream, where: str, call) -> None:
-    """call(stream pointer) with `device` current, on `stream` or that device's current stream."""
-    with torch.cuda.device(device):
-        _check(call(_stream(torch.cuda.current_stream(device) if stream is None else stream)), where)
+def _launch(where: str, device: int, stream, function, *args) -> None:
+    """function(*args, stream pointer) with `device` current, on `stream` or that device's current stream.
+    (The raw-stream call spares building a Stream object, and the device guard is entered only for another
+    device: a decoding step's calls are short enough for either to show.)"""
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == device:
+        status = function(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = function(*args, s)
+    if status != STOF_OK:
+        raise StofError(status, where)
 
 
 def _int32(where: str, name: str, t: torch.Tensor | None, shape: tuple) -> int | None:
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise StofError(STOF_ERR_SHAPE, f"{where}: {name} must be contiguous int32 {list(shape)}")
     return t.data_ptr()
 
@@ -682,43 +687,55 @@ def stof_rope_plan_custom(frequencies, interleaved: bool = False, amplitude: flo
     return plan
 
 
+_RowsArray = ctypes.c_int64 * 24  # six stof_rows
+
+
 def _rope(where, plan, x, y, positions, counts, rows, device_error, stream):
     """x, y: (q, k, v) and their outputs, [B, heads, T, d] with contiguous rows of d, any other strides."""
-    named = dict(zip(("q", "k", "v", "q_out", "k_out", "v_out"), (*x, *y)))
-    device = _device_of(where, {**named, "positions": positions, "counts": counts, "rows": rows,
-                                "device_error": device_error})
-    given = [t for t in x if t is not None]
-    if not given:
-        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: give q or k")
-    for name, t in named.items():
-        if t is not None and (t.dim() != 4 or t.dtype != given[0].dtype or (t.shape[3] > 1 and t.stride(3) != 1)):
-            raise StofError(STOF_ERR_SHAPE, f"{where}: {name} must be [B, heads, T, d], rows contiguous, of one dtype")
     q, k, v = x
-    B, _, T, d = given[0].shape
-    for a, out in zip(x, y):
-        if (a is None) != (out is None):
-            raise StofError(STOF_ERR_INVALID_ARG, f"{where}: an input needs its output")
-        if a is not None and (tuple(a.shape) != (B, a.shape[1], T, d) or (B, a.shape[1], d) != (out.shape[0], out.shape[1],
-                                                                                                out.shape[3])):
+    lead = q if q is not None else k
+    if lead is None:
+        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: give q or k")
+    device = _device_of(where, *x, *y, positions, counts, rows, device_error)
+    if lead.dim() != 4:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: tensors must be [B, heads, T, d]")
+    B, _, T, d = lead.shape
+    dtype, kv_rows, heads = lead.dtype, T, [0, 0, 0]
+    fields, given = [], []
+    for i in range(3):
+        a, out = x[i], y[i]
+        if a is None or out is None:
+            if a is not out:
+                raise StofError(STOF_ERR_INVALID_ARG, f"{where}: an input needs its output, and an output its input")
+            continue
+        if a.dim() != 4 or out.dim() != 4 or a.dtype != dtype or out.dtype != dtype:
+            raise StofError(STOF_ERR_SHAPE, f"{where}: tensors must be [B, heads, T, d] of one dtype")
+        sa, so, (n, h, m, w) = a.stride(), out.stride(), out.shape
+        if a.shape != (B, h, T, d) or n != B or w != d or m < T and (i == 0 or rows is None):
             raise StofError(STOF_ERR_SHAPE, f"{where}: shapes differ")
-    if v is not None and (k is None or v.shape != k.shape or y[2].shape != y[1].shape):
-        raise StofError(STOF_ERR_SHAPE, f"{where}: v goes with a k of its shape")
-    if q is not None and y[0].shape[2] != T:
-        raise StofError(STOF_ERR_SHAPE, f"{where}: q_out must have q's shape")
-    kv_rows = T if k is None else y[1].shape[2]
-    if rows is None and kv_rows < T:
-        raise StofError(STOF_ERR_SHAPE, f"{where}: k_out has fewer rows than k")
-    c = [None if t is None else ctypes.byref(stof_rows(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
-         for t in (*x, *y)]
-    head = (ctypes.byref(plan), *c[:3], _dtype_code(given[0]), B, 0 if q is None else q.shape[1],
-            0 if k is None else k.shape[1], T, d, _int32(where, "positions", positions, (B, T)),
-            _int32(where, "counts", counts, (B,)))
+        if i == 0 and m != T:
+            raise StofError(STOF_ERR_SHAPE, f"{where}: q_out must have q's shape")
+        if d > 1 and (sa[3] != 1 or so[3] != 1):
+            raise StofError(STOF_ERR_SHAPE, f"{where}: a row's elements must be contiguous")
+        heads[i] = h
+        if i == 1:
+            kv_rows = m
+        elif i == 2 and (k is None or h != heads[1] or m != kv_rows):
+            raise StofError(STOF_ERR_SHAPE, f"{where}: v goes with a k of its shape")
+        given.append(i)
+        fields += (a.data_ptr(), sa[0], sa[1], sa[2], out.data_ptr(), so[0], so[1], so[2])
+    c = _RowsArray(*fields)
+    base, at = ctypes.addressof(c), [None] * 6
+    for place, i in enumerate(given):
+        at[i], at[3 + i] = base + 64 * place, base + 64 * place + 32
+    head = (ctypes.byref(plan), at[0], at[1], at[2], _dtype_code(lead), B, heads[0], heads[1], T, d,
+            _int32(where, "positions", positions, (B, T)), _int32(where, "counts", counts, (B,)))
     lib = load_library()
     if where == "stof_rope_bwd":
-        _launch(device, stream, where, lambda s: lib.stof_rope_bwd(*head, *c[3:], s))
+        _launch(where, device, stream, lib.stof_rope_bwd, *head, at[3], at[4], at[5])
     else:
-        args = (*head, _int32(where, "rows", rows, (B,)), kv_rows, *c[3:], _error_word(where, device_error))
-        _launch(device, stream, where, lambda s: lib.stof_rope_fwd(*args, s))
+        _launch(where, device, stream, lib.stof_rope_fwd, *head, _int32(where, "rows", rows, (B,)), kv_rows, at[3], at[4],
+                at[5], _error_word(where, device_error))
     return y
 
 
