@@ -475,49 +475,73 @@ __global__ void __launch_bounds__(kThreads, 7) encode_rules_kernel(const EncodeP
   finish_chunk(p, chunk, g, cs, s_words, local_nnz, tid);
 }
 
-// Phase 1 for a document mask: element (i, j) is valid iff query i and key j
-// are of one document (q_doc[i] == k_doc[j] >= 0) and the key is not later
-// than the query (k_order[j] <= q_order[i]).  The chunk's numbers come to
-// shared memory once; each group of 8 rows or columns is summarised (its one
-// document, if it has one, and its least and greatest order), which settles
-// most ITs of packed documents (other documents: empty; the same document
-// and every key earlier: full) without looking at their 64 elements.
+// Document masks: element (i, j) is valid iff query i and key j are of one
+// document (q_doc[i] == k_doc[j] >= 0) and the key is not later than the query
+// (k_order[j] <= q_order[i]).  The chunk's numbers come to shared memory
+// once; each group of 8 rows or columns, and each OT's rows and columns, are
+// summarised by their least and greatest document and order.  Disjoint ranges
+// of documents, or only later keys, make an OT empty; one common document and
+// only earlier keys make it full.  Only the OTs between (on a document's edge
+// or on the diagonal) get IT words, most of which their groups settle the same
+// way.  (A word per thread over the whole chunk: 17 us a kernel on 8 masks of
+// 2048, the chunk waiting for the warps that had the diagonal.)
 constexpr int kMaxChunkCols = 1024;  // ct * bn at most (encode_geometry)
-constexpr int kMixed = -3;           // a group of several documents
 
-struct DocChunk {
-  int q_doc[256], q_ord[256];
-  int k_doc[kMaxChunkCols], k_ord[kMaxChunkCols];
-  int4 q_sum[256 / 8], k_sum[kMaxChunkCols / 8];  // document or kMixed, least order, greatest order
+struct Extent {  // of documents and orders
+  int dlo, dhi, olo, ohi;
 };
+enum class Settled { empty, full, open };
 
-__device__ __forceinline__ int4 group_summary(const int* doc, const int* ord) {
-  int d = doc[0], lo = ord[0], hi = ord[0];
-#pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    if (doc[e] != d) d = kMixed;
-    lo = min(lo, ord[e]);
-    hi = max(hi, ord[e]);
-  }
-  return make_int4(d, lo, hi, 0);
+__device__ __forceinline__ Settled settle(const Extent& q, const Extent& k) {
+  if (q.dlo > k.dhi || k.dlo > q.dhi || k.olo > q.ohi) return Settled::empty;
+  if (q.dlo == q.dhi && q.dlo == k.dlo && q.dlo == k.dhi && k.ohi <= q.olo) return Settled::full;
+  return Settled::open;
 }
 
-// The chunk's IT words; returns this thread's valid elements.
-__device__ __forceinline__ unsigned long long document_words(const EncodeParams& p, const DocSet& ds, const ChunkGeom& g,
-                                                             DocChunk& dc, uint64_t* words, int tid) {
+struct DocChunk {
+  alignas(16) int q_doc[256], q_ord[256];
+  alignas(16) int k_doc[kMaxChunkCols], k_ord[kMaxChunkCols];
+  Extent q_sum[256 / 8], k_sum[kMaxChunkCols / 8];
+  int open[kMaxTilesPerChunk];  // the OTs that need words
+  int n_open;
+};
+
+__device__ __forceinline__ Extent group_extent(const int* doc, const int* ord) {
+  const int4 d0 = *reinterpret_cast<const int4*>(doc), d1 = *reinterpret_cast<const int4*>(doc + 4);
+  const int4 o0 = *reinterpret_cast<const int4*>(ord), o1 = *reinterpret_cast<const int4*>(ord + 4);
+  return Extent{min(min(min(d0.x, d0.y), min(d0.z, d0.w)), min(min(d1.x, d1.y), min(d1.z, d1.w))),
+                max(max(max(d0.x, d0.y), max(d0.z, d0.w)), max(max(d1.x, d1.y), max(d1.z, d1.w))),
+                min(min(min(o0.x, o0.y), min(o0.z, o0.w)), min(min(o1.x, o1.y), min(o1.z, o1.w))),
+                max(max(max(o0.x, o0.y), max(o0.z, o0.w)), max(max(o1.x, o1.y), max(o1.z, o1.w)))};
+}
+// Extent of n <= 32 groups (a whole warp).
+__device__ __forceinline__ Extent warp_extent(const Extent* sum, int n, int lane) {
+  const Extent e = sum[lane < n ? lane : 0];
+  return Extent{__reduce_min_sync(0xffffffffu, e.dlo), __reduce_max_sync(0xffffffffu, e.dhi),
+                __reduce_min_sync(0xffffffffu, e.olo), __reduce_max_sync(0xffffffffu, e.ohi)};
+}
+
+// The class of every OT of the chunk (cs.cls) and the IT words of those that
+// are neither empty nor full by their extents; the chunk's valid elements in
+// cs.nnz.  All kThreads threads; ends with a barrier.
+__device__ __forceinline__ void document_tiles(const EncodeParams& p, const DocSet& ds, const ChunkGeom& g, DocChunk& dc,
+                                               ChunkState& cs, uint64_t* words, int tid) {
+  const int lane = tid & 31, warp = tid >> 5;
   const int i0 = g.I * p.bm, j0 = g.J0 * p.bn, cols = g.itcols * 8;
   const int32_t* qd = ds.q_doc + static_cast<long long>(g.m) * p.lq;
   const int32_t* kd = ds.k_doc + static_cast<long long>(g.m) * p.lk;
   const int32_t* qo = ds.q_order ? ds.q_order + static_cast<long long>(g.m) * p.lq : nullptr;
   const int32_t* ko = ds.k_order ? ds.k_order + static_cast<long long>(g.m) * p.lk : nullptr;
+  if (tid == 0) cs.nnz = 0;
   // rows and columns past the mask's sides belong to no document (two
-  // different numbers below 0, and an order that is never the earlier)
+  // different numbers below 0)
   for (int r = tid; r < p.bm; r += kThreads) {
     const bool in = i0 + r < p.lq;
     const int d = in ? __ldg(qd + i0 + r) : -1;
     dc.q_doc[r] = d < 0 ? -1 : d;
     dc.q_ord[r] = in && qo ? __ldg(qo + i0 + r) : 0;
   }
+#pragma unroll 4
   for (int c = tid; c < cols; c += kThreads) {
     const bool in = j0 + c < p.lk;
     const int d = in ? __ldg(kd + j0 + c) : -2;
@@ -527,41 +551,80 @@ __device__ __forceinline__ unsigned long long document_words(const EncodeParams&
   __syncthreads();
   for (int e = tid; e < g.bands + g.itcols; e += kThreads) {
     if (e < g.bands)
-      dc.q_sum[e] = group_summary(dc.q_doc + 8 * e, dc.q_ord + 8 * e);
+      dc.q_sum[e] = group_extent(dc.q_doc + 8 * e, dc.q_ord + 8 * e);
     else
-      dc.k_sum[e - g.bands] = group_summary(dc.k_doc + 8 * (e - g.bands), dc.k_ord + 8 * (e - g.bands));
+      dc.k_sum[e - g.bands] = group_extent(dc.k_doc + 8 * (e - g.bands), dc.k_ord + 8 * (e - g.bands));
+  }
+  __syncthreads();
+  const Extent rows = warp_extent(dc.q_sum, g.bands, lane);
+  for (int t = warp; t < g.nt; t += kThreads / 32) {
+    const Settled s = settle(rows, warp_extent(dc.k_sum + t * g.itc, g.itc, lane));
+    if (lane == 0) cs.cls[t] = s == Settled::empty ? 0 : s == Settled::full ? 1 : 3;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0, full = 0;
+    for (int t0 = 0; t0 < g.nt; t0 += 32) {
+      const int cls = t0 + lane < g.nt ? cs.cls[t0 + lane] : 0;
+      const unsigned open = __ballot_sync(0xffffffffu, cls == 3);
+      if (cls == 3) dc.open[n + __popc(open & ((1u << lane) - 1u))] = t0 + lane;
+      n += __popc(open);
+      full += __popc(__ballot_sync(0xffffffffu, cls == 1));
+    }
+    if (lane == 0) {
+      dc.n_open = n;
+      if (full) atomicAdd(&cs.nnz, static_cast<unsigned long long>(full) * p.bm * p.bn);
+    }
   }
   __syncthreads();
   unsigned long long nnz = 0;
-  const int nw = g.bands * g.itcols;
-  for (int w = tid; w < nw; w += kThreads) {
-    const int pb = w / g.itcols, qc = w - pb * g.itcols;
-    const int4 a = dc.q_sum[pb], b = dc.k_sum[qc];
-    uint64_t word = 0;
-    if (a.x != kMixed && b.x != kMixed && (a.x != b.x || b.y > a.z)) {
-      // one document each, and not the same or every key later: empty
-    } else if (a.x != kMixed && a.x == b.x && b.z <= a.y) {
-      word = ~0ull;
-    } else {
-      int kdoc[8], kord[8];
+  // Each open OT's words over the threads.  (One loop over all open OTs'
+  // words, split by reciprocal division, gave every thread the first word when
+  // compiled by nvcc 13.0.88, and the right one with its indices checked.)
+  for (int o = 0; o < dc.n_open; ++o) {
+    const int col0 = dc.open[o] * g.itc;
+    for (int x = tid; x < g.wpt; x += kThreads) {
+      const int pb = x / g.itc, qc = col0 + x - pb * g.itc;
+      const Settled s = settle(dc.q_sum[pb], dc.k_sum[qc]);
+      uint64_t word = s == Settled::full ? ~0ull : 0ull;
+      if (s == Settled::open) {
+        int kdoc[8], kord[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        kdoc[c] = dc.k_doc[8 * qc + c];
-        kord[c] = dc.k_ord[8 * qc + c];
+        for (int c = 0; c < 8; ++c) {
+          kdoc[c] = dc.k_doc[8 * qc + c];
+          kord[c] = dc.k_ord[8 * qc + c];
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int d = dc.q_doc[8 * pb + r], ord = dc.q_ord[8 * pb + r];
+          uint32_t bits = 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) bits |= (kdoc[c] == d && kord[c] <= ord) ? 1u << c : 0u;
+          word |= static_cast<uint64_t>(bits) << (8 * r);
+        }
       }
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int d = dc.q_doc[8 * pb + r], o = dc.q_ord[8 * pb + r];
-        uint32_t bits = 0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) bits |= (kdoc[c] == d && kord[c] <= o) ? 1u << c : 0u;
-        word |= static_cast<uint64_t>(bits) << (8 * r);
-      }
+      words[pb * g.itcols + qc] = word;
+      nnz += __popcll(word);
     }
-    words[w] = word;
-    nnz += __popcll(word);
   }
-  return nnz;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) nnz += __shfl_xor_sync(0xffffffffu, nnz, off);
+  if (lane == 0 && nnz) atomicAdd(&cs.nnz, nnz);
+  __syncthreads();
+  for (int o = warp; o < dc.n_open; o += kThreads / 32) {  // the open OTs' classes, from their words
+    const int t = dc.open[o];
+    uint64_t any = 0, all = ~0ull;
+    for (int e = lane; e < g.wpt; e += 32) {
+      const int pb = e / g.itc;
+      const uint64_t w = words[pb * g.itcols + t * g.itc + e - pb * g.itc];
+      any |= w;
+      all &= w;
+    }
+    any = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any | any >> 32));
+    const uint32_t a = __reduce_and_sync(0xffffffffu, static_cast<uint32_t>(all) & static_cast<uint32_t>(all >> 32));
+    if (lane == 0) cs.cls[t] = any == 0 ? 0 : (a == ~0u ? 1 : 2);
+  }
+  __syncthreads();
 }
 
 // Single-pass encoder (many chunks): offsets by look-back, as for the other sources.
@@ -571,22 +634,21 @@ __global__ void __launch_bounds__(kThreads) encode_documents_kernel(const Encode
   __shared__ ChunkState cs;
   __shared__ DocChunk dc;
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    s_chunk = static_cast<long long>(atomicAdd(p.ticket, 1ull));
-    cs.nnz = 0;
-  }
+  if (tid == 0) s_chunk = static_cast<long long>(atomicAdd(p.ticket, 1ull));
   __syncthreads();
   const long long chunk = s_chunk;
   if (chunk >= p.n_chunks) return;
   const ChunkGeom g = chunk_geom(p, chunk);
-  const unsigned long long local_nnz = document_words(p, ds, g, dc, s_words, tid);
-  finish_chunk(p, chunk, g, cs, s_words, local_nnz, tid);
+  document_tiles(p, ds, g, dc, cs, s_words, tid);
+  if (tid < 32) rank_and_lookback(p, chunk, g, cs, tid);
+  __syncthreads();
+  write_outputs(p, chunk, s_words, g, cs, tid, kThreads);
 }
 
 // Up to kDirectChunks chunks: two kernels of the same grid, neither waiting
 // on a CTA of its own.  The first leaves each chunk's counts in its status
-// word, the second adds up the words before its chunk and writes.  Their
-// words are computed in both, the second's while the first still runs
+// word, the second adds up the words before its chunk and writes.  The OTs
+// are classified in both, in the second while the first still runs
 // (programmatic dependent launch), and no memory has to be cleared first.
 constexpr int kDirectChunks = 4096;
 
@@ -600,27 +662,20 @@ __global__ void __launch_bounds__(kThreads) documents_count_kernel(const EncodeP
   __shared__ ChunkState cs;
   __shared__ DocChunk dc;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const long long chunk = blockIdx.x;
-  if (tid == 0) cs.nnz = 0;
   if (chunk == 0 && tid < 8) p.counts[tid] = 0;  // the workspace's header: counts, error word, the attention kernel's counters
   const ChunkGeom g = chunk_geom(p, chunk);
-  unsigned long long nnz = document_words(p, ds, g, dc, s_words, tid);
-#pragma unroll
-  for (int off = 16; off; off >>= 1) nnz += __shfl_xor_sync(0xffffffffu, nnz, off);
-  if (lane == 0 && nnz) atomicAdd(&cs.nnz, nnz);
-  __syncthreads();
-  classify(s_words, g, cs, warp, lane, kThreads / 32);
-  __syncthreads();
-  if (warp == 0) {
+  document_tiles(p, ds, g, dc, cs, s_words, tid);
+  if (tid < 32) {
     int nf = 0, np = 0;
-    for (int t = lane; t < g.nt; t += 32) {
+    for (int t = tid; t < g.nt; t += 32) {
       nf += cs.cls[t] == 1;
       np += cs.cls[t] == 2;
     }
     nf = __reduce_add_sync(0xffffffffu, nf);
     np = __reduce_add_sync(0xffffffffu, np);
-    if (lane == 0) p.status[chunk] = pack_counts(cs.nnz, nf, np);
+    if (tid == 0) p.status[chunk] = pack_counts(cs.nnz, nf, np);
   }
 }
 
@@ -632,9 +687,7 @@ __global__ void __launch_bounds__(kThreads) documents_write_kernel(const EncodeP
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long chunk = blockIdx.x;
   const ChunkGeom g = chunk_geom(p, chunk);
-  document_words(p, ds, g, dc, s_words, tid);
-  __syncthreads();
-  classify(s_words, g, cs, warp, lane, kThreads / 32);
+  document_tiles(p, ds, g, dc, cs, s_words, tid);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel has ended
   // full << 31 | partial OTs before the chunk; the last chunk also adds up all valid elements
   const bool last = chunk == p.n_chunks - 1;
