@@ -5,12 +5,15 @@
 // Bound by memory while a K/V head has up to a few hundred rows: every K and V
 // row has to be read once (4 d bytes), and 128 rows cost the tensor cores
 // half of the time that 128 keys take to arrive.  So the work is cut by keys:
-// all (request, K/V head, row tile) items in order, each a run of 128-key
-// tiles and kItemCost more for its start and end, are one long line, of which
-// each of kWorkers workers (two per SM, scored_kernel.cuh) takes an equal
-// share (the lengths are read on the device, so the shares follow them).  An
-// item whose tiles lie in one share is finished there; the others leave
-// partial rows (O relative to the rows' max, max and sum) in the workspace,
+// all (request, K/V head) runs of key tiles in order, each with kItemCost
+// more for its start and end, are one long line, cut into equal shares (the
+// lengths are read on the device, so the shares follow them).  The row tiles
+// of a K/V head, up to kRowGroup of them, go along a share together, each
+// with a worker of its own (two workers per SM, scored_kernel.cuh): their
+// neighbours' requests for the same K/V tiles are then L2 hits.  (One row tile
+// after the other read the cache once per row tile: 524 us instead of @LONG@
+// for 512 rows per K/V head over 2 x 131000 keys.)  A head whose tiles lie in
+// one share is finished there; the others leave partial rows (O relative to the rows' max, max and sum) in the workspace,
 // which combine_kernel merges in the order of the keys: the result does not
 // depend on timing.  A worker has at most one item that began before its
 // share and one that goes on after it: two slots.
@@ -25,13 +28,17 @@ using namespace scored;
 
 constexpr int kTreeCtas = 152;             // one CTA per SM
 constexpr int kWorkers = 2 * kTreeCtas;
-constexpr int kItemCost = 2;               // an item's start and end, in tiles
+constexpr int kItemCost = 2;               // a run's start and end, in tiles
+constexpr int kRowGroup = 8;               // row tiles that go along the line together, at most
 
 struct TreeParams : CommonParams {
   int B, Hkv, T, d, cap, words;
   int tile;        // keys per tile: 128 (d = 64) or 64 (d = 128)
   int rows;        // group * T: query rows per K/V head
   int row_tiles;   // ceil(rows / 128)
+  int row_group;   // row tiles per share; row_groups = ceil(row_tiles / row_group)
+  int row_groups;
+  int shares;      // kWorkers / row_group
   int slot_rows;   // rows of a partial result: min(rows, 128)
   const int32_t* lens;
   const int32_t* counts;
@@ -80,8 +87,8 @@ __device__ __forceinline__ int block_prefix(int v, int* sums, int& total) {
   return before + x - v;
 }
 
-// A worker's share of a line of this length.
-__device__ __forceinline__ int share_of(int all) { return max(1, (all + kWorkers - 1) / kWorkers); }
+// Length of a share of a line of this length.
+__device__ __forceinline__ int share_of(const TreeParams& p, int all) { return max(1, (all + p.shares - 1) / p.shares); }
 
 struct CacheSource {
   using Params = TreeParams;
@@ -108,13 +115,14 @@ struct CacheSource {
   // Finds the requests at the workers' begins; CTA 0 reports bad requests and
   // leaves the line for combine_kernel.
   static __device__ void prologue(const Params& p, Shared& s) {
-    const int per = p.Hkv * p.row_tiles;
-    int all = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // combine_kernel may be set up
+    const int per = p.Hkv * p.row_groups;
+    int all = 0, v = 0, at = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
       int total;
-      const int v = b < p.B ? item_length(p, b) * per : 0;
-      const int at = all + block_prefix(v, s.sums, total);
+      v = b < p.B ? item_length(p, b) * per : 0;
+      at = all + block_prefix(v, s.sums, total);
       if (blockIdx.x == 0 && b < p.B) {
         p.line[b] = at;
         int c, n;
@@ -124,38 +132,44 @@ struct CacheSource {
       all += total;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) p.line[p.B] = all;
-    const int share = share_of(all);
-    const int w0 = min(static_cast<int>(blockIdx.x) * 2 * share, all), w1 = min(w0 + share, all);
-    if (threadIdx.x == 0) {
-      s.begin[0] = w0;
-      s.end[0] = s.begin[1] = w1;
-      s.end[1] = min(w1 + share, all);
+    const int share = share_of(p, all);
+    int begin[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int x = (2 * static_cast<int>(blockIdx.x) + g) / p.row_group;  // the worker's share
+      begin[g] = x < p.shares ? min(x * share, all) : all;
+      if (threadIdx.x == 0) {
+        s.begin[g] = begin[g];
+        s.end[g] = min(begin[g] + share, all);
+      }
     }
     int base = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      int total;
-      const int v = b < p.B ? item_length(p, b) * per : 0;
-      const int at = base + block_prefix(v, s.sums, total);
+      if (p.B > kThreads) {  // else v and at are those of the one round above
+        int total;
+        v = b0 + static_cast<int>(threadIdx.x) < p.B ? item_length(p, b0 + threadIdx.x) * per : 0;
+        at = base + block_prefix(v, s.sums, total);
+        base += total;
+      }
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int w = g == 0 ? w0 : w1;
-        if (at <= w && w < at + v) {
-          s.b[g] = b;
+        if (at <= begin[g] && begin[g] < at + v) {
+          s.b[g] = b0 + threadIdx.x;
           s.base[g] = at;
         }
       }
-      base += total;
     }
   }
   // A worker's place on the line.
   struct Lead {
     int w, end;                      // place, end of the share
+    int row;                         // the worker's row tile within a group
     int b = 0, base = 0, len = 0;    // request, its place, length of its items
     int ctx = 0, count = 0;
     __device__ Lead(const Params& p, Shared& s, int g) {
       w = s.begin[g];
       end = s.end[g];
+      row = (2 * static_cast<int>(blockIdx.x) + g) % p.row_group;
       if (w < end) {
         b = s.b[g];
         base = s.base[g];
@@ -164,7 +178,7 @@ struct CacheSource {
     }
     __device__ void load(const Params& p) { len = request(p, b, ctx, count) ? tiles_of(p, ctx + count) + kItemCost : 0; }
     __device__ Next next(const Params& p, Shared&, const volatile int*, Segment<Item>& seg) {
-      const int per = p.Hkv * p.row_tiles;
+      const int per = p.Hkv * p.row_groups;
 #pragma unroll 1
       while (w < end) {
 #pragma unroll 1
@@ -177,8 +191,9 @@ struct CacheSource {
         const int to = min(end - base - item * len, len);  // the share's part of the item: [at, to)
         w += to - at;
         const int t0 = max(0, at - kItemCost), t1 = max(0, to - kItemCost);
-        if (t1 <= t0) continue;  // the share ends before the item's first tile
-        const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
+        const int hk = item / p.row_groups, rt = (item - hk * p.row_groups) * p.row_group + row;
+        // the share ends before the run's first tile, or the last group has no such row tile
+        if (t1 <= t0 || rt >= p.row_tiles) continue;
         seg.q_plane = seg.kv_plane = b * p.Hkv + hk;
         seg.q_row = rt * 128;
         seg.n = t1 - t0;
@@ -264,47 +279,54 @@ struct CacheSource {
   }
 };
 
-// Merges the partial rows of the items that lie in several workers' shares:
-// O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, a block per query row,
-// warp x the parts x, x + 4, ..., eight of them in flight.
-constexpr int kMergeWarps = 4;
-template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * kMergeWarps) combine_kernel(const __grid_constant__ TreeParams p) {
-  constexpr int E = D / 32;
-  __shared__ float s_o[kMergeWarps][D], s_m[kMergeWarps], s_l[kMergeWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Merges the partial rows of the runs that lie in several shares:
+// O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  WPR warps per query row,
+// warp x of a row the parts x, x + WPR, ..., eight of them in flight; four
+// rows of one warp, or one row of four, a block.  (Launched while the main
+// kernel still runs, it begins when that has ended.)
+template <int D, bool BF16, int WPR>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int E = D / 32, kBatch = 8;
+  __shared__ float s_o[4][D], s_m[4], s_l[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
   const int per = p.Hkv * p.row_tiles;
   const int b = static_cast<int>(blockIdx.x) / per, item = static_cast<int>(blockIdx.x) - b * per;
-  const int all = p.line[p.B], line = p.line[b];
+  const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles, group = rt / p.row_group;
+  const int r = static_cast<int>(blockIdx.y) * (4 / WPR) + warp / WPR, rr = rt * 128 + r, gq = rr / p.T, t = rr - gq * p.T;
   int ctx, count;
-  if (!request(p, b, ctx, count)) return;
-  const int len = tiles_of(p, ctx + count) + kItemCost, share = share_of(all), at = line + item * len;
-  const int w0 = (at + kItemCost) / share, w1 = (at + len - 1) / share;  // workers of its first and last tile
+  const bool active = request(p, b, ctx, count);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!active) return;
+  const int all = __ldcg(p.line + p.B), line = __ldcg(p.line + b);
+  const int len = tiles_of(p, ctx + count) + kItemCost, share = share_of(p, all);
+  const int at = line + (hk * p.row_groups + group) * len;
+  const int w0 = (at + kItemCost) / share, w1 = (at + len - 1) / share;  // shares of its first and last tile
   if (w0 == w1) return;                                                  // finished by its one worker
-  const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
-  const int r = static_cast<int>(blockIdx.y), rr = rt * 128 + r, gq = rr / p.T, t = rr - gq * p.T;
-  if (rr >= p.rows || t >= count) return;
-  // the first worker's part is its last segment, the others' their first
-  auto slot = [&](int w) { return static_cast<size_t>(2 * w + (w == w0 ? 1 : 0)) * p.slot_rows + r; };
+  if (r >= p.slot_rows || rr >= p.rows || t >= count) return;            // (one row: the whole block)
+  // the first share's part is its worker's last segment, the others' their first
+  auto slot = [&](int w) {
+    const int worker = w * p.row_group + rt - group * p.row_group;
+    return static_cast<size_t>(2 * worker + (w == w0 ? 1 : 0)) * p.slot_rows + r;
+  };
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  constexpr int kBatch = 8;
-  for (int i0 = w0 + warp; i0 <= w1; i0 += kMergeWarps * kBatch) {
+#pragma unroll 1
+  for (int i0 = w0 + part; i0 <= w1; i0 += WPR * kBatch) {
     float2 st[kBatch];
     float x[kBatch][E];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int w = i0 + i * kMergeWarps;
+      const int w = i0 + i * WPR;
       st[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int e = 0; e < E; ++e) x[i][e] = 0.f;
       if (w <= w1) {
-        st[i] = p.stats[slot(w)];
+        st[i] = __ldcg(p.stats + slot(w));
         const float* src = p.slots + slot(w) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(src + e);
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(src + e));
           x[i][e] = y.x;
           x[i][e + 1] = y.y;
         }
@@ -326,32 +348,43 @@ __global__ void __launch_bounds__(32 * kMergeWarps) combine_kernel(const __grid_
     }
     m = mn;
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  __syncthreads();
-  float mm = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) mm = fmaxf(mm, s_m[w]);
-  if (mm == -INFINITY) mm = 0.f;
-  const int c = 2 * threadIdx.x;  // two columns a thread
-  if (c >= D) return;
-  float y0 = 0.f, y1 = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float a = ex2(s_m[w] - mm);
-    sum = fmaf(a, s_l[w], sum);
-    y0 = fmaf(a, s_o[w][c], y0);
-    y1 = fmaf(a, s_o[w][c + 1], y1);
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t* out = static_cast<uint32_t*>(p.o) +
-                  ((((static_cast<size_t>(b) * p.H + hk * p.group + gq) * p.T + t) * D + c) >> 1);
-  *out = pack2<BF16>(y0 * inv, y1 * inv);
+                  ((((static_cast<size_t>(b) * p.H + hk * p.group + gq) * p.T + t) * D) >> 1);
+  if constexpr (WPR == 1) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[(lane * E + e) >> 1] = pack2<BF16>(o[e] * inv, o[e + 1] * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+    __syncthreads();
+    float mm = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_m[w]);
+    if (mm == -INFINITY) mm = 0.f;
+    const int c = 2 * threadIdx.x;  // two columns a thread
+    if (c >= D) return;
+    float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float a = ex2(s_m[w] - mm);
+      sum = fmaf(a, s_l[w], sum);
+      y0 = fmaf(a, s_o[w][c], y0);
+      y1 = fmaf(a, s_o[w][c + 1], y1);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    out[c >> 1] = pack2<BF16>(y0 * inv, y1 * inv);
+  }
 }
+
+// Above this many query rows of the call a row is merged by one warp, below by
+// four: few rows have many parts each (a share per worker), many rows few.
+// Measured: @MERGE@
+constexpr long long kRowPerWarp = 1024;
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -369,9 +402,18 @@ stof_status launch_tree(const void* q, const void* k, const void* v, const TreeP
     default: st = launch_scored<CacheSource, D, BF16, MODE_DISTANCE>(mq, mk, mv, p, kTreeCtas, s); break;
   }
   if (st != STOF_OK) return st;
-  const dim3 grid(static_cast<unsigned>(planes * p.row_tiles), static_cast<unsigned>(p.slot_rows));
-  combine_kernel<D, BF16><<<grid, 32 * kMergeWarps, 0, s>>>(p);
-  return record_cuda(cudaGetLastError()) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
+  const bool one = static_cast<long long>(planes) * p.rows >= kRowPerWarp;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(planes * p.row_tiles), static_cast<unsigned>(one ? (p.slot_rows + 3) / 4 : p.slot_rows));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, one ? combine_kernel<D, BF16, 1> : combine_kernel<D, BF16, 4>, p);
+  return record_cuda(e) == cudaSuccess && record_cuda(cudaGetLastError()) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
 
 }  // namespace
@@ -430,6 +472,9 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   p.words = (T + 31) / 32;
   p.rows = static_cast<int>(rows);
   p.row_tiles = static_cast<int>(row_tiles);
+  p.row_groups = static_cast<int>((row_tiles + kRowGroup - 1) / kRowGroup);
+  p.row_group = (p.row_tiles + p.row_groups - 1) / p.row_groups;
+  p.shares = kWorkers / p.row_group;
   p.slot_rows = static_cast<int>(rows < 128 ? rows : 128);
   p.lens = lens;
   p.counts = counts;
