@@ -22,6 +22,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 
@@ -29,7 +30,11 @@ namespace stof {
 namespace {
 
 constexpr int kThreadsRope = 256;
-constexpr int kBatch = 4;  // heads in flight per thread
+// Heads in flight per thread and blocks per SM: the product of loads in flight
+// is what counts.  16384 tokens: 4 heads x 2 blocks 73.2 us, 2 x 4 67.6, 2 x 5
+// (spills) 91.6, 1 x 6 80.0.
+constexpr int kBatch = 2, kBlocksRope = 4;
+constexpr int kCopies = 4;  // copies in flight per thread
 
 struct Rows {
   uint16_t* data;
@@ -88,7 +93,7 @@ __device__ __forceinline__ void angle(const RopeParams& p, int pair, int64_t pos
 // WIDE: a unit is 8 pairs (2 x 16 bytes of the two halves) or, interleaved, 4
 // pairs (16 bytes), moved by 16-byte accesses; else one pair by 2-byte ones.
 template <bool BF16, bool INTER, bool WIDE>
-__global__ void __launch_bounds__(kThreadsRope) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreadsRope, kBlocksRope) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int PAIRS = WIDE ? (INTER ? 4 : 8) : 1;  // pairs per unit
   const uint32_t tid = blockIdx.x * kThreadsRope + threadIdx.x;
   if (tid >= p.n_threads) return;
@@ -171,27 +176,33 @@ __global__ void __launch_bounds__(kThreadsRope) rope_kernel(const __grid_constan
 
   // what is only copied: the elements past rot of Q's and K's heads, and V
   constexpr int E = WIDE ? 8 : 1;  // elements per copy
-  auto copy = [&](const uint16_t* from, uint16_t* to) {
-    if constexpr (WIDE)
-      *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
-    else
-      *to = *from;
+  using Unit = std::conditional_t<WIDE, uint4, uint16_t>;
+  // n copies of E elements, `from` and `to` giving the places of copy x
+  auto copy_all = [&](uint32_t n, auto&& from, auto&& to) {
+    for (uint32_t x0 = in_token; x0 < n; x0 += per_token * kCopies) {
+      Unit u[kCopies];
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i)
+        if (x0 + i * per_token < n) u[i] = *reinterpret_cast<const Unit*>(from(x0 + i * per_token));
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i)
+        if (x0 + i * per_token < n) *reinterpret_cast<Unit*>(to(x0 + i * per_token)) = u[i];
+    }
   };
   const uint32_t rest = static_cast<uint32_t>(p.d - p.rot) / E;
   if (rest) {
-    for (uint32_t x = in_token; x < rest * heads; x += per_token) {
-      const int h = static_cast<int>(x / rest), e = p.rot + static_cast<int>(x - h * rest) * E;
-      copy(src(h) + e, dst(h) + e);
-    }
+    copy_all(
+        rest * heads,
+        [&](uint32_t x) { return src(static_cast<int>(x / rest)) + p.rot + x % rest * E; },
+        [&](uint32_t x) { return dst(static_cast<int>(x / rest)) + p.rot + x % rest * E; });
   }
   if (p.has_v && kv) {
     const uint16_t* v = p.v.data + b * p.v.sb + t * p.v.st;
     uint16_t* vo = p.vo.data + b * p.vo.sb + row * p.vo.st;
     const uint32_t per_head = static_cast<uint32_t>(p.d) / E;
-    for (uint32_t x = in_token; x < per_head * p.Hkv; x += per_token) {
-      const int h = static_cast<int>(x / per_head), e = static_cast<int>(x - h * per_head) * E;
-      copy(v + h * p.v.sh + e, vo + h * p.vo.sh + e);
-    }
+    copy_all(
+        per_head * p.Hkv, [&](uint32_t x) { return v + static_cast<int64_t>(x / per_head) * p.v.sh + x % per_head * E; },
+        [&](uint32_t x) { return vo + static_cast<int64_t>(x / per_head) * p.vo.sh + x % per_head * E; });
   }
 }
 
@@ -203,13 +214,14 @@ template <bool BF16, bool INTER, bool WIDE>
 cudaError_t launch(RopeParams& p, long long tokens, cudaStream_t s) {
   constexpr int PAIRS = WIDE ? (INTER ? 4 : 8) : 1;
   const long long units = p.rot / 2 / PAIRS, heads = p.H + p.Hkv;
-  // Head slots per token: one when the tokens alone fill the GPU (an angle
-  // is then computed once for all heads), more when they do not, up to a
-  // thread per head.
-  const long long want = 1024ll * device_sm_count();
-  long long slots = 1;
-  while (slots < heads && tokens * units * slots < want) slots *= 2;
+  // Head slots per token: as few as come near the 1024 threads per SM that
+  // are resident (an angle is then computed for as many heads as can be), up
+  // to a thread per head when there are few tokens.  16384 tokens, 40 heads of
+  // 128: 1 slot 71.6 us, 2 slots 67.5, 4 slots 69.8, 8 slots 73.8.
+  const long long want = 870ll * device_sm_count();
+  long long slots = (want + tokens * units - 1) / (tokens * units);
   if (slots > heads) slots = heads;
+  while (heads % slots) ++slots;  // as many heads for every slot (3 slots for 32 heads: 41.5 us, 4: 36.2)
   p.slots = static_cast<int>(slots);
   p.n_threads = static_cast<uint32_t>(tokens * units * slots);
   const unsigned grid = static_cast<unsigned>((tokens * units * slots + kThreadsRope - 1) / kThreadsRope);
