@@ -615,11 +615,18 @@ stof_status stof_rope_plan_custom(stof_rope_plan* plan, int rot_dim, int interle
                                   double amplitude);
 
 /* Rows of d contiguous 16-bit elements in device memory: row (b, h, t)
- * starts at data + b stride_b + h stride_h + t stride_t (elements). */
+ * starts at data + b stride_b + h stride_h + t stride_t (elements).  data
+ * NULL: absent. */
 typedef struct {
   void* data;
   int64_t stride_b, stride_h, stride_t;
 } stof_rows;
+
+/* The inputs of a rotation and where they go: an input and its output are
+ * both present or both absent. */
+typedef struct {
+  stof_rows q, k, v, q_out, k_out, v_out;
+} stof_rope_rows;
 
 /*
  * Rotary positions on the Q and K of B requests of T tokens, moved from the
@@ -631,10 +638,10 @@ typedef struct {
  *   y[c] = amplitude (x[c] cos phi + x[a] sin phi),   phi = position * frequency of the pair,
  * in fp32 from an exactly reduced phi, rounded once; the head's other
  * elements and all of V are copied.
- *   q, q_out   H heads; both NULL (or H = 0) for none.
- *   k, k_out   Hkv heads; v, v_out Hkv heads; each pair NULL for none.
- *              An output may be its input (same data and strides); otherwise
- *              no output overlaps an input or another output.
+ *   x          HOST struct, copied at the call: q and q_out with H heads, k,
+ *              k_out, v and v_out with Hkv; V only beside K.  An output may
+ *              be its input (same data and strides); otherwise no output
+ *              overlaps an input or another output.
  *   positions  device int32 [B][T], any values; or NULL: token (b, t) has
  *              position rows[b] + t (t without rows).
  *   counts     device int32 [B] or NULL (all T): tokens of request b; what
@@ -650,21 +657,18 @@ typedef struct {
  * stream; the call needs no workspace.
  */
 #define STOF_DEVERR_BAD_LENGTH 0x8 /* a length or row from device memory is out of range: skipped */
-stof_status stof_rope_fwd(const stof_rope_plan* plan, const stof_rows* q, const stof_rows* k, const stof_rows* v,
-                          stof_dtype dt, int B, int H, int Hkv, int T, int d, const int32_t* positions,
-                          const int32_t* counts, const int32_t* rows, int kv_rows, const stof_rows* q_out,
-                          const stof_rows* k_out, const stof_rows* v_out, int64_t* device_error, void* stream);
+stof_status stof_rope_fwd(const stof_rope_plan* plan, const stof_rope_rows* x, stof_dtype dt, int B, int H, int Hkv, int T,
+                          int d, const int32_t* positions, const int32_t* counts, const int32_t* rows, int kv_rows,
+                          int64_t* device_error, void* stream);
 
 /*
  * The gradient of stof_rope_fwd() without rows: from the gradients of its
- * outputs (dq, dk, dv) to those of its inputs, the rotation by -phi with the
+ * outputs (in x's q, k, v) to those of its inputs (q_out, ...), the rotation by -phi with the
  * same amplitude.  Any strides on both sides: a gradient can go straight into
  * the packed projection's gradient.  Other arguments as stof_rope_fwd().
  */
-stof_status stof_rope_bwd(const stof_rope_plan* plan, const stof_rows* dq, const stof_rows* dk, const stof_rows* dv,
-                          stof_dtype dt, int B, int H, int Hkv, int T, int d, const int32_t* positions,
-                          const int32_t* counts, const stof_rows* dq_out, const stof_rows* dk_out,
-                          const stof_rows* dv_out, void* stream);
+stof_status stof_rope_bwd(const stof_rope_plan* plan, const stof_rope_rows* x, stof_dtype dt, int B, int H, int Hkv, int T,
+                          int d, const int32_t* positions, const int32_t* counts, void* stream);
 
 /*
  * Diagnostic of the failure handling (the paper has no counterpart): every

@@ -240,25 +240,24 @@ bool plan_ok(const stof_rope_plan* plan) {
          plan->rot_dim % 2 == 0 && (plan->interleaved == 0 || plan->interleaved == 1) && std::isfinite(plan->amplitude);
 }
 
-stof_status rope_call(const stof_rope_plan* plan, const stof_rows* q, const stof_rows* k, const stof_rows* v,
-                      stof_dtype dt, int B, int H, int Hkv, int T, int d, const int32_t* positions,
-                      const int32_t* counts, const int32_t* rows, int kv_rows, const stof_rows* q_out,
-                      const stof_rows* k_out, const stof_rows* v_out, bool backward, int64_t* err, void* stream) {
-  if (!plan_ok(plan)) return STOF_ERR_INVALID_ARG;
+stof_status rope_call(const stof_rope_plan* plan, const stof_rope_rows* x, stof_dtype dt, int B, int H, int Hkv, int T, int d,
+                      const int32_t* positions, const int32_t* counts, const int32_t* rows, int kv_rows, bool backward,
+                      int64_t* err, void* stream) {
+  if (!plan_ok(plan) || !x) return STOF_ERR_INVALID_ARG;
   if (dt != STOF_F16 && dt != STOF_BF16) return STOF_ERR_DTYPE;
   if (B < 0 || T < 0 || H < 0 || Hkv < 0 || d < 1 || kv_rows < 0) return STOF_ERR_INVALID_ARG;
-  if (!q != !q_out || !k != !k_out || !v != !v_out) return STOF_ERR_INVALID_ARG;
+  if (!x->q.data != !x->q_out.data || !x->k.data != !x->k_out.data || !x->v.data != !x->v_out.data)
+    return STOF_ERR_INVALID_ARG;
+  if (x->v.data && !x->k.data) return STOF_ERR_INVALID_ARG;  // V is moved beside K
   if (d > 256 || d % 2) return STOF_ERR_UNSUPPORTED;
   if (plan->rot_dim > d) return STOF_ERR_SHAPE;
-  if (v && !k) return STOF_ERR_INVALID_ARG;  // V is moved beside K
   RopeParams p;
   std::memset(&p, 0, sizeof(p));
   bool wide = d % 8 == 0 && plan->rot_dim % (plan->interleaved ? 8 : 16) == 0;
-  const stof_rows* in[6] = {q, k, v, q_out, k_out, v_out};
+  const stof_rows* in[6] = {&x->q, &x->k, &x->v, &x->q_out, &x->k_out, &x->v_out};
   Rows* to[6] = {&p.q, &p.k, &p.v, &p.qo, &p.ko, &p.vo};
   for (int i = 0; i < 6; ++i) {
-    if (!in[i]) continue;
-    if (!in[i]->data) return STOF_ERR_INVALID_ARG;
+    if (!in[i]->data) continue;
     if (reinterpret_cast<uintptr_t>(in[i]->data) % 2) return STOF_ERR_ALIGNMENT;
     *to[i] = Rows{static_cast<uint16_t*>(in[i]->data), in[i]->stride_b, in[i]->stride_h, in[i]->stride_t};
     wide = wide && wide_rows(*to[i]);
@@ -268,9 +267,9 @@ stof_status rope_call(const stof_rope_plan* plan, const stof_rows* q, const stof
   if (words % 4 || reinterpret_cast<uintptr_t>(err) % 8) return STOF_ERR_ALIGNMENT;
   const long long tokens = static_cast<long long>(B) * T;
   if (H > (1 << 20) || Hkv > (1 << 20) || tokens * (plan->rot_dim / 2) >= (1ll << 31)) return STOF_ERR_SHAPE;
-  p.H = q ? H : 0;
-  p.Hkv = k ? Hkv : 0;
-  p.has_v = v ? 1 : 0;
+  p.H = x->q.data ? H : 0;
+  p.Hkv = x->k.data ? Hkv : 0;
+  p.has_v = x->v.data ? 1 : 0;
   if (tokens == 0 || p.H + p.Hkv == 0) return STOF_OK;  // nothing to turn
   p.T = T;
   p.d = d;
@@ -364,19 +363,13 @@ extern "C" stof_status stof_rope_plan_custom(stof_rope_plan* plan, int rot_dim, 
   return STOF_OK;
 }
 
-extern "C" stof_status stof_rope_fwd(const stof_rope_plan* plan, const stof_rows* q, const stof_rows* k,
-                                     const stof_rows* v, stof_dtype dt, int B, int H, int Hkv, int T, int d,
-                                     const int32_t* positions, const int32_t* counts, const int32_t* rows, int kv_rows,
-                                     const stof_rows* q_out, const stof_rows* k_out, const stof_rows* v_out,
-                                     int64_t* device_error, void* stream) {
-  return rope_call(plan, q, k, v, dt, B, H, Hkv, T, d, positions, counts, rows, kv_rows, q_out, k_out, v_out, false,
-                   device_error, stream);
+extern "C" stof_status stof_rope_fwd(const stof_rope_plan* plan, const stof_rope_rows* x, stof_dtype dt, int B, int H,
+                                     int Hkv, int T, int d, const int32_t* positions, const int32_t* counts,
+                                     const int32_t* rows, int kv_rows, int64_t* device_error, void* stream) {
+  return rope_call(plan, x, dt, B, H, Hkv, T, d, positions, counts, rows, kv_rows, false, device_error, stream);
 }
 
-extern "C" stof_status stof_rope_bwd(const stof_rope_plan* plan, const stof_rows* dq, const stof_rows* dk,
-                                     const stof_rows* dv, stof_dtype dt, int B, int H, int Hkv, int T, int d,
-                                     const int32_t* positions, const int32_t* counts, const stof_rows* dq_out,
-                                     const stof_rows* dk_out, const stof_rows* dv_out, void* stream) {
-  return rope_call(plan, dq, dk, dv, dt, B, H, Hkv, T, d, positions, counts, nullptr, T, dq_out, dk_out, dv_out, true,
-                   nullptr, stream);
+extern "C" stof_status stof_rope_bwd(const stof_rope_plan* plan, const stof_rope_rows* x, stof_dtype dt, int B, int H,
+                                     int Hkv, int T, int d, const int32_t* positions, const int32_t* counts, void* stream) {
+  return rope_call(plan, x, dt, B, H, Hkv, T, d, positions, counts, nullptr, T, true, nullptr, stream);
 }

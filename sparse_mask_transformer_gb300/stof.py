@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -126,9 +127,8 @@ class stof_rope_plan(ctypes.Structure):
                 ("made", ctypes.c_int32), ("step", ctypes.c_uint64 * STOF_ROPE_MAX_PAIRS)]
 
 
-class stof_rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
-                ("stride_t", ctypes.c_int64)]
+# stof_rope_rows: data, stride_b, stride_h, stride_t of q, k, v, q_out, k_out, v_out
+_rope_rows = struct.Struct("24q").pack
 
 
 _lib = None
@@ -202,12 +202,9 @@ def load_library(path: str = LIB_PATH):
         lib.stof_rope_plan_custom.argtypes = [ctypes.POINTER(stof_rope_plan), i32, i32, ctypes.POINTER(ctypes.c_double),
                                               ctypes.c_double]
         lib.stof_rope_plan_custom.restype = i32
-        R = P  # stof_rows
-        lib.stof_rope_fwd.argtypes = [ctypes.POINTER(stof_rope_plan), R, R, R, i32, i32, i32, i32, i32, i32, P, P, P, i32,
-                                      R, R, R, P, P]
+        lib.stof_rope_fwd.argtypes = [ctypes.POINTER(stof_rope_plan), P, i32, i32, i32, i32, i32, i32, P, P, P, i32, P, P]
         lib.stof_rope_fwd.restype = i32
-        lib.stof_rope_bwd.argtypes = [ctypes.POINTER(stof_rope_plan), R, R, R, i32, i32, i32, i32, i32, i32, P, P,
-                                      R, R, R, P]
+        lib.stof_rope_bwd.argtypes = [ctypes.POINTER(stof_rope_plan), P, i32, i32, i32, i32, i32, i32, P, P, P]
         lib.stof_rope_bwd.restype = i32
         lib.stof_tune_workspace_bytes.argtypes = [i32, i32]
         lib.stof_tune_workspace_bytes.restype = sz
@@ -687,56 +684,60 @@ def stof_rope_plan_custom(frequencies, interleaved: bool = False, amplitude: flo
     return plan
 
 
-_RowsArray = ctypes.c_int64 * 24  # six stof_rows
+_ABSENT = (0, 0, 0, 0)
 
 
-def _rope(where, plan, x, y, positions, counts, rows, device_error, stream):
-    """x, y: (q, k, v) and their outputs, [B, heads, T, d] with contiguous rows of d, any other strides."""
-    q, k, v = x
+def _rope_pair(where, a, out, B, T, d, dtype):
+    """Checks one input and its output; their stof_rows, the heads and the output's rows."""
+    if out is None or a is None:
+        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: an input needs its output, and an output its input")
+    shape, to = a.shape, out.shape
+    if len(shape) != 4 or len(to) != 4 or a.dtype != dtype or out.dtype != dtype:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: tensors must be [B, heads, T, d] of one dtype")
+    n, h, t, w = shape
+    if n != B or t != T or w != d or to[0] != B or to[1] != h or to[3] != d:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: shapes differ")
+    sb, sh, st, se = a.stride()
+    ob, oh, ot, oe = out.stride()
+    if d > 1 and (se != 1 or oe != 1):
+        raise StofError(STOF_ERR_SHAPE, f"{where}: a row's elements must be contiguous")
+    return (a.data_ptr(), sb, sh, st), (out.data_ptr(), ob, oh, ot), h, to[2]
+
+
+def _rope(where, plan, q, k, v, q_out, k_out, v_out, positions, counts, rows, device_error, stream):
+    """q, k, v and their outputs, [B, heads, T, d] with contiguous rows of d, any other strides."""
+    device = _device_of(where, q, k, v, q_out, k_out, v_out, positions, counts, rows, device_error)
     lead = q if q is not None else k
-    if lead is None:
-        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: give q or k")
-    device = _device_of(where, *x, *y, positions, counts, rows, device_error)
-    if lead.dim() != 4:
-        raise StofError(STOF_ERR_SHAPE, f"{where}: tensors must be [B, heads, T, d]")
+    if lead is None or lead.dim() != 4:
+        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: give q or k, [B, heads, T, d]")
     B, _, T, d = lead.shape
-    dtype, kv_rows, heads = lead.dtype, T, [0, 0, 0]
-    fields, given = [], []
-    for i in range(3):
-        a, out = x[i], y[i]
-        if a is None or out is None:
-            if a is not out:
-                raise StofError(STOF_ERR_INVALID_ARG, f"{where}: an input needs its output, and an output its input")
-            continue
-        if a.dim() != 4 or out.dim() != 4 or a.dtype != dtype or out.dtype != dtype:
-            raise StofError(STOF_ERR_SHAPE, f"{where}: tensors must be [B, heads, T, d] of one dtype")
-        sa, so, (n, h, m, w) = a.stride(), out.stride(), out.shape
-        if a.shape != (B, h, T, d) or n != B or w != d or m < T and (i == 0 or rows is None):
-            raise StofError(STOF_ERR_SHAPE, f"{where}: shapes differ")
-        if i == 0 and m != T:
+    dtype = lead.dtype
+    qi = qo = ki = ko = vi = vo = _ABSENT
+    H = Hkv = 0
+    kv_rows = T
+    if q is not None or q_out is not None:
+        qi, qo, H, m = _rope_pair(where, q, q_out, B, T, d, dtype)
+        if m != T:
             raise StofError(STOF_ERR_SHAPE, f"{where}: q_out must have q's shape")
-        if d > 1 and (sa[3] != 1 or so[3] != 1):
-            raise StofError(STOF_ERR_SHAPE, f"{where}: a row's elements must be contiguous")
-        heads[i] = h
-        if i == 1:
-            kv_rows = m
-        elif i == 2 and (k is None or h != heads[1] or m != kv_rows):
+    if k is not None or k_out is not None:
+        ki, ko, Hkv, kv_rows = _rope_pair(where, k, k_out, B, T, d, dtype)
+        if kv_rows < T and rows is None:
+            raise StofError(STOF_ERR_SHAPE, f"{where}: k_out has fewer rows than k")
+    if v is not None or v_out is not None:
+        vi, vo, h, m = _rope_pair(where, v, v_out, B, T, d, dtype)
+        if k is None or h != Hkv or m != kv_rows:
             raise StofError(STOF_ERR_SHAPE, f"{where}: v goes with a k of its shape")
-        given.append(i)
-        fields += (a.data_ptr(), sa[0], sa[1], sa[2], out.data_ptr(), so[0], so[1], so[2])
-    c = _RowsArray(*fields)
-    base, at = ctypes.addressof(c), [None] * 6
-    for place, i in enumerate(given):
-        at[i], at[3 + i] = base + 64 * place, base + 64 * place + 32
-    head = (ctypes.byref(plan), at[0], at[1], at[2], _dtype_code(lead), B, heads[0], heads[1], T, d,
-            _int32(where, "positions", positions, (B, T)), _int32(where, "counts", counts, (B,)))
+    x = _rope_rows(*qi, *ki, *vi, *qo, *ko, *vo)
+    p = None if positions is None else _int32(where, "positions", positions, (B, T))
+    n = None if counts is None else _int32(where, "counts", counts, (B,))
     lib = load_library()
     if where == "stof_rope_bwd":
-        _launch(where, device, stream, lib.stof_rope_bwd, *head, at[3], at[4], at[5])
+        _launch(where, device, stream, lib.stof_rope_bwd, plan, x, _dtype_code(lead), B, H, Hkv, T, d, p, n)
     else:
-        _launch(where, device, stream, lib.stof_rope_fwd, *head, _int32(where, "rows", rows, (B,)), kv_rows, at[3], at[4],
-                at[5], _error_word(where, device_error))
-    return y
+        _launch(where, device, stream, lib.stof_rope_fwd, plan, x, _dtype_code(lead), B, H, Hkv, T, d, p, n,
+                None if rows is None else _int32(where, "rows", rows, (B,)), kv_rows,
+                None if device_error is None else _error_word(where, device_error))
+    return q_out, k_out, v_out
 
 
 def stof_rope_fwd(plan: stof_rope_plan, q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
@@ -746,7 +747,7 @@ def stof_rope_fwd(plan: stof_rope_plan, q: torch.Tensor | None, k: torch.Tensor 
     """q [B, H, T, d], k and v [B, Hkv, T, d] (views of a packed projection included) turned by their positions
     (int32 [B, T]; None: rows[b] + t) and written to q_out [B, H, T, d] and k_out, v_out [B, Hkv, T or more, d],
     there from row rows[b] (int32 [B]; None: 0) on.  counts (int32 [B]): tokens of each request.  Returns the outputs."""
-    return _rope("stof_rope_fwd", plan, (q, k, v), (q_out, k_out, v_out), positions, counts, rows, device_error, stream)
+    return _rope("stof_rope_fwd", plan, q, k, v, q_out, k_out, v_out, positions, counts, rows, device_error, stream)
 
 
 def stof_rope_bwd(plan: stof_rope_plan, dq: torch.Tensor | None, dk: torch.Tensor | None, dv: torch.Tensor | None,
@@ -755,7 +756,7 @@ def stof_rope_bwd(plan: stof_rope_plan, dq: torch.Tensor | None, dk: torch.Tenso
     """Gradients of stof_rope_fwd's outputs (no rows) to those of its inputs; any strides on both sides."""
     if dk_out is not None and dk is not None and dk_out.dim() == 4 and dk.dim() == 4 and dk_out.shape[2] != dk.shape[2]:
         raise StofError(STOF_ERR_SHAPE, "stof_rope_bwd: dk_out must have dk's shape")
-    return _rope("stof_rope_bwd", plan, (dq, dk, dv), (dq_out, dk_out, dv_out), positions, counts, None, None, stream)
+    return _rope("stof_rope_bwd", plan, dq, dk, dv, dq_out, dk_out, dv_out, positions, counts, None, None, stream)
 
 
 def stof_tune_workspace_bytes(n_masks: int, L: int) -> int:

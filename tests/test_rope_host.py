@@ -3,6 +3,7 @@ definition in exact arithmetic, and the refusals of plans and calls (before
 any launch, so no GPU is needed)."""
 import ctypes
 import math
+import struct
 from fractions import Fraction
 
 import pytest
@@ -85,10 +86,9 @@ FAKE = 1 << 20  # never dereferenced: every call below is refused first
 def _call(lib, plan=None, q=True, k=True, v=True, dt=0, B=2, H=4, Hkv=2, T=8, d=64, positions=None, counts=None,
           rows=None, kv_rows=8, q_out=True, k_out=True, v_out=True, data=FAKE, err=None):
     plan = stof.stof_rope_plan_init(64) if plan is None else plan
-    r = stof.stof_rows(data, 4096, 512, 64)
-    ref = lambda on: ctypes.byref(r) if on else None  # noqa: E731
-    return lib.stof_rope_fwd(ctypes.byref(plan), ref(q), ref(k), ref(v), dt, B, H, Hkv, T, d, positions, counts, rows,
-                             kv_rows, ref(q_out), ref(k_out), ref(v_out), err, None)
+    row = lambda on: (data or 0, 4096, 512, 64) if on else (0, 0, 0, 0)  # noqa: E731
+    x = struct.pack("24q", *row(q), *row(k), *row(v), *row(q_out), *row(k_out), *row(v_out))
+    return lib.stof_rope_fwd(ctypes.byref(plan), x, dt, B, H, Hkv, T, d, positions, counts, rows, kv_rows, err, None)
 
 
 def test_bad_calls_are_refused(lib):
@@ -102,7 +102,8 @@ def test_bad_calls_are_refused(lib):
     assert _call(lib, d=63) == stof.STOF_ERR_UNSUPPORTED
     assert _call(lib, d=258) == stof.STOF_ERR_UNSUPPORTED
     assert _call(lib, d=32) == stof.STOF_ERR_SHAPE
-    assert _call(lib, data=None) == stof.STOF_ERR_INVALID_ARG
+    assert lib.stof_rope_fwd(ctypes.byref(stof.stof_rope_plan_init(64)), None, 0, 2, 4, 2, 8, 64, None, None, None, 8, None,
+                             None) == stof.STOF_ERR_INVALID_ARG
     assert _call(lib, data=FAKE + 1) == stof.STOF_ERR_ALIGNMENT
     assert _call(lib, positions=FAKE + 2) == stof.STOF_ERR_ALIGNMENT
     assert _call(lib, err=FAKE + 4) == stof.STOF_ERR_ALIGNMENT
