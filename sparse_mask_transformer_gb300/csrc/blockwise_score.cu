@@ -177,16 +177,16 @@ struct FormatSource {
   }
   static __device__ bool partial(const Item& x, int t) { return t >= x.nf; }
   template <int BN>
-  static __device__ void bits(const Params&, const Row& row, const Item&, int, uint32_t (&b)[BN / 32]) {
+  static __device__ void bits(const Params&, const Row& row, const Item&, int, int, uint32_t (&b)[BN / 32]) {
 #pragma unroll
     for (int cc = 0; cc < BN / 32; ++cc)
       b[cc] = row.nb[4 * cc] | (row.nb[4 * cc + 1] << 8) | (row.nb[4 * cc + 2] << 16) | (row.nb[4 * cc + 3] << 24);
   }
-  template <int CHUNKS>
-  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, uint32_t (&sr)[CHUNKS][32], float c,
-                               float slope) {
+  template <int BN>
+  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, int, uint32_t (&sr)[BN / 32][32],
+                               float c, float slope) {
     const int rel = row.pos - tile_key(p, x, t);
-    lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= CHUNKS * 32 - 1));
+    lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= BN - 1));
   }
   static __device__ bool whole(const Item&) { return true; }
   static __device__ float* partial_o(const Params&, const Item&, int, int, int) { return nullptr; }

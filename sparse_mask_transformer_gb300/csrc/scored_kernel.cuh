@@ -24,9 +24,14 @@
 // (With K, V, score and PV warps that served both workers in turn the loops
 // took 32 KB, and 92% of the instruction fetch bandwidth behind the cache:
 // 723 us instead of @CAUSAL@ us for 8192 causal tokens, 32 heads of 128.)
+// REP > 1 (few query rows): Q's rows are in the tile REP times, 128 / REP rows
+// apart, and each copy's softmax threads take one REP-th of the tile's keys,
+// their P being 0 in the other columns: a tile then costs a thread 32 scores
+// instead of BN, in a fraction of the code.  The copies' partial rows are
+// merged at the segment's end through the worker's scratch rows in the
+// workspace.  (7 rows per K/V head, d = 64: 29.7 us, with a thread a row 50.2.)
 // A softmax warp whose 32 query rows are all past the tile's last one only
-// keeps the barriers' step: a decode step of four query rows runs one warp
-// in four.
+// keeps the barriers' step.
 // BN is 128 for d = 64 and 64 for d = 128: S, P and O of both workers then fit
 // the 512 TMEM columns, and a ring stage is 16 KB.  TMEM columns: S_g [BN g,
 // +BN), P_g [2 BN + BN / 2 g, +BN / 2), O_g [512 - 2 d + d g, +d).
@@ -96,7 +101,7 @@ template <class SRC, int D>
 struct Worker {
   uint64_t q_full, q_done;  // Q is in place; the segment's score MMAs are done
   uint64_t k_full[Shape<D>::K], k_free[Shape<D>::K], v_full[Shape<D>::V], v_free[Shape<D>::V];
-  uint64_t s_full, s_free, p_full, pv_done, drain;
+  uint64_t s_full, s_free, p_full, pv_done, merge, drain;
   uint64_t ring_full[kRing], ring_free[kRing];
   Segment<typename SRC::Item> ring[kRing];  // n < 0: no more segments
 };
@@ -131,12 +136,13 @@ __device__ __forceinline__ void rescale_row(uint32_t tOr, float alpha) {
   }
 }
 
-template <class SRC, int D, bool BF16, int MODE>
+template <class SRC, int D, bool BF16, int MODE, int REP>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ typename SRC::Params p) {
   using Sh = Shape<D>;
-  constexpr int BN = Sh::BN, REGIONS = D / 64, Q_ATOM = kBM * 128, CHUNKS = BN / 32;
+  constexpr int BN = Sh::BN, REGIONS = D / 64, Q_ATOM = kBM * 128;
+  constexpr int KEYS = BN / REP, CHUNKS = KEYS / 32, ROWS = kBM / REP;  // a thread's keys; rows of one copy of Q
   using Shared = Smem<SRC, D>;
   extern __shared__ uint8_t smem_raw[];
   Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -157,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&w.s_free, 128);
     mbar_init(&w.p_full, 128);
     mbar_init(&w.pv_done, 1);
+    mbar_init(&w.merge, 128);
     mbar_init(&w.drain, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&w.ring_full[i], 1);
@@ -253,7 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&w.q_full, kBM * D * 2);
 #pragma unroll
         for (int r = 0; r < REGIONS; ++r)
-          tma_load_3d(s.q[g] + r * Q_ATOM, &tmQ, &w.q_full, 64 * r, seg.q_row, seg.q_plane);
+#pragma unroll
+          for (int x = 0; x < REP; ++x)
+            tma_load_3d(s.q[g] + r * Q_ATOM + x * ROWS * 128, &tmQ, &w.q_full, 64 * r, seg.q_row, seg.q_plane);
         // K_0, K_1, V_0, K_2, V_1, ...
 #pragma unroll 1
         for (int x = 0; ok && x < 2 * seg.n; ++x) {
@@ -362,9 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // query row in the tile == TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tSr = tS + lane_off, tPr = tP + lane_off, tOr = tO + lane_off;
+    const int part = r / ROWS;  // the copy of Q this thread's row belongs to: its keys of a tile are KEYS part ..
+    const uint32_t tSr = tS + lane_off + KEYS * part, tPr = tP + lane_off + KEYS / 2 * part, tOr = tO + lane_off;
     typename SRC::Row row;
-    int j = 0;  // tiles so far
+    int j = 0, merges = 0;  // tiles so far; segments merged (REP > 1)
+    if constexpr (REP > 1) {  // P is 0 outside this copy's keys, from here on
+      const uint32_t zero[16] = {};
+#pragma unroll
+      for (int x = 0; x < BN / 32; ++x) tmem_st16(tP + lane_off + 16 * x, zero);
+      tmem_st_wait();
+    }
 #pragma unroll 1
     for (int handed = 0;; ++handed) {
       const Next got = read_ring(handed, seg);
@@ -372,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = got == Next::none;
         break;
       }
-      const bool live = SRC::begin_row(p, row, seg, r);   // the row is one of the call's
+      const bool live = SRC::begin_row(p, row, seg, r % ROWS);   // the row is one of the call's
       const bool alive = __any_sync(0xffffffffu, live);   // the warp has such a row
       float slope = 0.f;
       if (MODE == MODE_DISTANCE && p.slopes && live) slope = __ldg(p.slopes + row.head) * kLog2e;
@@ -389,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&w.s_free);  // the scores are in registers: S may be overwritten
           const bool partial = SRC::partial(seg.item, t);
           uint32_t bits[CHUNKS] = {};
-          if (partial) SRC::template bits<BN>(p, row, seg.item, t, bits);
+          if (partial) SRC::template bits<BN>(p, row, seg.item, t, KEYS * part, bits);
           SRC::template prefetch<BN>(p, row, seg.item, t + 1, seg.n);
           uint32_t pk[CHUNKS][16];
           float alpha = 1.f;
@@ -449,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               cap_scores(sr, p.k, __all_sync(0xffffffffu, row_within(sr, p.k.lim)));
               c = 1.f;
             }
-            SRC::lower(p, row, seg.item, t, sr, c, slope);
+            SRC::template lower<BN>(p, row, seg.item, t, KEYS * part, sr, c, slope);
             if (partial) mask_scores(sr, bits);
             const float nmu = raise_ref(row_max(sr));
             l += exp_pack<CHUNKS, BF16>(sr, 1.f, nmu, pk);
@@ -472,6 +488,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || (seg.n > 0 && !warp_wait(&w.pv_done, (j - 1) & 1, abort_flag))) {
         ok = false;
         break;
+      }
+      if constexpr (REP > 1) {
+        // O of every copy, unscaled, and its rows' max and sum to the worker's
+        // scratch; then all threads merge the copies' rows.  Two scratch
+        // buffers in turn: the barrier of the next segment comes between this
+        // segment's reads and the second next's writes.
+        float* scratch = SRC::scratch(p, g, merges & 1, D);
+        float2* stats = reinterpret_cast<float2*>(scratch + static_cast<size_t>(REP) * p.rows * D);
+        if (alive) {
+          tc_fence_after();
+          const size_t at = static_cast<size_t>(part) * p.rows + r % ROWS;
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(tOr + cc * 32, o);
+            tmem_ld_wait(o);
+            if (live) {
+              float4* dst = reinterpret_cast<float4*>(scratch + at * D + cc * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                     __uint_as_float(o[4 * i + 3]));
+            }
+          }
+          if (live) stats[at] = make_float2(m_ref, l);
+          tc_fence_before();
+        }
+        mbar_arrive(&w.merge);
+        if (!warp_wait(&w.merge, merges & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ++merges;
+        const bool whole = SRC::whole(seg.item);
+        const int n = p.rows * (D / 4);
+#pragma unroll 2
+        for (int i = r; i < n; i += 128) {
+          const int rr = i / (D / 4), c = (i - rr * (D / 4)) * 4;
+          size_t out;
+          if (!SRC::out_of(p, seg.item, rr, out)) continue;
+          float m = -INFINITY, sum = 0.f;
+          float2 st[REP];
+          float4 x[REP], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < REP; ++k) {
+            const size_t at = static_cast<size_t>(k) * p.rows + rr;
+            st[k] = stats[at];
+            x[k] = *reinterpret_cast<const float4*>(scratch + at * D + c);
+            m = fmaxf(m, st[k].x);
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int k = 0; k < REP; ++k) {
+            const float a = ex2(st[k].x - ref);
+            sum = fmaf(a, st[k].y, sum);
+            // a copy that has seen no key: its O is a sum of zeros, or unset
+            if (st[k].y != 0.f) {
+              y.x = fmaf(a, x[k].x, y.x);
+              y.y = fmaf(a, x[k].y, y.y);
+              y.z = fmaf(a, x[k].z, y.z);
+              y.w = fmaf(a, x[k].w, y.w);
+            }
+          }
+          if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + out * D + c) =
+                make_uint2(pack2<BF16>(y.x * inv, y.y * inv), pack2<BF16>(y.z * inv, y.w * inv));
+          } else {
+            *reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, g, rr, D) + c) = y;
+            if (c == 0) SRC::put_stats(p, seg.item, g, rr, m, sum);
+          }
+        }
+        continue;
       }
       if (!alive) continue;
       tc_fence_after();
@@ -516,16 +605,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Launches an instance with its shared memory and register split prepared.
-template <class SRC, int D, bool BF16, int MODE>
+template <class SRC, int D, bool BF16, int MODE, int REP = 1>
 stof_status launch_scored(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                           const typename SRC::Params& p, unsigned grid, cudaStream_t s) {
-  auto* kernel = scored_kernel<SRC, D, BF16, MODE>;
+  auto* kernel = scored_kernel<SRC, D, BF16, MODE, REP>;
   constexpr size_t smem = sizeof(Smem<SRC, D>) + 1024;
   static_assert(smem <= 232448, "shared memory");
   stof_status prep = STOF_OK;
   auto prepare = [](const void* arg) {
     stof_status* st = static_cast<stof_status*>(const_cast<void*>(arg));
-    auto* k = scored_kernel<SRC, D, BF16, MODE>;
+    auto* k = scored_kernel<SRC, D, BF16, MODE, REP>;
     cudaFuncAttributes fa;
     if (record_cuda(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
             cudaSuccess ||

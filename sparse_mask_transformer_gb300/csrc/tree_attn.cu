@@ -44,8 +44,10 @@ struct TreeParams : CommonParams {
   const int32_t* counts;
   const uint32_t* tree;
   const int32_t* positions;
+  int copies;      // copies of Q's rows in a tile
   float* slots;    // [2 kWorkers][slot_rows][d] partial O
   float2* stats;   // [2 kWorkers][slot_rows] (max, sum)
+  float* scratch;  // [2 kWorkers][copies * rows][d + 2], copies > 1
   int32_t* line;   // [B + 1] place of each request on the line, its length
 };
 
@@ -233,11 +235,11 @@ struct CacheSource {
     const int left = x.count - 32 * word;
     return left >= 32 ? bits : bits & ((1u << left) - 1u);
   }
-  template <int BN>
-  static __device__ void bits(const Params& p, const Row& row, const Item& x, int t, uint32_t (&out)[BN / 32]) {
+  template <int BN, int CHUNKS>
+  static __device__ void bits(const Params& p, const Row& row, const Item& x, int t, int first, uint32_t (&out)[CHUNKS]) {
 #pragma unroll
-    for (int cc = 0; cc < BN / 32; ++cc) {
-      const int u0 = (x.t0 + t) * BN + 32 * cc - x.ctx;  // drafted token of the chunk's first key
+    for (int cc = 0; cc < CHUNKS; ++cc) {
+      const int u0 = (x.t0 + t) * BN + first + 32 * cc - x.ctx;  // drafted token of the chunk's first key
       if (u0 <= -32)
         out[cc] = ~0u;
       else if (u0 < 0)
@@ -246,10 +248,10 @@ struct CacheSource {
         out[cc] = __funnelshift_r(seen(p, row, x, u0 >> 5), seen(p, row, x, (u0 >> 5) + 1), u0 & 31);
     }
   }
-  template <int CHUNKS>
-  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, uint32_t (&sr)[CHUNKS][32], float c,
-                               float slope) {
-    const int j0 = (x.t0 + t) * CHUNKS * 32;
+  template <int BN, int CHUNKS>
+  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, int first, uint32_t (&sr)[CHUNKS][32],
+                               float c, float slope) {
+    const int j0 = (x.t0 + t) * BN + first;
     const long long rel = static_cast<long long>(row.pos) - j0;
     if (p.positions && partial(x, t)) {
       float at[CHUNKS];  // position of key 32 i + lane of the tile
@@ -266,6 +268,16 @@ struct CacheSource {
     }
   }
   static __device__ bool whole(const Item& x) { return x.whole; }
+  // Row of O of the K/V head's query row rr; false if the request has no such token.
+  static __device__ bool out_of(const Params& p, const Item& x, int rr, size_t& out) {
+    const int gq = rr / p.T, t = rr - gq * p.T;
+    out = (static_cast<size_t>(x.b) * p.H + x.hk * p.group + gq) * p.T + t;
+    return t < x.count;
+  }
+  // A worker's rows for merging copies of Q: [copies * rows][d] O and (max, sum), two buffers.
+  static __device__ float* scratch(const Params& p, int g, int buffer, int d) {
+    return p.scratch + static_cast<size_t>(2 * (2 * blockIdx.x + g) + buffer) * p.copies * p.rows * (d + 2);
+  }
   // A segment that begins its item goes on in a later share: slot 2 w + 1 of
   // worker w; one that does not: slot 2 w.
   static __device__ size_t slot_row(const Params& p, const Item& x, int g, int r) {
@@ -388,18 +400,35 @@ constexpr long long kRowPerWarp = 1024;
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// Copies of Q's rows in a tile, each with a part of its keys: four at d = 64
+// where the rows leave room for them.  7 rows per K/V head, 32 requests: 29.7 us
+// with four copies, 50.2 with one.  At d = 128 a tile is 64 keys and one copy's
+// code fits the instruction cache: 64 rows, 8 requests took 54.9 us with two
+// copies, 29.9 with one (merging costs more than it saves), 4 rows 13.3 and 13.2.
+constexpr int kCopies64 = 4;
+inline int copies_of(int d, long long rows) { return d == 64 && rows * kCopies64 <= kBM ? kCopies64 : 1; }
+
+template <int D, bool BF16, int MODE>
+stof_status launch_mode(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p,
+                        cudaStream_t s) {
+  if constexpr (D == 64) {
+    if (p.copies == kCopies64) return launch_scored<CacheSource, D, BF16, MODE, kCopies64>(mq, mk, mv, p, kTreeCtas, s);
+  }
+  return launch_scored<CacheSource, D, BF16, MODE, 1>(mq, mk, mv, p, kTreeCtas, s);
+}
+
 template <int D, bool BF16>
 stof_status launch_tree(const void* q, const void* k, const void* v, const TreeParams& p, int mode, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   const uint64_t planes = static_cast<uint64_t>(p.B) * p.Hkv;
-  if (!make_bw_map(&mq, q, planes, p.rows, D, kBM, BF16) || !make_bw_map(&mk, k, planes, p.cap, D, Shape<D>::BN, BF16) ||
-      !make_bw_map(&mv, v, planes, p.cap, D, Shape<D>::BN, BF16))
+  if (!make_bw_map(&mq, q, planes, p.rows, D, kBM / p.copies, BF16) ||
+      !make_bw_map(&mk, k, planes, p.cap, D, Shape<D>::BN, BF16) || !make_bw_map(&mv, v, planes, p.cap, D, Shape<D>::BN, BF16))
     return STOF_ERR_CUDA;
   stof_status st;
   switch (mode) {
-    case MODE_PLAIN: st = launch_scored<CacheSource, D, BF16, MODE_PLAIN>(mq, mk, mv, p, kTreeCtas, s); break;
-    case MODE_CAP: st = launch_scored<CacheSource, D, BF16, MODE_CAP>(mq, mk, mv, p, kTreeCtas, s); break;
-    default: st = launch_scored<CacheSource, D, BF16, MODE_DISTANCE>(mq, mk, mv, p, kTreeCtas, s); break;
+    case MODE_PLAIN: st = launch_mode<D, BF16, MODE_PLAIN>(mq, mk, mv, p, s); break;
+    case MODE_CAP: st = launch_mode<D, BF16, MODE_CAP>(mq, mk, mv, p, s); break;
+    default: st = launch_mode<D, BF16, MODE_DISTANCE>(mq, mk, mv, p, s); break;
   }
   if (st != STOF_OK) return st;
   const bool one = static_cast<long long>(planes) * p.rows >= kRowPerWarp;
@@ -425,7 +454,10 @@ extern "C" size_t stof_tree_attn_workspace_bytes(int B, int H, int Hkv, int T, i
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || T < 1 || T > STOF_TREE_MAX_TOKENS || (d != 64 && d != 128)) return 0;
   const long long rows = static_cast<long long>(H / Hkv) * T;
   const size_t slots = static_cast<size_t>(2 * kWorkers) * (rows < 128 ? rows : 128);
-  return up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + (static_cast<size_t>(B) + 1) * sizeof(int32_t);
+  const int copies = copies_of(d, rows);
+  const size_t scratch = copies > 1 ? slots * copies * (d + 2) * sizeof(float) : 0;
+  return up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + up256(scratch) +
+         (static_cast<size_t>(B) + 1) * sizeof(int32_t);
 }
 
 extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H,
@@ -471,6 +503,7 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   p.tile = d == 64 ? Shape<64>::BN : Shape<128>::BN;
   p.words = (T + 31) / 32;
   p.rows = static_cast<int>(rows);
+  p.copies = copies_of(d, rows);
   p.row_tiles = static_cast<int>(row_tiles);
   p.row_groups = static_cast<int>((row_tiles + kRowGroup - 1) / kRowGroup);
   p.row_group = (p.row_tiles + p.row_groups - 1) / p.row_groups;
@@ -484,7 +517,10 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   const size_t slots = static_cast<size_t>(2 * kWorkers) * p.slot_rows;
   uint8_t* ws = static_cast<uint8_t*>(workspace) + up256(slots * d * sizeof(float));
   p.stats = reinterpret_cast<float2*>(ws);
-  p.line = reinterpret_cast<int32_t*>(ws + up256(slots * sizeof(float2)));
+  ws += up256(slots * sizeof(float2));
+  p.scratch = reinterpret_cast<float*>(ws);
+  if (p.copies > 1) ws += up256(slots * p.copies * (d + 2) * sizeof(float));
+  p.line = reinterpret_cast<int32_t*>(ws);
   const int mode = mode_of(scale, softcap, p.slopes != nullptr);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
