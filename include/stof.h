@@ -352,15 +352,19 @@ typedef struct {
  *   q, o      device [B][H][Lq][d];  k, v  device [B][Hkv][Lk][d], H a
  *             multiple of Hkv; query head h reads K/V head h / (H / Hkv).
  *   score     HOST struct, copied at the call, or NULL for plain scores.
- *   which     as stof_mha_fwd(); STOF_KERNEL_AUTO also takes a format that is
- *             not synced and then runs the block-wise kernel wherever it
- *             takes the sizes (d 64 or 128, 128 x 64 or 128 x 128 OTs), else
+ *   which     as stof_mha_fwd(), but with scores capped or lowered or shared
+ *             K/V heads the block-wise kernel takes 128 x 128 OTs only.
+ *             STOF_KERNEL_AUTO also takes a format that is not synced and
+ *             then runs the block-wise kernel wherever it takes the sizes, else
  *             the row-wise one, so that encoding and attention need no host
  *             round trip between them.
  * The scores are capped and lowered in fp32 (the cap to a few 2^-24 of
  * softcap).  Masked keys take no part whatever their scores; as in
- * stof_mha_fwd(), K and V rows inside a listed OT have to be finite.  Other
- * arguments, formats and errors as stof_mha_fwd_cross().
+ * stof_mha_fwd(), V rows inside a listed OT have to be finite (a masked key's
+ * V row is multiplied by 0).  Plain scores with a K/V head each run
+ * stof_mha_fwd_cross()'s kernels, with its condition on calls that share a
+ * format; the other calls may overlap.  Other arguments, formats and errors
+ * as stof_mha_fwd_cross().
  */
 stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Hkv, int Lq,
                                int Lk, int d, float scale, const stof_score* score, const stof_format* fmt,
@@ -378,7 +382,9 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
  * whose bit is set in its tree row.
  *   q, o       device [B][H][T][d], dt; o is written.
  *   k, v       device [B][Hkv][cap][d], dt; H a multiple of Hkv.  Rows from
- *              lens[b] + counts[b] on are not used, whatever they hold.
+ *              lens[b] + counts[b] on are not used, whatever they hold; the
+ *              V rows before them have to be finite (one that a token does
+ *              not see is multiplied by 0).
  *   lens       device int32 [B]; counts device int32 [B] or NULL (all T).
  *              Needs lens[b] >= 0, 0 <= counts[b] <= T and lens[b] +
  *              counts[b] <= cap; a request that breaks this is skipped and

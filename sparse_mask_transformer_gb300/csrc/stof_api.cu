@@ -587,19 +587,25 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
   if (Hkv < 1) return STOF_ERR_INVALID_ARG;
   if (H % Hkv) return STOF_ERR_SHAPE;
   if (score && (st = check_score(*score, scale)) != STOF_OK) return st;
+  const bool scored = score && (score->softcap > 0.f || score->slopes);
+  const bool usual = !scored && H == Hkv;  // plain scores, a K/V head each: stof_mha_fwd_cross's kernels
+  // OTs and head sizes of the block-wise kernel that would run
+  const bool blk = blockwise_tiles(*fmt) && (usual || fmt->bn == 128) && (d == 64 || d == 128);
   KernelChoice c;
   int source = 0;
   if (which == STOF_KERNEL_AUTO && !fmt->synced) {
     // the tile counts are not on the host: the block-wise kernel, whose time
     // follows the listed tiles, wherever it takes the sizes
-    const bool blk = blockwise_tiles(*fmt) && (d == 64 || d == 128);
     c = KernelChoice{blk ? STOF_KERNEL_BLOCKWISE : STOF_KERNEL_ROWWISE, fmt->bn, 0, kVariantAuto, 0, 0, 0};
   } else {
     st = plan_call(*fmt, B, H, Lq, Lk, d, which, &c, &source);
     if (st != STOF_OK) return st;
+    if (c.kernel == STOF_KERNEL_BLOCKWISE && !blk) {
+      if (which == STOF_KERNEL_BLOCKWISE) return STOF_ERR_UNSUPPORTED;
+      c.kernel = STOF_KERNEL_ROWWISE;
+    }
   }
-  const bool scored = score && (score->softcap > 0.f || score->slopes);
-  if (!scored && H == Hkv)  // plain scores, a K/V head each
+  if (usual)
     return mha_fwd_choice(q, k, v, dt, B, H, Lq, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, c, o, stream);
   ScoredParams p;
   c.rows_per_warp = 0;  // a tuned setting was measured on plain scores
@@ -610,7 +616,7 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
   p.slopes = score ? score->slopes : nullptr;
   p.q_start = score ? score->q_start : 0;
   cudaStream_t s = as_stream(stream);
-  if (c.kernel == STOF_KERNEL_BLOCKWISE && fmt->bn == 128) return launch_blockwise_scored(p, dt == STOF_BF16, s);
+  if (c.kernel == STOF_KERNEL_BLOCKWISE) return launch_blockwise_scored(p, dt == STOF_BF16, s);
   return record_cuda(launch_rowwise_scored(p, dt == STOF_BF16, s)) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
 

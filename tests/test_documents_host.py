@@ -74,6 +74,12 @@ def test_scored_attention_refuses(lib):
     assert _score(lib, score=S(0.0, FAKE, (1 << 30) + 1)) == stof.STOF_ERR_SHAPE
     assert _score(lib, d=32, which=stof.STOF_KERNEL_BLOCKWISE) == stof.STOF_ERR_UNSUPPORTED
     assert _score(lib, fmt=_fmt(256, 64, 64), which=stof.STOF_KERNEL_BLOCKWISE) == stof.STOF_ERR_UNSUPPORTED
+    # 128 x 64 OTs: block-wise only for plain scores with a K/V head each
+    half = _fmt(256, 128, 128)
+    half.bn, half.n_tc = 64, 4
+    assert _score(lib, fmt=half, which=stof.STOF_KERNEL_BLOCKWISE) == stof.STOF_ERR_UNSUPPORTED
+    assert _score(lib, fmt=half, H=4, Hkv=4, score=S(30.0, None, 0), which=stof.STOF_KERNEL_BLOCKWISE) == \
+        stof.STOF_ERR_UNSUPPORTED
 
 
 def test_bindings_refuse_host_tensors(lib):

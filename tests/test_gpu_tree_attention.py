@@ -108,7 +108,8 @@ def test_one_token(gpu_lib, dtype, d, length):
     Case(1, 8, 2, 1, d, [length], dtype, sees="chain", seed=length).run()
 
 
-@pytest.mark.parametrize("T,H,Hkv", [(1, 4, 4), (3, 6, 1), (16, 8, 2), (31, 8, 1), (33, 4, 1), (64, 16, 2), (100, 5, 5), (257, 2, 2)])
+@pytest.mark.parametrize("T,H,Hkv", [(1, 4, 4), (3, 6, 1), (16, 8, 2), (31, 8, 1), (33, 4, 1), (64, 16, 2), (100, 5, 5), (257, 2, 2),
+                                     (8, 4, 1), (16, 2, 1), (33, 1, 1), (130, 9, 1)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_trees_and_groups(gpu_lib, T, H, Hkv, d):
     """Rows of a group that fill part of a tile, one tile and several; bitsets of one and several words."""
@@ -136,6 +137,12 @@ def test_many_requests(gpu_lib):
     lens = rng.integers(0, 900, 450)
     lens[7] = 6000
     Case(450, 2, 2, 2, 64, lens, counts=rng.integers(0, 3, 450), seed=4).run()
+
+
+def test_more_row_tiles_than_go_together(gpu_lib):
+    """Nine and more row tiles per K/V head: two groups, the last one smaller; several shares and requests."""
+    Case(2, 10, 1, 116, 64, [0, 700], seed=21).run(planes={(0, 0), (0, 9), (1, 3), (1, 9)})
+    Case(1, 19, 1, 128, 128, [3000], seed=22).run(planes={(0, 0), (0, 7), (0, 8), (0, 18)})
 
 
 def test_a_long_cache(gpu_lib):
