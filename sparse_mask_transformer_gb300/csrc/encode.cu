@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kThreads) documents_count_kernel(const EncodeP
   extern __shared__ uint64_t s_words[];
   __shared__ ChunkState cs;
   __shared__ DocChunk dc;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  dependents_launch();
   const int tid = threadIdx.x;
   const long long chunk = blockIdx.x;
   if (chunk == 0 && tid < 8) p.counts[tid] = 0;  // the workspace's header: counts, error word, the attention kernel's counters
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kThreads) documents_write_kernel(const EncodeP
   const long long chunk = blockIdx.x;
   const ChunkGeom g = chunk_geom(p, chunk);
   document_tiles(p, ds, g, dc, cs, s_words, tid);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel has ended
+  dependents_wait();  // the first kernel has ended
   // full << 31 | partial OTs before the chunk; the last chunk also adds up all valid elements
   const bool last = chunk == p.n_chunks - 1;
   unsigned long long before = 0, nnz = 0;
@@ -1073,18 +1073,7 @@ cudaError_t launch_encode_documents(const EncodeParams& p_in, const EncodeGeom& 
     return cudaGetLastError();
   }
   documents_count_kernel<<<grid, kThreads, g.smem_bytes, s>>>(p, ds);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = g.smem_bytes;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, documents_write_kernel, p, ds);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_early(documents_write_kernel, dim3(grid), kThreads, g.smem_bytes, s, p, ds);
 }
 
 // ------------------------------------------------------------------------

@@ -28,6 +28,33 @@ int device_sm_count();
 // when it already succeeded on this device.
 bool once_per_device(const void* key, bool (*prepare)(const void*), const void* arg);
 
+// Launches kernel<<<grid, block, smem, s>>>(args...) so that it may be set up
+// while the stream's last kernel is still running (programmatic dependent
+// launch); the kernel calls dependents_wait() before it reads what that one
+// writes or writes what it reads.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
+}
+#ifdef __CUDACC__
+// Until every kernel this one may have been launched early beside has ended and its writes are visible.
+__device__ __forceinline__ void dependents_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// This kernel's CTAs are all running: the stream's next kernel may be set up.
+__device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 // ---------------------------------------------------------------- encoder
 // A chunk is one OT row band (bm mask rows) times `ct` consecutive OTs.
 struct EncodeGeom {

@@ -117,7 +117,7 @@ struct CacheSource {
   // Finds the requests at the workers' begins; CTA 0 reports bad requests and
   // leaves the line for combine_kernel.
   static __device__ void prologue(const Params& p, Shared& s) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // combine_kernel may be set up
+    dependents_launch();  // combine_kernel may be set up
     const int per = p.Hkv * p.row_groups;
     int all = 0, v = 0, at = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -305,10 +305,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   const int b = static_cast<int>(blockIdx.x) / per, item = static_cast<int>(blockIdx.x) - b * per;
   const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles, group = rt / p.row_group;
   const int r = static_cast<int>(blockIdx.y) * (4 / WPR) + warp / WPR, rr = rt * 128 + r, gq = rr / p.T, t = rr - gq * p.T;
+  dependents_wait();
   int ctx, count;
-  const bool active = request(p, b, ctx, count);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!active) return;
+  if (!request(p, b, ctx, count)) return;
   const int all = __ldcg(p.line + p.B), line = __ldcg(p.line + b);
   const int len = tiles_of(p, ctx + count) + kItemCost, share = share_of(p, all);
   const int at = line + (hk * p.row_groups + group) * len;
@@ -432,17 +431,9 @@ stof_status launch_tree(const void* q, const void* k, const void* v, const TreeP
   }
   if (st != STOF_OK) return st;
   const bool one = static_cast<long long>(planes) * p.rows >= kRowPerWarp;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(planes * p.row_tiles), static_cast<unsigned>(one ? (p.slot_rows + 3) / 4 : p.slot_rows));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, one ? combine_kernel<D, BF16, 1> : combine_kernel<D, BF16, 4>, p);
-  return record_cuda(e) == cudaSuccess && record_cuda(cudaGetLastError()) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
+  const dim3 grid(static_cast<unsigned>(planes * p.row_tiles), static_cast<unsigned>(one ? (p.slot_rows + 3) / 4 : p.slot_rows));
+  const cudaError_t e = launch_early(one ? combine_kernel<D, BF16, 1> : combine_kernel<D, BF16, 4>, grid, 128, 0, s, p);
+  return record_cuda(e) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
 
 }  // namespace
