@@ -167,8 +167,8 @@ struct FormatSource {
     return row.i < p.L;
   }
   template <int BN>
-  static __device__ void prefetch(const Params&, Row& row, const Item& x, int t, int n) {
-    if (t < n && t >= x.nf) {
+  static __device__ void prefetch(const Params&, Row& row, const Item& x, int t) {
+    if (t >= x.nf) {
       const int u = t - x.nf;
       const uint8_t* src = row.bits + static_cast<long long>(x.p0 + (BN == 64 ? u >> 1 : u)) * 2048 + (BN == 64 ? (u & 1) * 64 : 0);
 #pragma unroll

@@ -15,6 +15,9 @@
 //   warp 2 + g      score MMAs S = Q K^T and PV MMAs O += P V (P read from
 //                   TMEM), the scores of the next tile before the PV of this;
 //   warps 4 + 4 g ..  softmax, a thread per query row.
+// A segment's tiles go from the last to the first: the keys nearest to the
+// rows come first, so that with distance the running max is settled by the
+// first tile.
 // While one worker loads Q, starts or finishes a segment or waits for a tile,
 // the other one's tiles go on, so that short segments (a few tiles, as
 // packed documents and short caches give) cost little more than their tiles.
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&w.ring_free[slot]);
     return seg.n >= 0 ? Next::segment : Next::none;
   };
-  Segment<typename SRC::Item> seg;
+  Segment<typename SRC::Item> seg{};
   bool ok = true;
 
   if (warp < 4)
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int& ph = is_k ? pk : pv;
         const int depth = is_k ? Sh::K : Sh::V;
         uint64_t* full = (is_k ? w.k_full : w.v_full) + st;
-        const int row = SRC::tile_key(p, seg.item, t);
+        const int row = SRC::tile_key(p, seg.item, seg.n - 1 - t);
         if (i >= depth && !mbar_wait((is_k ? w.k_free : w.v_free) + st, ph ^ 1, abort_flag, kWaitNs)) return false;
         uint8_t* to = is_k ? s.k[g][st] : s.v[g][st];
         const CUtensorMap* map = is_k ? &tmK : &tmV;
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (SRC::kClearsV) {
         // V rows behind the request's last token may hold anything, and
         // 0 * NaN is NaN: clear them before the MMA reads the tile
-        const int end = SRC::tile_end(seg.item, t);
+        const int end = SRC::tile_end(seg.item, seg.n - 1 - t);
         if (end < BN) {
 #pragma unroll 1
           for (int x = lane + end * 8; x < BN * 8; x += 32)
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float slope = 0.f;
       if (MODE == MODE_DISTANCE && p.slopes && live) slope = __ldg(p.slopes + row.head) * kLog2e;
       float m_ref = -INFINITY, l = 0.f;
-      SRC::template prefetch<BN>(p, row, seg.item, 0, seg.n);
+      SRC::template prefetch<BN>(p, row, seg.item, seg.n - 1);
 #pragma unroll 1
       for (int t = 0; t < seg.n; ++t, ++j) {
         if (!warp_wait(&w.s_full, j & 1, abort_flag)) { ok = false; break; }
@@ -403,10 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_scores(tSr, sr);
           tc_fence_before();
           mbar_arrive(&w.s_free);  // the scores are in registers: S may be overwritten
-          const bool partial = SRC::partial(seg.item, t);
+          const int tile = seg.n - 1 - t;
+          const bool partial = SRC::partial(seg.item, tile);
           uint32_t bits[CHUNKS] = {};
-          if (partial) SRC::template bits<BN>(p, row, seg.item, t, KEYS * part, bits);
-          SRC::template prefetch<BN>(p, row, seg.item, t + 1, seg.n);
+          if (partial) SRC::template bits<BN>(p, row, seg.item, tile, KEYS * part, bits);
+          SRC::template prefetch<BN>(p, row, seg.item, tile - 1);
           uint32_t pk[CHUNKS][16];
           float alpha = 1.f;
           // the max mt of the tile's scores (log2 units) becomes the
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               cap_scores(sr, p.k, __all_sync(0xffffffffu, row_within(sr, p.k.lim)));
               c = 1.f;
             }
-            SRC::template lower<BN>(p, row, seg.item, t, KEYS * part, sr, c, slope);
+            SRC::template lower<BN>(p, row, seg.item, tile, KEYS * part, sr, c, slope);
             if (partial) mask_scores(sr, bits);
             const float nmu = raise_ref(row_max(sr));
             l += exp_pack<CHUNKS, BF16>(sr, 1.f, nmu, pk);

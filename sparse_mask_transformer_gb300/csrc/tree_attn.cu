@@ -222,7 +222,7 @@ struct CacheSource {
     return live;
   }
   template <int BN>
-  static __device__ void prefetch(const Params&, Row&, const Item&, int, int) {}
+  static __device__ void prefetch(const Params&, Row&, const Item&, int) {}
   static __device__ bool partial(const Item& x, int t) { return (x.t0 + t + 1) * x.tile > x.ctx; }  // it has drafted keys
   // Bits of drafted tokens 32 x .. 32 x + 31 that the row sees.
   static __device__ uint32_t seen(const Params& p, const Row& row, const Item& x, int word) {
