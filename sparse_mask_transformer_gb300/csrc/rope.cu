@@ -221,7 +221,13 @@ cudaError_t launch(RopeParams& p, long long tokens, cudaStream_t s) {
   const long long want = 870ll * device_sm_count();
   long long slots = (want + tokens * units - 1) / (tokens * units);
   if (slots > heads) slots = heads;
-  while (heads % slots) ++slots;  // as many heads for every slot (3 slots for 32 heads: 41.5 us, 4: 36.2)
+  // as many heads for every slot where a number up to twice as large divides them (3 slots for 32 heads: 41.5 us, 4: 36.2)
+  for (long long more = slots; more <= 2 * slots; ++more) {
+    if (heads % more == 0) {
+      slots = more;
+      break;
+    }
+  }
   p.slots = static_cast<int>(slots);
   p.n_threads = static_cast<uint32_t>(tokens * units * slots);
   const unsigned grid = static_cast<unsigned>((tokens * units * slots + kThreadsRope - 1) / kThreadsRope);

@@ -215,3 +215,16 @@ def test_graph_replay_and_streams(gpu_lib):
         stof.stof_rope_fwd(plan, q, None, None, y, None, None, positions=pos, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], o) and torch.equal(outs[1], o)
+
+
+@pytest.mark.parametrize("d,rot", [(64, 64), (6, 2)])
+def test_head_counts_that_nothing_divides(gpu_lib, d, rot):
+    """Head slots need not divide the heads: one slot per head would be the only divisor."""
+    B, H, Hkv, T, dtype = 3, 60, 1, 401, torch.float16
+    plan = stof.stof_rope_plan_init(rot)
+    q, k = rand((B, H, T, d), dtype, 30), rand((B, Hkv, T, d), dtype, 31)
+    qo, ko = torch.full_like(q, float("nan")), torch.full_like(k, float("nan"))
+    stof.stof_rope_fwd(plan, q, k, None, qo, ko, None)
+    pos = np.tile(np.arange(T), (B, 1))
+    for x, y in ((q, qo), (k, ko)):
+        check(y, *turned(f64(x), pos, frequencies(rot), rot, False), dtype)
