@@ -341,7 +341,7 @@ stof_status stof_mha_fwd_cross(const void* q, const void* k, const void* v, stof
 typedef struct {
   float softcap;        /* > 0: score <- softcap * tanh(score / softcap); 0: none */
   const float* slopes;  /* device fp32 [H] (4-byte aligned) or NULL: then score <- score - slopes[h] * |i + q_start - j|,
-                           finite slopes of either sign */
+                           slopes of either sign, magnitude below 2^64 */
   int32_t q_start;      /* position of query row 0 among the keys, in [-2^30, 2^30]; read only with slopes */
 } stof_score;
 
@@ -380,7 +380,7 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
  * drafted tokens' own K and V, for instance by stof_rope_fwd() with rows =
  * lens); drafted token t sees every committed row and the drafted rows u
  * whose bit is set in its tree row.
- *   q, o       device [B][H][T][d], dt; o is written.
+ *   q, o       device [B][H][T][d], dt; o is written and overlaps no input.
  *   k, v       device [B][Hkv][cap][d], dt; H a multiple of Hkv.  Rows from
  *              lens[b] + counts[b] on are not used, whatever they hold; the
  *              V rows before them have to be finite (one that a token does

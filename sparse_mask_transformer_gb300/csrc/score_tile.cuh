@@ -154,15 +154,16 @@ __device__ __forceinline__ void lower_by_distance(uint32_t (&sr)[CHUNKS][32], fl
 }
 
 // The same with the keys' own positions: lane x holds at[i] = position of key
-// 32 i + x, minus j0.  A warp-wide call.
+// 32 i + x.  The positions are any, so they are subtracted as integers (the
+// difference of two neighbours at 2 10^9 would be lost in fp32).  A warp-wide call.
 template <int CHUNKS>
-__device__ __forceinline__ void lower_by_positions(uint32_t (&sr)[CHUNKS][32], float c, float slope, float rel,
-                                                   const float (&at)[CHUNKS]) {
+__device__ __forceinline__ void lower_by_positions(uint32_t (&sr)[CHUNKS][32], float c, float slope, int pos,
+                                                   const int (&at)[CHUNKS]) {
 #pragma unroll
   for (int cc = 0; cc < CHUNKS; ++cc)
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      const float d = fabsf(rel - __shfl_sync(0xffffffffu, at[cc], i));
+      const float d = static_cast<float>(__sad(pos, __shfl_sync(0xffffffffu, at[cc], i), 0u));  // |pos - at|, 32 bits unsigned
       sr[cc][i] = __float_as_uint(fmaf(__uint_as_float(sr[cc][i]), c, -slope * d));
     }
 }

@@ -142,7 +142,7 @@ struct CacheSource {
       begin[g] = x < p.shares ? min(x * share, all) : all;
       if (threadIdx.x == 0) {
         s.begin[g] = begin[g];
-        s.end[g] = min(begin[g] + share, all);
+        s.end[g] = begin[g] + min(share, all - begin[g]);
       }
     }
     int base = 0;
@@ -252,18 +252,16 @@ struct CacheSource {
   static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, int first, uint32_t (&sr)[CHUNKS][32],
                                float c, float slope) {
     const int j0 = (x.t0 + t) * BN + first;
-    const long long rel = static_cast<long long>(row.pos) - j0;
     if (p.positions && partial(x, t)) {
-      float at[CHUNKS];  // position of key 32 i + lane of the tile
+      int at[CHUNKS];  // position of key 32 i + lane of the tile
 #pragma unroll
       for (int i = 0; i < CHUNKS; ++i) {
-        const int key = 32 * i + static_cast<int>(threadIdx.x & 31), u = j0 + key - x.ctx;
-        long long pos = key;
-        if (u >= 0) pos = u < x.count ? static_cast<long long>(__ldg(p.positions + static_cast<size_t>(x.b) * p.T + u)) - j0 : 0;
-        at[i] = static_cast<float>(pos);
+        const int key = j0 + 32 * i + static_cast<int>(threadIdx.x & 31), u = key - x.ctx;
+        at[i] = u < 0 ? key : (u < x.count ? __ldg(p.positions + static_cast<size_t>(x.b) * p.T + u) : 0);
       }
-      lower_by_positions(sr, c, slope, static_cast<float>(rel), at);
+      lower_by_positions(sr, c, slope, row.pos, at);
     } else {
+      const long long rel = static_cast<long long>(row.pos) - j0;
       lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= CHUNKS * 32 - 1));
     }
   }

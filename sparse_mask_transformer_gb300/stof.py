@@ -41,6 +41,7 @@ STOF_DEVERR_LOOKBACK_TIMEOUT = 0x1
 STOF_DEVERR_PIPE_TIMEOUT = 0x2
 STOF_DEVERR_BAD_FORMAT = 0x4
 STOF_DEVERR_BAD_LENGTH = 0x8
+STOF_TREE_MAX_TOKENS = 1024
 
 STOF_ROPE_PLAIN = 0
 STOF_ROPE_LINEAR = 1

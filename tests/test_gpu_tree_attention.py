@@ -233,3 +233,44 @@ def test_two_streams_with_their_own_workspaces(gpu_lib):
     torch.cuda.synchronize()
     for c, o in zip(cs, oo):
         c.check(o)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H", [2, 40])
+def test_far_positions_are_subtracted_exactly(gpu_lib, d, H):
+    """Drafted tokens at positions near 2^31, whose neighbours fp32 cannot tell apart; and at the two ends of 32 bits."""
+    T = 12
+    c = Case(2, H, 1, T, d, [0, 0], torch.float16, slopes=head_slopes(H), seed=13)
+    c.positions = 2_000_000_000 + np.arange(T)[None, :] + np.array([[0], [77]])
+    c.run()
+    c = Case(1, H, 1, T, d, [0], torch.float16, slopes=[2.0 ** -31] * H, seed=14)
+    c.positions = np.where(np.arange(T) % 3 == 0, -2 ** 31, 2 ** 31 - 1 - np.arange(T))[None, :]
+    c.run()
+
+
+def test_the_most_drafted_tokens(gpu_lib):
+    T = stof.STOF_TREE_MAX_TOKENS
+    Case(1, 2, 1, T, 64, [100], seed=15, counts=[T - 1]).run()
+    Case(1, 1, 1, T, 128, [33], seed=16, sees="chain").run()
+
+
+def test_two_graphs_that_share_a_workspace_in_turn(gpu_lib):
+    cs = [Case(2, 8, 2, 4, 64, [1000, 100], seed=17), Case(2, 8, 2, 4, 64, [3, 2500], seed=18)]
+    aa = [c.args() for c in cs]
+    oo = [torch.full(c.q.shape, 5.0, dtype=c.dtype, device="cuda") for c in cs]
+    graphs = []
+    for c, a, o in zip(cs, aa, oo):
+        a["ws"] = aa[0]["ws"]
+        c.call(a, o)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.call(a, o)
+    for o in oo:
+        o.fill_(5.0)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for c, o in zip(cs, oo):
+        c.check(o)
