@@ -650,6 +650,9 @@ __global__ void __launch_bounds__(kThreads) encode_documents_kernel(const Encode
 // word, the second adds up the words before its chunk and writes.  The OTs
 // are classified in both, in the second while the first still runs
 // (programmatic dependent launch), and no memory has to be cleared first.
+// Two kernels and the single-pass one, packed documents in 128 x 128 OTs: 32
+// chunks 8.9 and 12.4 us, 256 12.2 and 15.5, 4096 63.8 and 67.5, 8192 110 to 126
+// and 117 to 121, 16384 278 and 236 (each chunk reads all counts before it).
 constexpr int kDirectChunks = 4096;
 
 // valid elements (2^18 at most) | full OTs | partial OTs of a chunk

@@ -11,11 +11,11 @@
 // of a K/V head, up to kRowGroup of them, go along a share together, each
 // with a worker of its own (two workers per SM, scored_kernel.cuh): their
 // neighbours' requests for the same K/V tiles are then L2 hits.  (One row tile
-// after the other read the cache once per row tile: 524 us instead of @LONG@
+// after the other read the cache once per row tile: 524 us instead of 355
 // for 512 rows per K/V head over 2 x 131000 keys.)  A head whose tiles lie in
-// one share is finished there; the others leave partial rows (O relative to the rows' max, max and sum) in the workspace,
-// which combine_kernel merges in the order of the keys: the result does not
-// depend on timing.  A worker has at most one item that began before its
+// one share is finished there; the others leave partial rows (O relative to
+// the rows' max, max and sum) in the workspace, which combine_kernel merges in
+// the order of the keys: the result does not depend on timing.  A worker has at most one item that began before its
 // share and one that goes on after it: two slots.
 #include <cmath>
 
@@ -289,6 +289,14 @@ struct CacheSource {
   }
 };
 
+// A row is merged by four warps while the call has fewer rows than 128 times
+// the shares that a run lies in, else by one: many parts take one warp long,
+// many rows keep the SMs busy without more warps.  d = 128, one warp and four:
+// 32 rows of 38 shares each 40.0 and 31.8 us (the whole call), 1024 rows of 38
+// shares 46.9 and 40.7, 640 of 7.6 36.6 and 35.3; 1024 of 4.8 30.6 and 31.3,
+// 4096 of 9.5 73.5 and 78.0, 16384 of 1.2 61.5 and 84.6.
+constexpr int kRowsPerShare = 128;
+
 // Merges the partial rows of the runs that lie in several shares:
 // O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  WPR warps per query row,
 // warp x of a row the parts x, x + WPR, ..., eight of them in flight; four
@@ -390,11 +398,6 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   }
 }
 
-// Above this many query rows of the call a row is merged by one warp, below by
-// four: few rows have many parts each (a share per worker), many rows few.
-// Measured: @MERGE@
-constexpr long long kRowPerWarp = 1024;
-
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Copies of Q's rows in a tile, each with a part of its keys: four at d = 64
@@ -428,7 +431,7 @@ stof_status launch_tree(const void* q, const void* k, const void* v, const TreeP
     default: st = launch_mode<D, BF16, MODE_DISTANCE>(mq, mk, mv, p, s); break;
   }
   if (st != STOF_OK) return st;
-  const bool one = static_cast<long long>(planes) * p.rows >= kRowPerWarp;
+  const bool one = planes * p.rows * planes * p.row_groups >= static_cast<uint64_t>(kRowsPerShare) * p.shares;
   const dim3 grid(static_cast<unsigned>(planes * p.row_tiles), static_cast<unsigned>(one ? (p.slot_rows + 3) / 4 : p.slot_rows));
   const cudaError_t e = launch_early(one ? combine_kernel<D, BF16, 1> : combine_kernel<D, BF16, 4>, grid, 128, 0, s, p);
   return record_cuda(e) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;

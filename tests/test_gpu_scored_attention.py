@@ -186,3 +186,27 @@ def test_documents_then_attention_without_a_host_round_trip(gpu_lib):
         masks = ((doc[:, :, None] == doc[:, None, :]) & (doc[:, :, None] >= 0) & np.tril(np.ones((L, L), dtype=bool))).astype(np.uint8)
         check(o, q, k, v, masks, 1, 0, 40.0, head_slopes(H))
         assert torch.all(o[1, :, 580:] == 0)
+
+
+@pytest.mark.parametrize("which", [ROW, BLOCK])
+def test_calls_that_share_a_format_may_overlap(gpu_lib, which):
+    """Two streams, one format, calls queued behind one another on both; every result as alone."""
+    B, H, Hkv, L, d = 1, 8, 2, 1500, 64
+    masks = np.tril(np.ones((1, L, L), dtype=np.uint8))
+    fmt, ws, _ = gpu_encode(torch.from_numpy(masks).cuda(), 128, 128)
+    slopes = torch.tensor(head_slopes(H), dtype=torch.float32, device="cuda")
+    sets = [[t.cuda() for t in tensors(B, H, Hkv, L, L, d, torch.bfloat16, seed)] for seed in (20, 21)]
+    scores = [stof.Score(30.0), stof.Score(0.0, slopes)]
+    want, got = ([torch.full_like(s[0], float("nan")) for s in sets] for _ in range(2))
+    for (q, k, v), sc, o in zip(sets, scores, want):
+        stof.stof_mha_fwd_score(q, k, v, fmt, 0.125, sc, 0, 0, which, o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(6):
+        for (q, k, v), sc, o, s in zip(sets, scores, got, streams):
+            stof.stof_mha_fwd_score(q, k, v, fmt, 0.125, sc, 0, 0, which, o, stream=s)
+    torch.cuda.synchronize()
+    stof.stof_format_sync(fmt)
+    assert fmt.device_error == 0
+    for a, b in zip(want, got):
+        assert torch.equal(a, b) and torch.isfinite(a.float()).all()
