@@ -334,14 +334,14 @@ def stof_encode_documents(q_doc: torch.Tensor, k_doc: torch.Tensor, q_order: tor
     Query i sees key j iff q_doc[i] == k_doc[j] >= 0 and k_order[j] <= q_order[i]."""
     where = "stof_encode_documents"
     device = _device_of(where, q_doc, k_doc, q_order, k_order, workspace)
-    if q_doc.dim() != 2 or k_doc.dim() != 2 or q_doc.shape[0] != k_doc.shape[0]:
+    qs, ks = q_doc.shape, k_doc.shape
+    if len(qs) != 2 or len(ks) != 2 or qs[0] != ks[0]:
         raise StofError(STOF_ERR_SHAPE, f"{where}: q_doc must be [n_masks, lq] and k_doc [n_masks, lk]")
-    (n, lq), (_, lk) = q_doc.shape, k_doc.shape
+    (n, lq), lk = qs, ks[1]
     fmt = fmt if fmt is not None else stof_format()
-    _launch(where, device, stream, load_library().stof_encode_documents, _int32(where, "q_doc", q_doc, (n, lq)),
-            _int32(where, "k_doc", k_doc, (n, lk)), _int32(where, "q_order", q_order, (n, lq)),
-            _int32(where, "k_order", k_order, (n, lk)), n, lq, lk, bm, bn, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), ctypes.byref(fmt))
+    _launch(where, device, stream, load_library().stof_encode_documents, _int32(where, "q_doc", q_doc, qs),
+            _int32(where, "k_doc", k_doc, ks), _int32(where, "q_order", q_order, qs), _int32(where, "k_order", k_order, ks),
+            n, lq, lk, bm, bn, workspace.data_ptr(), workspace.nbytes, ctypes.byref(fmt))
     return fmt
 
 
@@ -430,13 +430,7 @@ def stof_mha_fwd_score(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, fmt: s
     STOF_KERNEL_AUTO needs no synced format here."""
     where = "stof_mha_fwd_score"
     device = _device_of(where, q, k, v, o, score.slopes if score is not None else None)
-    if q.dim() != 4 or k.dim() != 4:
-        raise StofError(STOF_ERR_SHAPE, f"{where}: q, k must be [B, heads, L, d]")
-    B, H, Lq, d = q.shape
-    Hkv, Lk = k.shape[1], k.shape[2]
-    if (o.shape != q.shape or k.shape != (B, Hkv, Lk, d) or v.shape != k.shape
-            or any(t.dtype != q.dtype or not t.is_contiguous() for t in (q, k, v, o))):
-        raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, Lq, d] and k, v [B, Hkv, Lk, d], contiguous")
+    B, H, Lq, d, Hkv, Lk = _heads_of(where, q, k, v, o)
     _launch(where, device, stream, load_library().stof_mha_fwd_score, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             _dtype_code(q), B, H, Hkv, Lq, Lk, d, float(scale), None if score is None else ctypes.byref(score.as_c(where, H)),
             ctypes.byref(fmt), mask_stride_b, mask_stride_h, which, o.data_ptr())
@@ -456,18 +450,14 @@ def stof_tree_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens: 
     where = "stof_tree_attn_fwd"
     slopes = score.slopes if score is not None else None
     device = _device_of(where, q, k, v, o, lens, workspace, tree, counts, positions, slopes, device_error)
-    if q.dim() != 4 or k.dim() != 4:
-        raise StofError(STOF_ERR_SHAPE, f"{where}: q, k must be [B, heads, rows, d]")
-    B, H, T, d = q.shape
-    Hkv, cap = k.shape[1], k.shape[2]
-    if (o.shape != q.shape or k.shape != (B, Hkv, cap, d) or v.shape != k.shape
-            or any(t.dtype != q.dtype or not t.is_contiguous() for t in (q, k, v, o))):
-        raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, T, d] and k, v [B, Hkv, cap, d], contiguous")
+    B, H, T, d, Hkv, cap = _heads_of(where, q, k, v, o)
     _launch(where, device, stream, load_library().stof_tree_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            _dtype_code(q), B, H, Hkv, T, d, cap, _int32(where, "lens", lens, (B,)), _int32(where, "counts", counts, (B,)),
-            _int32(where, "tree", tree, (B, T, (T + 31) // 32)), _int32(where, "positions", positions, (B, T)), float(scale),
+            _dtype_code(q), B, H, Hkv, T, d, cap, _int32(where, "lens", lens, (B,)),
+            None if counts is None else _int32(where, "counts", counts, (B,)),
+            None if tree is None else _int32(where, "tree", tree, (B, T, (T + 31) // 32)),
+            None if positions is None else _int32(where, "positions", positions, (B, T)), float(scale),
             None if score is None else ctypes.byref(score.as_c(where, H)), o.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _error_word(where, device_error))
+            workspace.nbytes, None if device_error is None else _error_word(where, device_error))
     return o
 
 
@@ -631,6 +621,19 @@ def _device_of(where: str, *tensors) -> int:
     if device < 0:
         raise StofError(STOF_ERR_INVALID_ARG, f"{where}: no tensor given")
     return device
+
+
+def _heads_of(where: str, q, k, v, o) -> tuple:
+    """B, H, rows of q, d, Hkv, rows of k of contiguous q, o [B, H, ., d] and k, v [B, Hkv, ., d] of one dtype."""
+    qs, ks, dt = q.shape, k.shape, q.dtype
+    if len(qs) != 4 or len(ks) != 4:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q, k must be [B, heads, rows, d]")
+    B, H, n, d = qs
+    kb, Hkv, m, kd = ks
+    if (kb != B or kd != d or o.shape != qs or v.shape != ks or k.dtype != dt or v.dtype != dt or o.dtype != dt
+            or not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and o.is_contiguous())):
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, rows, d] and k, v [B, Hkv, rows, d], contiguous, one dtype")
+    return B, H, n, d, Hkv, m
 
 
 def _launch(where: str, device: int, stream, function, *args) -> None:
