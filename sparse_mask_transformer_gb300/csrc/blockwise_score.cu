@@ -185,9 +185,9 @@ struct FormatSource {
       b[cc] = row.nb[4 * cc] | (row.nb[4 * cc + 1] << 8) | (row.nb[4 * cc + 2] << 16) | (row.nb[4 * cc + 3] << 24);
   }
   template <int BN>
-  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, int, uint32_t (&sr)[BN / 32][32],
-                               float c, float slope) {
-    const int rel = row.pos - tile_key(p, x, t);
+  static __device__ void lower(const Params&, const Row& row, const Item&, int, int key, uint32_t (&sr)[BN / 32][32], float c,
+                               float slope) {
+    const int rel = row.pos - key;
     lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= BN - 1));
   }
   static __device__ bool whole(const Item&) { return true; }

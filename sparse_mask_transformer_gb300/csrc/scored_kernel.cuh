@@ -108,6 +108,9 @@ struct Worker {
   uint64_t s_full, s_free, p_full, pv_done, merge, drain;
   uint64_t ring_full[kRing], ring_free[kRing];
   Segment<typename SRC::Item> ring[kRing];  // n < 0: no more segments
+  // First keys of the K tiles, for the distance.  The K tile 8 later is copied
+  // once the score MMA 5 later is done, and so the softmax 4 later has begun.
+  int key[8];
 };
 
 template <class SRC, int D>
@@ -231,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i >= depth && !mbar_wait((is_k ? w.k_free : w.v_free) + st, ph ^ 1, abort_flag, kWaitNs)) return false;
         uint8_t* to = is_k ? s.k[g][st] : s.v[g][st];
         const CUtensorMap* map = is_k ? &tmK : &tmV;
+        if (MODE == MODE_DISTANCE && is_k) w.key[i & 7] = row;
         mbar_arrive_expect_tx(full, Sh::STAGE);
 #pragma unroll
         for (int r = 0; r < REGIONS; ++r) tma_load_3d(to + r * Sh::ATOM, map, full, 64 * r, row, seg.kv_plane);
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               cap_scores(sr, p.k, __all_sync(0xffffffffu, row_within(sr, p.k.lim)));
               c = 1.f;
             }
-            SRC::template lower<BN>(p, row, seg.item, tile, KEYS * part, sr, c, slope);
+            SRC::template lower<BN>(p, row, seg.item, tile, w.key[j & 7] + KEYS * part, sr, c, slope);
             if (partial) mask_scores(sr, bits);
             const float nmu = raise_ref(row_max(sr));
             l += exp_pack<CHUNKS, BF16>(sr, 1.f, nmu, pk);

@@ -249,9 +249,8 @@ struct CacheSource {
     }
   }
   template <int BN, int CHUNKS>
-  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, int first, uint32_t (&sr)[CHUNKS][32],
+  static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, int j0, uint32_t (&sr)[CHUNKS][32],
                                float c, float slope) {
-    const int j0 = (x.t0 + t) * BN + first;
     if (p.positions && partial(x, t)) {
       int at[CHUNKS];  // position of key 32 i + lane of the tile
 #pragma unroll
