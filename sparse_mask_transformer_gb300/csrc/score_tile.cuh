@@ -168,10 +168,11 @@ __device__ __forceinline__ void lower_by_positions(uint32_t (&sr)[CHUNKS][32], f
     }
 }
 
-// exp_pack of capped scores straight from the products: P = 2^(s P(s^2) + nmu).
-template <int CHUNKS, bool BF16>
+// exp_pack of capped scores straight from the products: P = 2^(s P(s^2) + nmu),
+// MASKED: 0 for keys whose bit is not set.
+template <int CHUNKS, bool BF16, bool MASKED>
 __device__ __forceinline__ float exp_pack_capped(const uint32_t (&sr)[CHUNKS][32], const ScoreConst& k, float nmu,
-                                                 uint32_t (&pk)[CHUNKS][16]) {
+                                                 uint32_t (&pk)[CHUNKS][16], const uint32_t (&bits)[CHUNKS]) {
   float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int cc = 0; cc < CHUNKS; ++cc)
@@ -181,6 +182,13 @@ __device__ __forceinline__ float exp_pack_capped(const uint32_t (&sr)[CHUNKS][32
       float x0, x1;
       cap_bracket(k, s0, s1, x0, x1);
       ffma2(x0, x1, x0, x1, s0, s1, nmu, nmu);
+      if (MASKED) {
+        uint32_t m0 = __float_as_uint(x0), m1 = __float_as_uint(x1);
+        keep_if_set(m0, bits[cc], 1u << i);
+        keep_if_set(m1, bits[cc], 2u << i);
+        x0 = __uint_as_float(m0);
+        x1 = __uint_as_float(m1);
+      }
       const float e0 = ex2(x0), e1 = ex2(x1);
       fadd2(ls[((i >> 1) & 1) * 2], ls[((i >> 1) & 1) * 2 + 1], e0, e1);
       pk[cc][i / 2] = pack2<BF16>(e0, e1);

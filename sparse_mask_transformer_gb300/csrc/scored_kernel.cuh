@@ -437,31 +437,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             // larger cap to MODE_DISTANCE), and bf16 and fp32 hold 2^-a to
             // 2^a: no running max, the reference is 0 throughout.
             m_ref = 0.f;
-            bool within = true;
-            if (CHUNKS > 2 || partial) within = __all_sync(0xffffffffu, row_within(sr, p.k.lim));
-            if (!partial && CHUNKS > 2 && within) {
-              l += exp_pack_capped<CHUNKS, BF16>(sr, p.k, 0.f, pk);
-            } else if (!partial && CHUNKS == 2) {
-              // the polynomial for all, while its range is being checked (the
-              // scores stay: registers for 64 of them, not for 128)
-              const float sum = exp_pack_capped<CHUNKS, BF16>(sr, p.k, 0.f, pk);
-              if (__all_sync(0xffffffffu, row_within(sr, p.k.lim))) {
-                l += sum;
+            if constexpr (CHUNKS > 2) {
+              const bool within = __all_sync(0xffffffffu, row_within(sr, p.k.lim));
+              if (!partial && within) {
+                l += exp_pack_capped<CHUNKS, BF16, false>(sr, p.k, 0.f, pk, bits);
               } else {
-                cap_scores(sr, p.k, false);
+                cap_scores(sr, p.k, within);
+                if (partial) mask_scores(sr, bits);
                 l += exp_pack<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
               }
             } else {
-              cap_scores(sr, p.k, within);
-              if (partial) mask_scores(sr, bits);
-              l += exp_pack<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
+              // up to 64 scores: the polynomial for all while its range is
+              // being checked (there are registers to keep the scores; with
+              // 128 of them this spills 530 bytes a thread)
+              float sum = partial ? exp_pack_capped<CHUNKS, BF16, true>(sr, p.k, 0.f, pk, bits)
+                                  : exp_pack_capped<CHUNKS, BF16, false>(sr, p.k, 0.f, pk, bits);
+              if (!__all_sync(0xffffffffu, row_within(sr, p.k.lim))) {
+                cap_scores(sr, p.k, false);
+                if (partial) mask_scores(sr, bits);
+                sum = exp_pack<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
+              }
+              l += sum;
             }
           } else if constexpr (MODE == MODE_CAP) {
             const bool within = __all_sync(0xffffffffu, row_within(sr, p.k.lim));
             if (within && !partial && p.k.k1 > 0.f) {
               // the cap is increasing: its max is that of the largest product
               const float nmu = raise_ref(cap_poly(p.k, row_max(sr)));
-              l += exp_pack_capped<CHUNKS, BF16>(sr, p.k, nmu, pk);
+              l += exp_pack_capped<CHUNKS, BF16, false>(sr, p.k, nmu, pk, bits);
             } else {
               cap_scores(sr, p.k, within);
               if (partial) mask_scores(sr, bits);
