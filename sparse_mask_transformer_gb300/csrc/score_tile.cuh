@@ -168,10 +168,42 @@ __device__ __forceinline__ void lower_by_positions(uint32_t (&sr)[CHUNKS][32], f
     }
 }
 
-// exp_pack of capped scores straight from the products: P = 2^(s P(s^2) + nmu),
+// The sum of P that O is divided by is that of the rounded values which the
+// tensor cores multiply: a rounding d of p_j then moves O by d (V_j - O), not
+// d V_j, so a key that has nearly all the weight is not rounded at all.
+// (Adds both halves of a pair, exactly widened, to s0 and s1.)
+template <bool BF16>
+__device__ __forceinline__ void add_pair(float& s0, float& s1, uint32_t pair) {
+  if constexpr (BF16)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
+        : "+f"(s0), "+f"(s1)
+        : "r"(pair));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.f16 %0, l, %0;\n\tadd.f32.f16 %1, h, %1;\n\t}"
+        : "+f"(s0), "+f"(s1)
+        : "r"(pair));
+}
+
+// P = 2^(c s + nmu) of the row's scores, rounded and packed; the sum of the rounded values.
+template <int CHUNKS, bool BF16>
+__device__ __forceinline__ float exp_row(const uint32_t (&sr)[CHUNKS][32], float c, float nmu, uint32_t (&pk)[CHUNKS][16]) {
+  float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int cc = 0; cc < CHUNKS; ++cc)
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float x0, x1;
+      ffma2(x0, x1, __uint_as_float(sr[cc][i]), __uint_as_float(sr[cc][i + 1]), c, c, nmu, nmu);
+      pk[cc][i / 2] = pack2<BF16>(ex2(x0), ex2(x1));
+      add_pair<BF16>(ls[((i >> 1) & 1) * 2], ls[((i >> 1) & 1) * 2 + 1], pk[cc][i / 2]);
+    }
+  return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+}
+
+// exp_row of capped scores straight from the products: P = 2^(s P(s^2) + nmu),
 // MASKED: 0 for keys whose bit is not set.
 template <int CHUNKS, bool BF16, bool MASKED>
-__device__ __forceinline__ float exp_pack_capped(const uint32_t (&sr)[CHUNKS][32], const ScoreConst& k, float nmu,
+__device__ __forceinline__ float exp_row_capped(const uint32_t (&sr)[CHUNKS][32], const ScoreConst& k, float nmu,
                                                  uint32_t (&pk)[CHUNKS][16], const uint32_t (&bits)[CHUNKS]) {
   float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -189,9 +221,8 @@ __device__ __forceinline__ float exp_pack_capped(const uint32_t (&sr)[CHUNKS][32
         x0 = __uint_as_float(m0);
         x1 = __uint_as_float(m1);
       }
-      const float e0 = ex2(x0), e1 = ex2(x1);
-      fadd2(ls[((i >> 1) & 1) * 2], ls[((i >> 1) & 1) * 2 + 1], e0, e1);
-      pk[cc][i / 2] = pack2<BF16>(e0, e1);
+      pk[cc][i / 2] = pack2<BF16>(ex2(x0), ex2(x1));
+      add_pair<BF16>(ls[((i >> 1) & 1) * 2], ls[((i >> 1) & 1) * 2 + 1], pk[cc][i / 2]);
     }
   return (ls[0] + ls[1]) + (ls[2] + ls[3]);
 }

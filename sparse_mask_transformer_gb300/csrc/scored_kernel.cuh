@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (MODE == MODE_PLAIN) {
             if (partial) mask_scores(sr, bits);
             const float nmu = raise_ref(row_max(sr) * p.k.c);
-            l += exp_pack<CHUNKS, BF16>(sr, p.k.c, nmu, pk);
+            l += exp_row<CHUNKS, BF16>(sr, p.k.c, nmu, pk);
           } else if constexpr (MODE == MODE_CAP && BF16) {
             // Capped scores lie within a of 0 (log2 units; the host sends a
             // larger cap to MODE_DISTANCE), and bf16 and fp32 hold 2^-a to
@@ -440,22 +440,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (CHUNKS > 2) {
               const bool within = __all_sync(0xffffffffu, row_within(sr, p.k.lim));
               if (!partial && within) {
-                l += exp_pack_capped<CHUNKS, BF16, false>(sr, p.k, 0.f, pk, bits);
+                l += exp_row_capped<CHUNKS, BF16, false>(sr, p.k, 0.f, pk, bits);
               } else {
                 cap_scores(sr, p.k, within);
                 if (partial) mask_scores(sr, bits);
-                l += exp_pack<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
+                l += exp_row<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
               }
             } else {
               // up to 64 scores: the polynomial for all while its range is
               // being checked (there are registers to keep the scores; with
               // 128 of them this spills 530 bytes a thread)
-              float sum = partial ? exp_pack_capped<CHUNKS, BF16, true>(sr, p.k, 0.f, pk, bits)
-                                  : exp_pack_capped<CHUNKS, BF16, false>(sr, p.k, 0.f, pk, bits);
+              float sum = partial ? exp_row_capped<CHUNKS, BF16, true>(sr, p.k, 0.f, pk, bits)
+                                  : exp_row_capped<CHUNKS, BF16, false>(sr, p.k, 0.f, pk, bits);
               if (!__all_sync(0xffffffffu, row_within(sr, p.k.lim))) {
                 cap_scores(sr, p.k, false);
                 if (partial) mask_scores(sr, bits);
-                sum = exp_pack<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
+                sum = exp_row<CHUNKS, BF16>(sr, 1.f, 0.f, pk);
               }
               l += sum;
             }
@@ -464,12 +464,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (within && !partial && p.k.k1 > 0.f) {
               // the cap is increasing: its max is that of the largest product
               const float nmu = raise_ref(cap_poly(p.k, row_max(sr)));
-              l += exp_pack_capped<CHUNKS, BF16, false>(sr, p.k, nmu, pk, bits);
+              l += exp_row_capped<CHUNKS, BF16, false>(sr, p.k, nmu, pk, bits);
             } else {
               cap_scores(sr, p.k, within);
               if (partial) mask_scores(sr, bits);
               const float nmu = raise_ref(row_max(sr));
-              l += exp_pack<CHUNKS, BF16>(sr, 1.f, nmu, pk);
+              l += exp_row<CHUNKS, BF16>(sr, 1.f, nmu, pk);
             }
           } else {
             float c = p.k.c;
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             SRC::template lower<BN>(p, row, seg.item, tile, w.key[j & 7] + KEYS * part, sr, c, slope);
             if (partial) mask_scores(sr, bits);
             const float nmu = raise_ref(row_max(sr));
-            l += exp_pack<CHUNKS, BF16>(sr, 1.f, nmu, pk);
+            l += exp_row<CHUNKS, BF16>(sr, 1.f, nmu, pk);
           }
           if (t > 0) {
             // P is rewritten and O rescaled once the PV of the tile before is done

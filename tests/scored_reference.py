@@ -13,7 +13,8 @@ def attend(q, k, v, valid, distance, scale, softcap=0.0, slope=0.0, dtype=torch.
 
     The tolerance counts, with p the softmax, a = sum_j p_j |v_j| and u half a step of the type:
       - the output's rounding: u |O|;
-      - P rounded to the type before P V, the sum unrounded: u a;
+      - P rounded to the type, p_j (1 + e_j) with |e_j| <= u, before both P V and its own sum: O then moves by
+        sum p_j e_j (v_j - O) / (1 + sum p_j e_j), at most u (a + |O|) / (1 - u);
       - the scores: an fp32 product is off by at most 2^-20 s, s = scale sum |q| |k| (64 to 256 additions
         of 2^-24 each, and the tensor cores' own accumulation), the cap by 2^-20 softcap, the distance term by
         2^-22 of itself; a score off by e moves p by a factor within 1 +- e of it and O by at most 2 e a;
@@ -36,7 +37,7 @@ def attend(q, k, v, valid, distance, scale, softcap=0.0, slope=0.0, dtype=torch.
     o, a = p @ v, p @ np.abs(v)
     e = np.where(valid, e, 0.0).max(axis=1, keepdims=True)
     u = HALF[dtype]
-    tol = u * np.abs(o) * (1 + 2.0 ** -6) + (u + 2 * e + 2.0 ** -18) * a
+    tol = 2 * u * np.abs(o) * (1 + 2.0 ** -6) + (u * (1 + 2.0 ** -6) + 2 * e + 2.0 ** -18) * a
     if dtype == torch.float16:
         tol = tol + 2.0 ** -25 * (1 + np.where(valid, 1.0, 0.0) @ np.abs(v))
     return o, tol
