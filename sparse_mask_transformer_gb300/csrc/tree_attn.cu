@@ -11,7 +11,7 @@
 // of a K/V head, up to kRowGroup of them, go along a share together, each
 // with a worker of its own (two workers per SM, scored_kernel.cuh): their
 // neighbours' requests for the same K/V tiles are then L2 hits.  (One row tile
-// after the other read the cache once per row tile: 524 us instead of 355
+// after the other read the cache once per row tile: 524 us instead of 366
 // for 512 rows per K/V head over 2 x 131000 keys.)  A head whose tiles lie in
 // one share is finished there; the others leave partial rows (O relative to
 // the rows' max, max and sum) in the workspace, which combine_kernel merges in
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Copies of Q's rows in a tile, each with a part of its keys: four at d = 64
-// where the rows leave room for them.  7 rows per K/V head, 32 requests: 29.7 us
+// where the rows leave room for them.  7 rows per K/V head, 32 requests: 27.7 us
 // with four copies, 50.2 with one.  At d = 128 a tile is 64 keys and one copy's
 // code fits the instruction cache: 64 rows, 8 requests took 54.9 us with two
 // copies, 29.9 with one (merging costs more than it saves), 4 rows 13.3 and 13.2.

@@ -274,3 +274,20 @@ def test_two_graphs_that_share_a_workspace_in_turn(gpu_lib):
     torch.cuda.synchronize()
     for c, o in zip(cs, oo):
         c.check(o)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("softcap,sl", [(0.0, False), (0.0, True), (200.0, False)])
+def test_scores_that_rise_far_above_the_first_tiles(gpu_lib, dtype, softcap, sl):
+    """The tiles go from the last key to the first: keys ever earlier have scores ever higher (by 15 nats a tile of 64 keys,
+    a step of 60 among them), so that a reference taken from the tiles before is passed by more than P can hold."""
+    T, H, n = 3, 2, 700
+    c = Case(1, H, 1, T, 128, [n], dtype, softcap=softcap, slopes=head_slopes(H) if sl else None, seed=19, scale=1.0)
+    level = torch.zeros(n + T)
+    for at in range(0, n, 64):
+        level[at:at + 64] = 15.0 * ((n - at) // 64) + (60.0 if at < 256 else 0.0)
+    c.q[:] = 0.0
+    c.q[..., 0] = 1.0                                      # score = K's first element, exact in both types
+    c.k[0, 0, :n + T, 0] = level.to(dtype)
+    c.k[0, 0, :n + T, 1:] = 0.0
+    c.run()
