@@ -11,7 +11,7 @@
 // of a K/V head, up to kRowGroup of them, go along a share together, each
 // with a worker of its own (two workers per SM, scored_kernel.cuh): their
 // neighbours' requests for the same K/V tiles are then L2 hits.  (One row tile
-// after the other read the cache once per row tile: 524 us instead of 366
+// after the other read the cache once per row tile: 524 us instead of 332
 // for 512 rows per K/V head over 2 x 131000 keys.)  A head whose tiles lie in
 // one share is finished there; the others leave partial rows (O relative to
 // the rows' max, max and sum) in the workspace, which combine_kernel merges in
