@@ -503,7 +503,8 @@ struct DocChunk {
   alignas(16) int k_doc[kMaxChunkCols], k_ord[kMaxChunkCols];
   Extent q_sum[256 / 8], k_sum[kMaxChunkCols / 8];
   int open[kMaxTilesPerChunk];  // the OTs that need words
-  int n_open;
+  uint16_t todo[256 / 8 * kMaxChunkCols / 8];  // the words that their groups do not settle
+  int n_open, n_todo;
 };
 
 __device__ __forceinline__ Extent group_extent(const int* doc, const int* ord) {
@@ -573,39 +574,48 @@ __device__ __forceinline__ void document_tiles(const EncodeParams& p, const DocS
     }
     if (lane == 0) {
       dc.n_open = n;
+      dc.n_todo = 0;
       if (full) atomicAdd(&cs.nnz, static_cast<unsigned long long>(full) * p.bm * p.bn);
     }
   }
   __syncthreads();
   unsigned long long nnz = 0;
-  // Each open OT's words over the threads.  (One loop over all open OTs'
-  // words, split by reciprocal division, gave every thread the first word when
-  // compiled by nvcc 13.0.88, and the right one with its indices checked.)
+  // Each open OT's words over the threads: those that their groups settle are
+  // written, the others (a document's edge, the diagonal) listed.  (One loop
+  // over all open OTs' words, split by reciprocal division, gave every thread
+  // the first word when compiled by nvcc 13.0.88, and the right one with its
+  // indices checked.)
   for (int o = 0; o < dc.n_open; ++o) {
     const int col0 = dc.open[o] * g.itc;
-    for (int x = tid; x < g.wpt; x += kThreads) {
-      const int pb = x / g.itc, qc = col0 + x - pb * g.itc;
-      const Settled s = settle(dc.q_sum[pb], dc.k_sum[qc]);
-      uint64_t word = s == Settled::full ? ~0ull : 0ull;
-      if (s == Settled::open) {
-        int kdoc[8], kord[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          kdoc[c] = dc.k_doc[8 * qc + c];
-          kord[c] = dc.k_ord[8 * qc + c];
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int d = dc.q_doc[8 * pb + r], ord = dc.q_ord[8 * pb + r];
-          uint32_t bits = 0;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) bits |= (kdoc[c] == d && kord[c] <= ord) ? 1u << c : 0u;
-          word |= static_cast<uint64_t>(bits) << (8 * r);
-        }
+    for (int x0 = 0; x0 < g.wpt; x0 += kThreads) {
+      const int x = x0 + tid, pb = x / g.itc, qc = col0 + x - pb * g.itc;
+      bool open = false;
+      if (x < g.wpt) {
+        const Settled s = settle(dc.q_sum[pb], dc.k_sum[qc]);
+        open = s == Settled::open;
+        words[pb * g.itcols + qc] = s == Settled::full ? ~0ull : 0ull;
+        if (s == Settled::full) nnz += 64;
       }
-      words[pb * g.itcols + qc] = word;
-      nnz += __popcll(word);
+      const unsigned all = __ballot_sync(0xffffffffu, open);
+      int first = 0;
+      if (lane == 0 && all) first = atomicAdd(&dc.n_todo, __popc(all));
+      first = __shfl_sync(0xffffffffu, first, 0);
+      if (open) dc.todo[first + __popc(all & ((1u << lane) - 1u))] = static_cast<uint16_t>(pb * g.itcols + qc);
     }
+  }
+  __syncthreads();
+  // A thread per row of the listed words.
+  for (int x = tid; x < 8 * dc.n_todo; x += kThreads) {
+    const int id = dc.todo[x >> 3], pb = id / g.itcols, qc = id - pb * g.itcols, r = 8 * pb + (x & 7);
+    const int d = dc.q_doc[r], ord = dc.q_ord[r];
+    const int4* kd4 = reinterpret_cast<const int4*>(dc.k_doc + 8 * qc);
+    const int4* ko4 = reinterpret_cast<const int4*>(dc.k_ord + 8 * qc);
+    const int4 d0 = kd4[0], d1 = kd4[1], o0 = ko4[0], o1 = ko4[1];
+    auto bit = [&](int doc, int key_ord, int c) { return doc == d && key_ord <= ord ? 1u << c : 0u; };
+    const uint32_t bits = bit(d0.x, o0.x, 0) | bit(d0.y, o0.y, 1) | bit(d0.z, o0.z, 2) | bit(d0.w, o0.w, 3) |
+                          bit(d1.x, o1.x, 4) | bit(d1.y, o1.y, 5) | bit(d1.z, o1.z, 6) | bit(d1.w, o1.w, 7);
+    reinterpret_cast<uint8_t*>(words + id)[x & 7] = static_cast<uint8_t>(bits);
+    nnz += __popc(bits);
   }
 #pragma unroll
   for (int off = 16; off; off >>= 1) nnz += __shfl_xor_sync(0xffffffffu, nnz, off);
@@ -1068,13 +1078,35 @@ cudaError_t launch_encode_rules(const EncodeParams& p_in, const EncodeGeom& g, c
 
 bool documents_direct(const EncodeGeom& g) { return g.n_chunks <= kDirectChunks; }
 
+// The kernels' own shared memory and a chunk's words can pass 48 KB together.
+using DocKernel = void (*)(EncodeParams, DocSet);
+cudaError_t documents_prepare(DocKernel kernel) {
+  struct {
+    DocKernel kernel;
+    cudaError_t error;
+  } arg{kernel, cudaSuccess};
+  once_per_device(
+      reinterpret_cast<const void*>(kernel),
+      [](const void* x) {
+        auto* a = static_cast<decltype(arg)*>(const_cast<void*>(x));
+        a->error = cudaFuncSetAttribute(a->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        256 / 8 * kMaxChunkCols / 8 * sizeof(uint64_t));
+        return a->error == cudaSuccess;
+      },
+      &arg);
+  return arg.error;
+}
+
 cudaError_t launch_encode_documents(const EncodeParams& p_in, const EncodeGeom& g, const DocSet& ds, cudaStream_t s) {
   const EncodeParams p = with_reciprocals(p_in);
   const unsigned grid = static_cast<unsigned>(g.n_chunks);
   if (!documents_direct(g)) {
+    if (const cudaError_t e = documents_prepare(encode_documents_kernel); e != cudaSuccess) return e;
     encode_documents_kernel<<<grid, kThreads, g.smem_bytes, s>>>(p, ds);
     return cudaGetLastError();
   }
+  for (DocKernel k : {documents_count_kernel, documents_write_kernel})
+    if (const cudaError_t e = documents_prepare(k); e != cudaSuccess) return e;
   documents_count_kernel<<<grid, kThreads, g.smem_bytes, s>>>(p, ds);
   return launch_early(documents_write_kernel, dim3(grid), kThreads, g.smem_bytes, s, p, ds);
 }
