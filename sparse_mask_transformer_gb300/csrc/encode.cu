@@ -483,8 +483,10 @@ __global__ void __launch_bounds__(kThreads, 7) encode_rules_kernel(const EncodeP
 // of documents, or only later keys, make an OT empty; one common document and
 // only earlier keys make it full.  Only the OTs between (on a document's edge
 // or on the diagonal) get IT words, most of which their groups settle the same
-// way.  (A word per thread over the whole chunk: 17 us a kernel on 8 masks of
-// 2048, the chunk waiting for the warps that had the diagonal.)
+// way; the others are listed and computed a thread per row.  (A word per
+// thread over the whole chunk: 17 us a kernel on 8 masks of 2048, the chunk
+// waiting for the warps that had the diagonal; a word per thread over each open
+// OT: both kernels 11.4 us for 5 documents in 4096 tokens, now 9.6.)
 constexpr int kMaxChunkCols = 1024;  // ct * bn at most (encode_geometry)
 
 struct Extent {  // of documents and orders
@@ -661,8 +663,9 @@ __global__ void __launch_bounds__(kThreads) encode_documents_kernel(const Encode
 // are classified in both, in the second while the first still runs
 // (programmatic dependent launch), and no memory has to be cleared first.
 // Two kernels and the single-pass one, packed documents in 128 x 128 OTs: 32
-// chunks 8.9 and 12.4 us, 256 12.2 and 15.5, 4096 63.8 and 67.5, 8192 110 to 126
-// and 117 to 121, 16384 278 and 236 (each chunk reads all counts before it).
+// chunks 8.4 and 12.3 us, 256 9.7 and 14.8, 2048 30.6 and 33.7, 4096 54.3 and
+// 55.8, 8192 99 to 108 and 98 to 100, 16384 243 and 194 (each chunk reads all
+// counts before it).
 constexpr int kDirectChunks = 4096;
 
 // valid elements (2^18 at most) | full OTs | partial OTs of a chunk

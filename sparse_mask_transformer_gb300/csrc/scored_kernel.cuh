@@ -444,12 +444,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (CHUNKS != 2) {
               sum = exp_row<CHUNKS, BF16>(sr, c, raise_ref(row_max(sr) * c), pk);
             } else {
-              bool look = __any_sync(0xffffffffu, m_ref == -INFINITY);
+              bool look = __any_sync(0xffffffffu, live && m_ref == -INFINITY);
 #pragma unroll 1
               for (;;) {
                 const float nmu = look ? raise_ref(row_max(sr) * c) : -m_ref;
                 sum = exp_row<CHUNKS, BF16>(sr, c, nmu, pk);
-                if (look || !__any_sync(0xffffffffu, sum > kSlack<BF16>)) break;
+                if (look || !__any_sync(0xffffffffu, live && sum > kSlack<BF16>)) break;
                 look = true;
               }
             }
