@@ -164,6 +164,7 @@ struct ScoredParams : AttnParams {
   float softcap;           // > 0: scores become softcap * tanh(score / softcap)
   const float* slopes;     // [H] or null: scores are lowered by slopes[h] * |i + q_start - j|
   int q_start;
+  int row_ots;             // OTs that the longest OT rows may list, as far as the host knows
 };
 // STOF_OK, or what is wrong with a call's score options at this scale.
 stof_status check_score(const stof_score& s, float scale);

@@ -1,7 +1,7 @@
 // The block-wise kernel of scored attention (TMA + tcgen05 + TMEM, sm_103a),
 // shared by its two sources of tiles:
 //   FormatSource  the listed outer tiles of the query tiles of a mask format
-//                 (blockwise_score.cu, stof_mha_fwd_score);
+//                 (format_source.cuh, stof_mha_fwd_score);
 //   CacheSource   the tiles of the requests' K/V caches (tree_attn.cu,
 //                 stof_tree_attn_fwd).
 // A segment is a run of K/V tiles of BN keys for one tile of 128 query rows;
@@ -128,6 +128,102 @@ struct alignas(1024) Smem {
   int abort_flag;
   typename SRC::Shared src;
 };
+
+// ---- a split item (SRC::kSplit): its parts' rows are merged through the
+// shared memory of the cluster's CTAs.
+// Address in CTA `rank` of the cluster of what is at `addr` in this one.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t x;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
+  return x;
+}
+// (LOCAL: of this CTA, `rank` is not read)
+template <bool LOCAL>
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr, uint32_t rank) {
+  float4 x;
+  if constexpr (LOCAL)
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr));
+  else
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(cluster_addr(addr, rank)));
+  return x;
+}
+template <bool LOCAL>
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr, uint32_t rank) {
+  float2 x;
+  if constexpr (LOCAL)
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr));
+  else
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(cluster_addr(addr, rank)));
+  return x;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t x;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(x));
+  return x;
+}
+// All threads of the cluster's CTAs; every one of them gets here, its waits being bounded.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Where a worker leaves 4 columns (c4) of row r of its O: chunks of 32 columns
+// in its K stages and, at d = 128, its first V stage (all of its MMAs are done).
+template <class SMEM>
+__device__ __forceinline__ uint32_t split_o(SMEM& s, int g, int r, int c4) {
+  const int cc = c4 >> 3;
+  return smem_u32(cc < 3 ? s.k[g][cc] : s.v[g][0]) + r * 128 + (((c4 & 7) ^ (r & 7)) << 4);
+}
+
+// O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the item's parts.  Each
+// worker's softmax threads take an equal share of the rows' columns, four
+// columns at a time, kOnce of those at once (a round trip to another CTA is
+// some 200 ns).
+template <class SRC, int D, bool BF16, bool LOCAL, class SMEM, class PARAMS>
+__device__ __forceinline__ void merge_split(const PARAMS& p, SMEM& s, int g) {
+  constexpr int kOnce = 4;
+  size_t out;
+  const int rows = SRC::place(p, out), parts = LOCAL ? 2 : 2 * p.cluster;
+  const int part = LOCAL ? g : 2 * static_cast<int>(cluster_rank()) + g;
+#pragma unroll 1
+  for (int i0 = part * 128 + (threadIdx.x & 127); i0 < rows * (D / 4); i0 += 128 * kOnce * parts) {
+    float m[kOnce], sum[kOnce];
+    float4 y[kOnce];
+#pragma unroll
+    for (int u = 0; u < kOnce; ++u) {
+      m[u] = -INFINITY;
+      sum[u] = 0.f;
+      y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (int k = 0; k < parts; ++k) {
+      float2 st[kOnce];
+      float4 x[kOnce];
+#pragma unroll
+      for (int u = 0; u < kOnce; ++u) {
+        const int i = min(i0 + 128 * parts * u, 128 * (D / 4) - 1), r = i / (D / 4);
+        st[u] = cluster_ld2<LOCAL>(smem_u32(s.q[k & 1]) + r * 8, k >> 1);
+        x[u] = cluster_ld4<LOCAL>(split_o(s, k & 1, r, i % (D / 4)), k >> 1);
+      }
+#pragma unroll
+      for (int u = 0; u < kOnce; ++u) {
+        const float mn = fmaxf(m[u], st[u].x), ref = mn == -INFINITY ? 0.f : mn, a = ex2(m[u] - ref), b = ex2(st[u].x - ref);
+        sum[u] = fmaf(sum[u], a, b * st[u].y);
+        y[u] = make_float4(fmaf(y[u].x, a, b * x[u].x), fmaf(y[u].y, a, b * x[u].y), fmaf(y[u].z, a, b * x[u].z),
+                           fmaf(y[u].w, a, b * x[u].w));
+        m[u] = mn;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kOnce; ++u) {
+      const int i = i0 + 128 * parts * u;
+      if (i >= rows * (D / 4)) break;
+      const float inv = sum[u] == 0.f ? 0.f : 1.f / sum[u];
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + (out + i / (D / 4)) * D + i % (D / 4) * 4) =
+          make_uint2(pack2<BF16>(y[u].x * inv, y[u].y * inv), pack2<BF16>(y[u].z * inv, y[u].w * inv));
+    }
+  }
+}
 
 // A wait that gives the same answer in every lane of the warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
@@ -601,6 +697,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!alive) continue;
       tc_fence_after();
+      if constexpr (SRC::kSplit) {
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          if (seg.n > 0) {
+            tmem_ld32(tOr + cc * 32, o);
+            tmem_ld_wait(o);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0u : o[i];  // no key seen: a sum of zeros, or unset
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(split_o(s, g, r, cc * 8 + i)), "r"(o[4 * i]),
+                         "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                         : "memory");
+        }
+        reinterpret_cast<float2*>(s.q[g])[r] = make_float2(m_ref, l);
+        tc_fence_before();
+        continue;
+      }
       const bool whole = SRC::whole(seg.item);
       const float scale = whole ? 1.f / l : 1.f;
 #pragma unroll 1
@@ -634,7 +750,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) fail();
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (SRC::kSplit) {
+    __syncwarp();
+    if (p.cluster > 1) {
+      cluster_sync();
+      if (warp >= 4) merge_split<SRC, D, BF16, false>(p, s, g);
+      __syncwarp();
+      cluster_sync();  // no CTA ends while another one reads its rows
+    } else {
+      __syncthreads();
+      if (warp >= 4) merge_split<SRC, D, BF16, true>(p, s, g);
+    }
+  } else {
+    __syncthreads();
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(s.tmem_base, 512);
@@ -666,6 +795,20 @@ stof_status launch_scored(const CUtensorMap& mq, const CUtensorMap& mk, const CU
     return true;
   };
   if (!once_per_device(reinterpret_cast<const void*>(kernel), prepare, &prep)) return prep;
+  if constexpr (SRC::kSplit) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {static_cast<unsigned>(p.cluster), 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, p), last = cudaGetLastError();
+    return record_cuda(e != cudaSuccess ? e : last) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
+  }
   kernel<<<grid, kThreads, smem, s>>>(mq, mk, mv, p);
   return record_cuda(cudaGetLastError()) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }

@@ -8,6 +8,7 @@
 // format; row-wise and block-wise kernels; analytic kernel selection).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -615,6 +616,11 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
   p.softcap = score ? score->softcap : 0.f;
   p.slopes = score ? score->slopes : nullptr;
   p.q_start = score ? score->q_start : 0;
+  p.row_ots = p.n_tc;
+  if (fmt->synced) {  // twice the mean, as causal masks have
+    const int64_t rows = static_cast<int64_t>(fmt->n_masks) * p.n_tr, listed = fmt->n_full + fmt->n_part;
+    p.row_ots = static_cast<int>(std::min<int64_t>(p.n_tc, (2 * listed + rows - 1) / rows));
+  }
   cudaStream_t s = as_stream(stream);
   if (c.kernel == STOF_KERNEL_BLOCKWISE) return launch_blockwise_scored(p, dt == STOF_BF16, s);
   return record_cuda(launch_rowwise_scored(p, dt == STOF_BF16, s)) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;

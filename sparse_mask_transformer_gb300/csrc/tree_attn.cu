@@ -94,7 +94,7 @@ __device__ __forceinline__ int share_of(const TreeParams& p, int all) { return m
 
 struct CacheSource {
   using Params = TreeParams;
-  static constexpr bool kClearsV = true;
+  static constexpr bool kClearsV = true, kSplit = false;
   struct Item {
     int b, hk;         // request, K/V head
     int ctx, count;    // committed and drafted tokens

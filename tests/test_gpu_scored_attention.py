@@ -210,3 +210,53 @@ def test_calls_that_share_a_format_may_overlap(gpu_lib, which):
     assert fmt.device_error == 0
     for a, b in zip(want, got):
         assert torch.equal(a, b) and torch.isfinite(a.float()).all()
+
+
+@pytest.mark.parametrize("option", list(OPTIONS))
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,L,Lk", [(1, 130, 4500), (1, 1100, 1100), (2, 1500, 1300), (5, 1024, 700), (160, 300, 300)])
+def test_few_query_tiles_share_out_their_keys(gpu_lib, option, d, H, L, Lk):
+    """Few query tiles: several workers take parts of one tile's keys and merge them; many: none does.  Rows that see
+    nothing, parts without tiles (the mask's lower rows list few), tiles past the last row."""
+    softcap, sl = OPTIONS[option]
+    slopes = head_slopes(H) if sl else None
+    rng = np.random.default_rng(H + L)
+    masks = (rng.random((1, L, Lk)) < 0.4).astype(np.uint8)
+    masks[0, :, 256:512] = 1
+    masks[0, 5] = 0
+    masks[0, :128, 640:] = 0
+    q, k, v = tensors(1, H, 1, L, Lk, d, torch.bfloat16, 31)
+    o = run(q, k, v, masks, 0, 0, BLOCK, softcap, slopes, q_start=Lk - L)
+    heads = sorted({0, H // 2, H - 1})
+    check(o[:, heads], q[:, heads], k, v, masks, 0, 0, softcap, None if slopes is None else [slopes[h] for h in heads],
+          q_start=Lk - L)
+    assert torch.all(o[0, :, 5] == 0)
+    again = run(q, k, v, masks, 0, 0, BLOCK, softcap, slopes, q_start=Lk - L)
+    assert torch.equal(o, again)
+
+
+def test_shared_out_keys_in_a_graph_beside_another_stream(gpu_lib):
+    """Calls that share out their keys among several workers, captured, replayed on two streams at once."""
+    H, L, d = 1, 1500, 128
+    masks = np.tril(np.ones((1, L, L), dtype=np.uint8))
+    fmt, ws, _ = gpu_encode(torch.from_numpy(masks).cuda(), 128, 128)
+    sets = [[t.cuda() for t in tensors(1, H, 1, L, L, d, torch.bfloat16, seed)] for seed in (40, 41)]
+    outs = [torch.full_like(s[0], float("nan")) for s in sets]
+    graphs = []
+    for (q, k, v), o in zip(sets, outs):
+        stof.stof_mha_fwd_score(q, k, v, fmt, 0.1, stof.Score(30.0), 0, 0, BLOCK, o)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(4):
+                stof.stof_mha_fwd_score(q, k, v, fmt, 0.1, stof.Score(30.0), 0, 0, BLOCK, o)
+        o.fill_(float("nan"))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (q, k, v), o in zip(sets, outs):
+        check(o, q.cpu(), k.cpu(), v.cpu(), masks, 0, 0, 30.0, None, scale=0.1)
