@@ -31,8 +31,9 @@
 // apart, and each copy's softmax threads take one REP-th of the tile's keys,
 // their P being 0 in the other columns: a tile then costs a thread 32 scores
 // instead of BN, in a fraction of the code.  The copies' partial rows are
-// merged at the segment's end through the worker's scratch rows in the
-// workspace.  (7 rows per K/V head, d = 64: 27.7 us, with a thread a row 50.2.)
+// merged at the segment's end through shared memory (through a scratch in
+// global memory by all threads, a call of 32 rows took 3 us longer, one of a
+// few rows 0.2 to 1 us less).  (7 rows per K/V head, d = 64: 27.7 us, with a thread a row 50.2.)
 // A softmax warp whose 32 query rows are all past the tile's last one only
 // keeps the barriers' step.
 // BN is 128 for d = 64 and 64 for d = 128: S, P and O of both workers then fit
@@ -91,10 +92,11 @@ struct Segment {
 
 // Tile width and ring depths (per worker): 16 KB a stage.  K tiles leave
 // early (their MMA comes first), V tiles a softmax later.
-template <int D>
+// Copies of Q's rows (REP > 1) are merged through what a third V stage takes.
+template <int D, int REP = 1>
 struct Shape {
   static constexpr int BN = D == 128 ? 64 : 128;
-  static constexpr int K = 3, V = D == 128 ? 2 : 3;
+  static constexpr int K = 3, V = D == 128 || REP > 1 ? 2 : 3;
   static constexpr int STAGE = BN * D * 2;
   static constexpr int ATOM = BN * 128;  // bytes of a 64-column swizzle atom of a K or V tile
 };
@@ -106,10 +108,10 @@ constexpr int kReaders = 5;  // the MMA warp, four softmax warps
 enum class Next { segment, none, lost };  // lost: a wait ran out
 
 // What one worker has in shared memory.
-template <class SRC, int D>
+template <class SRC, int D, int REP>
 struct Worker {
   uint64_t q_full, q_done;  // Q is in place; the segment's score MMAs are done
-  uint64_t k_full[Shape<D>::K], k_free[Shape<D>::K], v_full[Shape<D>::V], v_free[Shape<D>::V];
+  uint64_t k_full[Shape<D, REP>::K], k_free[Shape<D, REP>::K], v_full[Shape<D, REP>::V], v_free[Shape<D, REP>::V];
   uint64_t s_full, s_free, p_full, pv_done, merge, drain;
   uint64_t ring_full[kRing], ring_free[kRing];
   Segment<typename SRC::Item> ring[kRing];  // n < 0: no more segments
@@ -118,12 +120,16 @@ struct Worker {
   int key[8];
 };
 
-template <class SRC, int D>
+template <class SRC, int D, int REP>
 struct alignas(1024) Smem {
+  using Sh = Shape<D, REP>;
   uint8_t q[2][kBM * D * 2];
-  uint8_t k[2][Shape<D>::K][Shape<D>::STAGE];
-  uint8_t v[2][Shape<D>::V][Shape<D>::STAGE];
-  Worker<SRC, D> w[2];
+  uint8_t k[2][Sh::K][Sh::STAGE];
+  uint8_t v[2][Sh::V][Sh::STAGE];
+  // REP > 1: 32 columns of O of the copies but the first, and their (max, sum)
+  float4 merge[2][REP > 1 ? (REP - 1) * (kBM / REP) * 8 : 1];
+  float2 merge_stats[2][REP > 1 ? (REP - 1) * (kBM / REP) : 1];
+  Worker<SRC, D, REP> w[2];
   uint32_t tmem_base;
   int abort_flag;
   typename SRC::Shared src;
@@ -248,15 +254,15 @@ template <class SRC, int D, bool BF16, int MODE, int REP>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ typename SRC::Params p) {
-  using Sh = Shape<D>;
+  using Sh = Shape<D, REP>;
   constexpr int BN = Sh::BN, REGIONS = D / 64, Q_ATOM = kBM * 128;
   constexpr int KEYS = BN / REP, CHUNKS = KEYS / 32, ROWS = kBM / REP;  // a thread's keys; rows of one copy of Q
-  using Shared = Smem<SRC, D>;
+  using Shared = Smem<SRC, D, REP>;
   extern __shared__ uint8_t smem_raw[];
   Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x < 2) {
-    Worker<SRC, D>& w = s.w[threadIdx.x];
+    Worker<SRC, D, REP>& w = s.w[threadIdx.x];
     mbar_init(&w.q_full, 1);
     mbar_init(&w.q_done, 1);
     for (int i = 0; i < Sh::K; ++i) {
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const int g = warp < 4 ? warp & 1 : (warp - 4) >> 2;  // the warp's worker
-  Worker<SRC, D>& w = s.w[g];
+  Worker<SRC, D, REP>& w = s.w[g];
   const uint32_t tS = s.tmem_base + BN * g, tP = s.tmem_base + 2 * BN + BN / 2 * g, tO = s.tmem_base + 512 - 2 * D + D * g;
   volatile int* abort_flag = &s.abort_flag;
   auto fail = [&]() {
@@ -623,76 +629,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       if constexpr (REP > 1) {
-        // O of every copy, unscaled, and its rows' max and sum to the worker's
-        // scratch; then all threads merge the copies' rows.  Two scratch
-        // buffers in turn: the barrier of the next segment comes between this
-        // segment's reads and the second next's writes.
-        float* scratch = SRC::scratch(p, g, merges & 1, D);
-        float2* stats = reinterpret_cast<float2*>(scratch + static_cast<size_t>(REP) * p.rows * D);
-        if (alive) {
-          tc_fence_after();
-          const size_t at = static_cast<size_t>(part) * p.rows + r % ROWS;
+        // A warp has one copy of the rows: the first copy's warp merges the
+        // others' rows with its own, 32 columns at a time through shared
+        // memory.  (The next segment's rows come after barriers of its tiles.)
+        static_assert(REP == 1 || ROWS == 32, "a warp per copy");
+        auto barrier = [&]() {
+          mbar_arrive(&w.merge);
+          return warp_wait(&w.merge, merges++ & 1, abort_flag);
+        };
+        const int at = (part - 1) * ROWS + lane;  // part > 0: this thread's place
+        float a[REP];
+        tc_fence_after();
+        if (part > 0) s.merge_stats[g][at] = make_float2(m_ref, l);
 #pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          if (alive) {
             tmem_ld32(tOr + cc * 32, o);
             tmem_ld_wait(o);
-            if (live) {
-              float4* dst = reinterpret_cast<float4*>(scratch + at * D + cc * 32);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                     __uint_as_float(o[4 * i + 3]));
-            }
-          }
-          if (live) stats[at] = make_float2(m_ref, l);
-          tc_fence_before();
-        }
-        mbar_arrive(&w.merge);
-        if (!warp_wait(&w.merge, merges & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        ++merges;
-        const bool whole = SRC::whole(seg.item);
-        const int n = p.rows * (D / 4);
-#pragma unroll 2
-        for (int i = r; i < n; i += 128) {
-          const int rr = i / (D / 4), c = (i - rr * (D / 4)) * 4;
-          size_t out;
-          if (!SRC::out_of(p, seg.item, rr, out)) continue;
-          float m = -INFINITY, sum = 0.f;
-          float2 st[REP];
-          float4 x[REP], y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < REP; ++k) {
-            const size_t at = static_cast<size_t>(k) * p.rows + rr;
-            st[k] = stats[at];
-            x[k] = *reinterpret_cast<const float4*>(scratch + at * D + c);
-            m = fmaxf(m, st[k].x);
-          }
-          const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-          for (int k = 0; k < REP; ++k) {
-            const float a = ex2(st[k].x - ref);
-            sum = fmaf(a, st[k].y, sum);
             // a copy that has seen no key: its O is a sum of zeros, or unset
-            if (st[k].y != 0.f) {
-              y.x = fmaf(a, x[k].x, y.x);
-              y.y = fmaf(a, x[k].y, y.y);
-              y.z = fmaf(a, x[k].z, y.z);
-              y.w = fmaf(a, x[k].w, y.w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0u : o[i];
+          }
+          if (part > 0 && alive) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              s.merge[g][at * 8 + (i ^ (lane & 7))] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                                  __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          }
+          if (!(ok = barrier())) break;
+          if (part == 0 && alive) {
+            if (cc == 0) {
+              float m = m_ref, sum = 0.f;
+              float2 st[REP];
+              st[0] = make_float2(m_ref, l);
+#pragma unroll
+              for (int k = 1; k < REP; ++k) {
+                st[k] = s.merge_stats[g][(k - 1) * ROWS + lane];
+                m = fmaxf(m, st[k].x);
+              }
+              const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+              for (int k = 0; k < REP; ++k) {
+                a[k] = ex2(st[k].x - ref);
+                sum = fmaf(a[k], st[k].y, sum);
+              }
+              if (SRC::whole(seg.item)) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int k = 0; k < REP; ++k) a[k] *= inv;
+              } else if (live) {
+                SRC::put_stats(p, seg.item, g, lane, m, sum);
+              }
+            }
+            float y[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = a[0] * __uint_as_float(o[i]);
+#pragma unroll
+            for (int k = 1; k < REP; ++k)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 x = s.merge[g][((k - 1) * ROWS + lane) * 8 + (i ^ (lane & 7))];
+                y[4 * i] = fmaf(a[k], x.x, y[4 * i]);
+                y[4 * i + 1] = fmaf(a[k], x.y, y[4 * i + 1]);
+                y[4 * i + 2] = fmaf(a[k], x.z, y[4 * i + 2]);
+                y[4 * i + 3] = fmaf(a[k], x.w, y[4 * i + 3]);
+              }
+            if (live) {
+              if (SRC::whole(seg.item)) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row.out * D + cc * 32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  dst[i] = make_uint4(pack2<BF16>(y[8 * i], y[8 * i + 1]), pack2<BF16>(y[8 * i + 2], y[8 * i + 3]),
+                                      pack2<BF16>(y[8 * i + 4], y[8 * i + 5]), pack2<BF16>(y[8 * i + 6], y[8 * i + 7]));
+              } else {
+                float4* dst = reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, g, lane, D) + cc * 32);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+              }
             }
           }
-          if (whole) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + out * D + c) =
-                make_uint2(pack2<BF16>(y.x * inv, y.y * inv), pack2<BF16>(y.z * inv, y.w * inv));
-          } else {
-            *reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, g, rr, D) + c) = y;
-            if (c == 0) SRC::put_stats(p, seg.item, g, rr, m, sum);
-          }
+          if (cc + 1 < D / 32 && !(ok = barrier())) break;  // read before the next columns are written
         }
+        if (!ok) break;
+        tc_fence_before();
         continue;
       }
       if (!alive) continue;
@@ -775,7 +795,7 @@ template <class SRC, int D, bool BF16, int MODE, int REP = 1>
 stof_status launch_scored(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                           const typename SRC::Params& p, unsigned grid, cudaStream_t s) {
   auto* kernel = scored_kernel<SRC, D, BF16, MODE, REP>;
-  constexpr size_t smem = sizeof(Smem<SRC, D>) + 1024;
+  constexpr size_t smem = sizeof(Smem<SRC, D, REP>) + 1024;
   static_assert(smem <= 232448, "shared memory");
   stof_status prep = STOF_OK;
   auto prepare = [](const void* arg) {

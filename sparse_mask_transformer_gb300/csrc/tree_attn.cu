@@ -47,7 +47,6 @@ struct TreeParams : CommonParams {
   int copies;      // copies of Q's rows in a tile
   float* slots;    // [2 kWorkers][slot_rows][d] partial O
   float2* stats;   // [2 kWorkers][slot_rows] (max, sum)
-  float* scratch;  // [2 kWorkers][copies * rows][d + 2], copies > 1
   int32_t* line;   // [B + 1] place of each request on the line, its length
 };
 
@@ -265,16 +264,6 @@ struct CacheSource {
     }
   }
   static __device__ bool whole(const Item& x) { return x.whole; }
-  // Row of O of the K/V head's query row rr; false if the request has no such token.
-  static __device__ bool out_of(const Params& p, const Item& x, int rr, size_t& out) {
-    const int gq = rr / p.T, t = rr - gq * p.T;
-    out = (static_cast<size_t>(x.b) * p.H + x.hk * p.group + gq) * p.T + t;
-    return t < x.count;
-  }
-  // A worker's rows for merging copies of Q: [copies * rows][d] O and (max, sum), two buffers.
-  static __device__ float* scratch(const Params& p, int g, int buffer, int d) {
-    return p.scratch + static_cast<size_t>(2 * (2 * blockIdx.x + g) + buffer) * p.copies * p.rows * (d + 2);
-  }
   // A segment that begins its item goes on in a later share: slot 2 w + 1 of
   // worker w; one that does not: slot 2 w.
   static __device__ size_t slot_row(const Params& p, const Item& x, int g, int r) {
@@ -445,10 +434,7 @@ extern "C" size_t stof_tree_attn_workspace_bytes(int B, int H, int Hkv, int T, i
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || T < 1 || T > STOF_TREE_MAX_TOKENS || (d != 64 && d != 128)) return 0;
   const long long rows = static_cast<long long>(H / Hkv) * T;
   const size_t slots = static_cast<size_t>(2 * kWorkers) * (rows < 128 ? rows : 128);
-  const int copies = copies_of(d, rows);
-  const size_t scratch = copies > 1 ? slots * copies * (d + 2) * sizeof(float) : 0;
-  return up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + up256(scratch) +
-         (static_cast<size_t>(B) + 1) * sizeof(int32_t);
+  return up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + (static_cast<size_t>(B) + 1) * sizeof(int32_t);
 }
 
 extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H,
@@ -509,8 +495,6 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   uint8_t* ws = static_cast<uint8_t*>(workspace) + up256(slots * d * sizeof(float));
   p.stats = reinterpret_cast<float2*>(ws);
   ws += up256(slots * sizeof(float2));
-  p.scratch = reinterpret_cast<float*>(ws);
-  if (p.copies > 1) ws += up256(slots * p.copies * (d + 2) * sizeof(float));
   p.line = reinterpret_cast<int32_t*>(ws);
   const int mode = mode_of(scale, softcap, p.slopes != nullptr);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
