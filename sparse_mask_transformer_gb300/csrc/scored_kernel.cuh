@@ -629,15 +629,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       if constexpr (REP > 1) {
-        // A warp has one copy of the rows: the first copy's warp merges the
-        // others' rows with its own, 32 columns at a time through shared
+        // A warp has rows of one copy: the first copy's warps merge the
+        // others' rows with their own, 32 columns at a time through shared
         // memory.  (The next segment's rows come after barriers of its tiles.)
-        static_assert(REP == 1 || ROWS == 32, "a warp per copy");
+        static_assert(ROWS % 32 == 0, "whole warps per copy");
+        const int rr = r % ROWS;
         auto barrier = [&]() {
           mbar_arrive(&w.merge);
           return warp_wait(&w.merge, merges++ & 1, abort_flag);
         };
-        const int at = (part - 1) * ROWS + lane;  // part > 0: this thread's place
+        const int at = (part - 1) * ROWS + rr;  // part > 0: this thread's place
         float a[REP];
         tc_fence_after();
         if (part > 0) s.merge_stats[g][at] = make_float2(m_ref, l);
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (part > 0 && alive) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              s.merge[g][at * 8 + (i ^ (lane & 7))] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+              s.merge[g][at * 8 + (i ^ (rr & 7))] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                                   __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
           }
           if (!(ok = barrier())) break;
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               st[0] = make_float2(m_ref, l);
 #pragma unroll
               for (int k = 1; k < REP; ++k) {
-                st[k] = s.merge_stats[g][(k - 1) * ROWS + lane];
+                st[k] = s.merge_stats[g][(k - 1) * ROWS + rr];
                 m = fmaxf(m, st[k].x);
               }
               const float ref = m == -INFINITY ? 0.f : m;
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < REP; ++k) a[k] *= inv;
               } else if (live) {
-                SRC::put_stats(p, seg.item, g, lane, m, sum);
+                SRC::put_stats(p, seg.item, g, rr, m, sum);
               }
             }
             float y[32];
@@ -689,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 1; k < REP; ++k)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float4 x = s.merge[g][((k - 1) * ROWS + lane) * 8 + (i ^ (lane & 7))];
+                const float4 x = s.merge[g][((k - 1) * ROWS + rr) * 8 + (i ^ (rr & 7))];
                 y[4 * i] = fmaf(a[k], x.x, y[4 * i]);
                 y[4 * i + 1] = fmaf(a[k], x.y, y[4 * i + 1]);
                 y[4 * i + 2] = fmaf(a[k], x.z, y[4 * i + 2]);
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   dst[i] = make_uint4(pack2<BF16>(y[8 * i], y[8 * i + 1]), pack2<BF16>(y[8 * i + 2], y[8 * i + 3]),
                                       pack2<BF16>(y[8 * i + 4], y[8 * i + 5]), pack2<BF16>(y[8 * i + 6], y[8 * i + 7]));
               } else {
-                float4* dst = reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, g, lane, D) + cc * 32);
+                float4* dst = reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, g, rr, D) + cc * 32);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
               }

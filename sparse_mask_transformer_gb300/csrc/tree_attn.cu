@@ -388,19 +388,20 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Copies of Q's rows in a tile, each with a part of its keys: four at d = 64
-// where the rows leave room for them.  7 rows per K/V head, 32 requests: 27.7 us
-// with four copies, 50.2 with one.  At d = 128 a tile is 64 keys and one copy's
-// code fits the instruction cache: 64 rows, 8 requests took 54.9 us with two
-// copies, 29.9 with one (merging costs more than it saves), 4 rows 13.3 and 13.2.
-constexpr int kCopies64 = 4;
-inline int copies_of(int d, long long rows) { return d == 64 && rows * kCopies64 <= kBM ? kCopies64 : 1; }
+// Copies of Q's rows in a tile, each with a part of its keys: four or two at
+// d = 64 where the rows leave room for them.  7 rows per K/V head, 32 requests:
+// 26.2 us with four copies, 50.2 with one; two and one: 64 rows, 32 requests of
+// 1500, cap and slopes 51.2 and 74.8, cap 44.5 and 57.4, plain 43.9 and 44.6, 56
+// rows, 2 requests of 2200, plain 11.9 and 11.5.  At d = 128 a tile is 64 keys
+// and one copy's code fits the instruction cache: @D128@.
+inline int copies_of(int d, long long rows) { return d != 64 || 2 * rows > kBM ? 1 : (4 * rows > kBM ? 2 : 4); }
 
 template <int D, bool BF16, int MODE>
 stof_status launch_mode(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p,
                         cudaStream_t s) {
   if constexpr (D == 64) {
-    if (p.copies == kCopies64) return launch_scored<CacheSource, D, BF16, MODE, kCopies64>(mq, mk, mv, p, kTreeCtas, s);
+    if (p.copies == 4) return launch_scored<CacheSource, D, BF16, MODE, 4>(mq, mk, mv, p, kTreeCtas, s);
+    if (p.copies == 2) return launch_scored<CacheSource, D, BF16, MODE, 2>(mq, mk, mv, p, kTreeCtas, s);
   }
   return launch_scored<CacheSource, D, BF16, MODE, 1>(mq, mk, mv, p, kTreeCtas, s);
 }
@@ -480,7 +481,6 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   p.tile = d == 64 ? Shape<64>::BN : Shape<128>::BN;
   p.words = (T + 31) / 32;
   p.rows = static_cast<int>(rows);
-  p.copies = copies_of(d, rows);
   p.row_tiles = static_cast<int>(row_tiles);
   p.row_groups = static_cast<int>((row_tiles + kRowGroup - 1) / kRowGroup);
   p.row_group = (p.row_tiles + p.row_groups - 1) / p.row_groups;
@@ -497,6 +497,7 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   ws += up256(slots * sizeof(float2));
   p.line = reinterpret_cast<int32_t*>(ws);
   const int mode = mode_of(scale, softcap, p.slopes != nullptr);
+  p.copies = copies_of(d, rows);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
     return dt == STOF_BF16 ? launch_tree<64, true>(q, k, v, p, mode, s) : launch_tree<64, false>(q, k, v, p, mode, s);
