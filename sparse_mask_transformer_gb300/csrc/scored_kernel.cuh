@@ -33,7 +33,8 @@
 // instead of BN, in a fraction of the code.  The copies' partial rows are
 // merged at the segment's end through shared memory (through a scratch in
 // global memory by all threads, a call of 32 rows took 3 us longer, one of a
-// few rows 0.2 to 1 us less).  (7 rows per K/V head, d = 64: 27.7 us, with a thread a row 50.2.)
+// few rows 0.2 to 1 us less).  7 rows per K/V head, 32 requests, d = 64: 26.2
+// us, with a thread a row 50.2.
 // A softmax warp whose 32 query rows are all past the tile's last one only
 // keeps the barriers' step.
 // BN is 128 for d = 64 and 64 for d = 128: S, P and O of both workers then fit

@@ -393,7 +393,9 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // 26.2 us with four copies, 50.2 with one; two and one: 64 rows, 32 requests of
 // 1500, cap and slopes 51.2 and 74.8, cap 44.5 and 57.4, plain 43.9 and 44.6, 56
 // rows, 2 requests of 2200, plain 11.9 and 11.5.  At d = 128 a tile is 64 keys
-// and one copy's code fits the instruction cache: @D128@.
+// and one copy's code fits the instruction cache; two (with two K stages) and
+// one, 64 rows, 8 requests of 4000: plain 36.3 and 34.6, cap and slopes 36.3
+// and 37.5; 4 rows, one request 14.5 and 13.5.
 inline int copies_of(int d, long long rows) { return d != 64 || 2 * rows > kBM ? 1 : (4 * rows > kBM ? 2 : 4); }
 
 template <int D, bool BF16, int MODE>
