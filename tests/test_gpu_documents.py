@@ -107,3 +107,18 @@ def test_a_reused_workspace_and_graph_replay(gpu_lib):
         arrs["bitmaps"] = arrs["bitmaps"].view("uint64")
         o = np.tile(np.arange(L), (2, 1))
         assert_format_equal(fmt, arrs, oracle.encode(dense(d, d, o, o), 128, 128))
+
+
+@pytest.mark.parametrize("n,L,bm,bn", [(18, 1032, 8, 8), (520, 130, 16, 128)])
+def test_more_chunks_than_two_kernels_take(gpu_lib, n, L, bm, bn):
+    """Over 4096 chunks: the single-pass encoder."""
+    d = packed(np.random.default_rng(n), n, L, 3, 4)
+    order = np.tile(np.arange(L), (n, 1))
+    check(d, d, order, order, bm, bn)
+
+
+@pytest.mark.parametrize("bm,bn", [(256, 256), (256, 24), (128, 128), (8, 8)])
+def test_chunks_in_which_no_group_settles_a_word(gpu_lib, bm, bn):
+    rng = np.random.default_rng(bm + bn)
+    lq, lk = 300, 1100
+    check(rng.integers(0, 3, (2, lq)), rng.integers(0, 3, (2, lk)), rng.integers(0, 9, (2, lq)), rng.integers(0, 9, (2, lk)), bm, bn)
