@@ -361,7 +361,9 @@ typedef struct {
  * The scores are capped and lowered in fp32 (the cap to a few 2^-24 of
  * softcap).  Masked keys take no part whatever their scores; as in
  * stof_mha_fwd(), V rows inside a listed OT have to be finite (a masked key's
- * V row is multiplied by 0).  Plain scores with a K/V head each run
+ * V row is multiplied by 0): a K/V cache passed as k and v starts as zeros,
+ * its V at least, since rows that nothing has written yet may share an OT with
+ * the prompt's last ones.  Plain scores with a K/V head each run
  * stof_mha_fwd_cross()'s kernels, with its condition on calls that share a
  * format; the other calls may overlap.  Other arguments, formats and errors
  * as stof_mha_fwd_cross().

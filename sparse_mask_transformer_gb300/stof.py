@@ -427,7 +427,8 @@ def stof_mha_fwd_score(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, fmt: s
                        score: Score | None, mask_stride_b: int, mask_stride_h: int, which: int, o: torch.Tensor,
                        stream=None) -> torch.Tensor:
     """q, o: device [B, H, Lq, d]; k, v: device [B, Hkv, Lk, d], H a multiple of Hkv; fp16/bf16, contiguous.
-    STOF_KERNEL_AUTO needs no synced format here."""
+    STOF_KERNEL_AUTO needs no synced format here.  V rows of masked keys in a listed outer tile have to be finite: a
+    K/V cache passed as k and v starts as zeros."""
     where = "stof_mha_fwd_score"
     device = _device_of(where, q, k, v, o, score.slopes if score is not None else None)
     B, H, Lq, d, Hkv, Lk = _heads_of(where, q, k, v, o)
