@@ -359,7 +359,9 @@ typedef struct {
  *             the row-wise one, so that encoding and attention need no host
  *             round trip between them.
  * The scores are capped and lowered in fp32 (the cap to a few 2^-24 of
- * softcap).  Masked keys take no part whatever their scores; as in
+ * softcap, the distance to a few 2^-24 of slope times what it exceeds that of
+ * the nearest of the Lk keys by, or for a slope below 0 lacks to the
+ * farthest's: keys far from the query differ as near ones do).  Masked keys take no part whatever their scores; as in
  * stof_mha_fwd(), V rows inside a listed OT have to be finite (a masked key's
  * V row is multiplied by 0): a K/V cache passed as k and v starts as zeros,
  * its V at least, since rows that nothing has written yet may share an OT with
@@ -405,7 +407,8 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
  *   device_error  device int64 or NULL; the call ORs its error bits into it.
  * d is 64 or 128 (else STOF_ERR_UNSUPPORTED), T in [1, 1024], pointers of q,
  * k, v and o 16-byte aligned.  A row that sees nothing gives 0.  Scores and
- * precision as stof_mha_fwd_score().  Asynchronous on stream; the lengths are
+ * precision as stof_mha_fwd_score() (distances from that of the row's nearest,
+ * for a slope below 0 farthest, visible key).  Asynchronous on stream; the lengths are
  * read on the device only, so a captured call follows them.
  */
 #define STOF_TREE_MAX_TOKENS 1024

@@ -223,11 +223,14 @@ struct FormatSource {
     for (int cc = 0; cc < BN / 32; ++cc)
       b[cc] = row.nb[4 * cc] | (row.nb[4 * cc + 1] << 8) | (row.nb[4 * cc + 2] << 16) | (row.nb[4 * cc + 3] << 24);
   }
+  // Distance of the nearest (far: farthest) key.
+  static __device__ uint32_t reference(const Params& p, const Row& row, const Item&, bool far) {
+    return reference_distance(row.pos, p.n_tc * 128 - 1, far);
+  }
   template <int BN>
   static __device__ void lower(const Params&, const Row& row, const Item&, int, int key, uint32_t (&sr)[BN / 32][32], float c,
-                               float slope) {
-    const int rel = row.pos - key;
-    lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= BN - 1));
+                               float slope, uint32_t base) {
+    lower_by_distance(sr, c, slope, row.pos, key, base);
   }
   static __device__ bool whole(const Item&) { return true; }
   static __device__ float* partial_o(const Params&, const Item&, int, int, int) { return nullptr; }

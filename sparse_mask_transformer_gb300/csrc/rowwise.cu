@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rowwise_kernel(const RowwisePa
   ScoreRow score;  // SCORED: the row's cap and distance terms
   if constexpr (SCORED) {
     score = make_score_row(p.scale, p.softcap, p.slopes ? __ldg(p.slopes + h) : 0.f, i + p.q_start);
+    if (p.slopes) score.base = reference_distance(score.pos, p.Lk - 1, score.slope < 0.f);
   } else {
 #pragma unroll
     for (int t = 0; t < 16; ++t) qf[t] *= p.scale_log2;

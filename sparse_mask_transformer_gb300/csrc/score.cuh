@@ -25,11 +25,21 @@ __device__ __forceinline__ float score_rcp(float x) {
   return y;
 }
 
+// Distance from `pos` to the nearest (far: the farthest) of the keys 0 .. last.
+__device__ __forceinline__ uint32_t reference_distance(int pos, int last, bool far) {
+  const uint32_t a = __sad(pos, 0, 0u), b = __sad(pos, last, 0u);  // |pos|, |pos - last|
+  return far ? max(a, b) : (pos >= 0 && pos <= last ? 0u : min(a, b));
+}
+
 // What one query row needs: with a cap, the score is a + two_a u(b q.k);
-// without, two_a q.k.  slope is in log2 units per position.
+// without, two_a q.k.  slope is in log2 units per position, and the distances
+// are counted from `base`, the head's nearest key's (slope < 0: the farthest's):
+// a row's softmax does not change when all its scores move by slope base, and
+// keys 2^30 away differ as near ones do.
 struct ScoreRow {
   float a, two_a, b, slope;
   int pos;
+  uint32_t base;
   bool cap;
 };
 
@@ -41,13 +51,14 @@ __device__ __forceinline__ ScoreRow make_score_row(float scale, float cap, float
   r.b = r.cap ? 2.f * kLog2e * (scale / cap) : 0.f;
   r.slope = slope * kLog2e;
   r.pos = pos;
+  r.base = 0;
   return r;
 }
 
 // The log2-domain score of the row's product `dot` with key `key`.
 __device__ __forceinline__ float score_of(const ScoreRow& r, float dot, int key) {
   const float u = r.cap ? score_rcp(-1.f - score_ex2(r.b * dot)) : dot;
-  const float distance = fabsf(static_cast<float>(r.pos - key));
+  const float distance = static_cast<float>(static_cast<int>(__sad(r.pos, key, 0u - r.base)));  // |pos - key| - base
   return fmaf(-r.slope, distance, fmaf(r.two_a, u, r.a));
 }
 

@@ -11,9 +11,10 @@
 // formula with an exponential and a reciprocal of the special-function unit
 // for every score, which beside the softmax's own exponential would be the
 // kernel's bound for every tile.
-// The distance.  Row at position pos, keys of the tile at j0 + i: while no
-// key is past the row, -slope |pos - j| is linear in i and takes a packed
-// addition a pair; else one subtraction and one multiply-add per score.
+// The distance.  Row at position pos, keys of the tile at j0 + i: where no
+// warp's row lies among the tile's keys, -slope |pos - j| is linear in i for
+// each row and takes a packed addition a pair; else a subtraction and two
+// multiply-adds per score.
 #pragma once
 #include "blockwise_common.cuh"
 #include "score.cuh"
@@ -121,18 +122,30 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[CHUNKS][32], const Sco
   }
 }
 
-// sr <- c sr - slope |pos - (j0 + i)|, rel = pos - j0.  `before`: no key is
-// past the row (rel >= 32 CHUNKS - 1 in every row of the warp).
+// sr <- c sr - slope (|pos - (j0 + i)| - base); `base` is the row's reference
+// distance (the sources' reference()), no more than any visible key's (slope <
+// 0: no less).  A row's softmax does not change when all its scores move by
+// slope base, and with it the differences are small where the weights are not.
+// They are taken as integers, so that keys 2^30 away differ as near ones do:
+// with r the tile's key nearest to the row and e that key's distance,
+// |pos - (j0 + i)| - base = |i - r| + (e - base).  A warp-wide call.
 template <int CHUNKS>
-__device__ __forceinline__ void lower_by_distance(uint32_t (&sr)[CHUNKS][32], float c, float slope, float rel, bool before) {
-  if (before) {
-    const float base = -slope * rel;  // -slope (rel - i) = base + slope i
+__device__ __forceinline__ void lower_by_distance(uint32_t (&sr)[CHUNKS][32], float c, float slope, int pos, int j0, uint32_t base) {
+  constexpr int N = CHUNKS * 32;
+  const bool before = pos >= j0 + N - 1, after = pos <= j0;  // the tile's keys are all before the row, all after it
+  const uint32_t rel = static_cast<uint32_t>(pos) - static_cast<uint32_t>(j0);
+  const uint32_t e = before ? rel - (N - 1) : (after ? 0u - rel : 0u);
+  // e - base, which is more than -N (slope < 0: less than N)
+  const float k = slope < 0.f ? N - static_cast<float>(base - e + N) : static_cast<float>(e - base + N) - N;
+  if (__all_sync(0xffffffffu, before || after)) {  // |i - r| is linear in i
+    const float step = before ? slope : -slope;
+    const float at0 = -slope * (before ? k + (N - 1) : k);
 #pragma unroll
     for (int cc = 0; cc < CHUNKS; ++cc)
 #pragma unroll
       for (int i0 = 0; i0 < 32; i0 += 8) {
-        float b0 = fmaf(slope, static_cast<float>(cc * 32 + i0), base), b1 = b0 + slope;
-        const float two = 2.f * slope;
+        float b0 = fmaf(step, static_cast<float>(cc * 32 + i0), at0), b1 = b0 + step;
+        const float two = 2.f * step;
 #pragma unroll
         for (int i = i0; i < i0 + 8; i += 2) {
           float x0, x1;
@@ -143,28 +156,32 @@ __device__ __forceinline__ void lower_by_distance(uint32_t (&sr)[CHUNKS][32], fl
         }
       }
   } else {
+    const float r = before ? N - 1.f : (after ? 0.f : static_cast<float>(static_cast<int>(rel))), at0 = -slope * k;
 #pragma unroll
     for (int cc = 0; cc < CHUNKS; ++cc)
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float d = fabsf(rel - static_cast<float>(cc * 32 + i));
-        sr[cc][i] = __float_as_uint(fmaf(__uint_as_float(sr[cc][i]), c, -slope * d));
+        const float x = fmaf(__uint_as_float(sr[cc][i]), c, at0);
+        sr[cc][i] = __float_as_uint(fmaf(-slope, fabsf(r - static_cast<float>(cc * 32 + i)), x));
       }
   }
 }
 
 // The same with the keys' own positions: lane x holds at[i] = position of key
-// 32 i + x.  The positions are any, so they are subtracted as integers (the
-// difference of two neighbours at 2 10^9 would be lost in fp32).  A warp-wide call.
+// 32 i + x.  The positions are any and `base` is the least distance of the
+// row's visible keys (slope < 0: the greatest), so that what is left, modulo
+// 2^32, is the visible keys' difference.  A warp-wide call.
 template <int CHUNKS>
-__device__ __forceinline__ void lower_by_positions(uint32_t (&sr)[CHUNKS][32], float c, float slope, int pos,
+__device__ __forceinline__ void lower_by_positions(uint32_t (&sr)[CHUNKS][32], float c, float slope, int pos, uint32_t base,
                                                    const int (&at)[CHUNKS]) {
+  const uint32_t flip = slope < 0.f ? ~0u : 0u, less = slope < 0.f ? ~base : 0u - base;  // ~(x + ~base) = base - x
+  const float down = -fabsf(slope);
 #pragma unroll
   for (int cc = 0; cc < CHUNKS; ++cc)
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      const float d = static_cast<float>(__sad(pos, __shfl_sync(0xffffffffu, at[cc], i), 0u));  // |pos - at|, 32 bits unsigned
-      sr[cc][i] = __float_as_uint(fmaf(__uint_as_float(sr[cc][i]), c, -slope * d));
+      const uint32_t x = __sad(pos, __shfl_sync(0xffffffffu, at[cc], i), less);  // |pos - at| + less, 32 bits unsigned
+      sr[cc][i] = __float_as_uint(fmaf(__uint_as_float(sr[cc][i]), c, down * static_cast<float>(x ^ flip)));
     }
 }
 

@@ -507,7 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = SRC::begin_row(p, row, seg, r % ROWS);   // the row is one of the call's
       const bool alive = __any_sync(0xffffffffu, live);   // the warp has such a row
       float slope = 0.f;
-      if (MODE == MODE_DISTANCE && p.slopes && live) slope = __ldg(p.slopes + row.head) * kLog2e;
+      uint32_t base = 0;  // the row's reference distance
+      if (MODE == MODE_DISTANCE && p.slopes && live) {
+        slope = __ldg(p.slopes + row.head) * kLog2e;
+        base = SRC::reference(p, row, seg.item, slope < 0.f);
+      }
       float m_ref = -INFINITY, l = 0.f;
       SRC::template prefetch<BN>(p, row, seg.item, seg.n - 1);
 #pragma unroll 1
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               cap_scores(sr, p.k, __all_sync(0xffffffffu, row_within(sr, p.k.lim)));
               c = 1.f;
             }
-            SRC::template lower<BN>(p, row, seg.item, tile, w.key[j & 7] + KEYS * part, sr, c, slope);
+            SRC::template lower<BN>(p, row, seg.item, tile, w.key[j & 7] + KEYS * part, sr, c, slope, base);
             c = 1.f;
             if (partial) mask_scores(sr, bits);
             l += exp_rows(c);

@@ -247,9 +247,27 @@ struct CacheSource {
         out[cc] = __funnelshift_r(seen(p, row, x, u0 >> 5), seen(p, row, x, (u0 >> 5) + 1), u0 & 31);
     }
   }
+  // Distance of the row's nearest (far: farthest) visible key.  Without
+  // positions a bound on it does as well: it is 1024 away from it at most.
+  static __device__ uint32_t reference(const Params& p, const Row& row, const Item& x, bool far) {
+    if (!p.positions) return far ? max(row.pos, x.count) : 0;
+    if (!far && seen(p, row, x, row.t >> 5) >> (row.t & 31) & 1u) return 0u;  // it sees itself
+    uint32_t best = far ? 0u : ~0u;
+    if (x.ctx > 0) best = reference_distance(row.pos, x.ctx - 1, far);
+#pragma unroll 1
+    for (int word = 0; 32 * word < x.count; ++word) {
+#pragma unroll 1
+      for (uint32_t bits = seen(p, row, x, word); bits; bits &= bits - 1) {
+        const int u = 32 * word + __ffs(bits) - 1;
+        const uint32_t d = __sad(row.pos, __ldg(p.positions + static_cast<size_t>(x.b) * p.T + u), 0u);
+        best = far ? max(best, d) : min(best, d);
+      }
+    }
+    return best;
+  }
   template <int BN, int CHUNKS>
   static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, int j0, uint32_t (&sr)[CHUNKS][32],
-                               float c, float slope) {
+                               float c, float slope, uint32_t base) {
     if (p.positions && partial(x, t)) {
       int at[CHUNKS];  // position of key 32 i + lane of the tile
 #pragma unroll
@@ -257,10 +275,9 @@ struct CacheSource {
         const int key = j0 + 32 * i + static_cast<int>(threadIdx.x & 31), u = key - x.ctx;
         at[i] = u < 0 ? key : (u < x.count ? __ldg(p.positions + static_cast<size_t>(x.b) * p.T + u) : 0);
       }
-      lower_by_positions(sr, c, slope, row.pos, at);
+      lower_by_positions(sr, c, slope, row.pos, base, at);
     } else {
-      const long long rel = static_cast<long long>(row.pos) - j0;
-      lower_by_distance(sr, c, slope, static_cast<float>(rel), __all_sync(0xffffffffu, rel >= CHUNKS * 32 - 1));
+      lower_by_distance(sr, c, slope, row.pos, j0, base);
     }
   }
   static __device__ bool whole(const Item& x) { return x.whole; }
