@@ -365,7 +365,12 @@ typedef struct {
  * stof_mha_fwd(), V rows inside a listed OT have to be finite (a masked key's
  * V row is multiplied by 0): a K/V cache passed as k and v starts as zeros,
  * its V at least, since rows that nothing has written yet may share an OT with
- * the prompt's last ones.  Plain scores with a K/V head each run
+ * the prompt's last ones.  With STOF_BF16, a softcap of at most 60 and no
+ * slopes the block-wise kernel and stof_tree_attn_fwd() sum exponentials of
+ * the capped scores themselves, up to e^softcap: the number of keys times the
+ * largest |V| has to stay below e^(88 - softcap) (2^40 for a softcap of 60), and
+ * what is below e^(softcap - 87) of V (2^-39) counts as 0 in a row whose scores are
+ * all at -softcap.  Plain scores with a K/V head each run
  * stof_mha_fwd_cross()'s kernels, with its condition on calls that share a
  * format; the other calls may overlap.  Other arguments, formats and errors
  * as stof_mha_fwd_cross().
