@@ -409,6 +409,8 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
  *   workspace  device, >= stof_tree_attn_workspace_bytes(...) bytes, 16-byte
  *              aligned; scratch of one call: calls that share it must not
  *              overlap on the GPU.  Nothing is kept in it from call to call.
+ *              Its first 8 bytes hold the call's own error bits (int64) when
+ *              the call has ended, whether or not device_error is given.
  *   device_error  device int64 or NULL; the call ORs its error bits into it.
  * d is 64 or 128 (else STOF_ERR_UNSUPPORTED), T in [1, 1024], pointers of q,
  * k, v and o 16-byte aligned.  A row that sees nothing gives 0.  Scores and

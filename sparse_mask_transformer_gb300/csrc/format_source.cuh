@@ -70,6 +70,7 @@ struct FormatSource {
     s.lock = s.asked = s.done = 0;
   }
   static __device__ void prologue(const Params&, Shared&) {}
+  static __device__ void finish(const Params&, const Shared&, const volatile int*) {}  // the format always has an error word
 
   // A producer's way to its items.  One request to the hardware is in flight
   // at a time; either producer takes the answer and makes the next request,

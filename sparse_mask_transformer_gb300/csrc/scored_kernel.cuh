@@ -41,8 +41,8 @@
 // the 512 TMEM columns, and a ring stage is 16 KB.  TMEM columns: S_g [BN g,
 // +BN), P_g [2 BN + BN / 2 g, +BN / 2), O_g [512 - 2 d + d g, +d).
 // Every wait is bounded; on timeout the CTA raises STOF_DEVERR_PIPE_TIMEOUT
-// (where there is an error word), drains its copies and MMAs, frees TMEM and
-// exits.
+// (in the call's error word, where it has one, and in what the source keeps),
+// drains its copies and MMAs, frees TMEM and exits.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -790,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     __syncthreads();
   }
+  if (threadIdx.x == 0) SRC::finish(p, s.src, abort_flag);
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(s.tmem_base, 512);

@@ -45,6 +45,8 @@ struct TreeParams : CommonParams {
   const uint32_t* tree;
   const int32_t* positions;
   int copies;      // copies of Q's rows in a tile
+  long long* word;  // the call's error bits, put together by combine_kernel
+  int* status;      // [kTreeCtas] the CTAs' error bits
   float* slots;    // [2 kWorkers][slot_rows][d] partial O
   float2* stats;   // [2 kWorkers][slot_rows] (max, sum)
   int32_t* line;   // [B + 1] place of each request on the line, its length
@@ -105,6 +107,7 @@ struct CacheSource {
     int sums[kThreads / 32];
     int begin[2], end[2];  // the workers' shares
     int b[2], base[2];     // request that holds a share's begin, its place on the line
+    int bad;               // CTA 0: a request breaks the bounds
   };
   struct Row {
     int head, t, pos;
@@ -112,7 +115,7 @@ struct CacheSource {
     const uint32_t* tree;  // the row's bits, or null
   };
 
-  static __device__ void init(Shared&) {}
+  static __device__ void init(Shared& s) { s.bad = 0; }
   // Finds the requests at the workers' begins; CTA 0 reports bad requests and
   // leaves the line for combine_kernel.
   static __device__ void prologue(const Params& p, Shared& s) {
@@ -127,8 +130,10 @@ struct CacheSource {
       if (blockIdx.x == 0 && b < p.B) {
         p.line[b] = at;
         int c, n;
-        if (p.err && v == 0 && !request(p, b, c, n) && !(n == 0 && c >= 0 && c <= p.cap))
-          raise_error(p.err, STOF_DEVERR_BAD_LENGTH);
+        if (v == 0 && !request(p, b, c, n) && !(n == 0 && c >= 0 && c <= p.cap)) {
+          s.bad = 1;
+          if (p.err) raise_error(p.err, STOF_DEVERR_BAD_LENGTH);
+        }
       }
       all += total;
     }
@@ -160,6 +165,11 @@ struct CacheSource {
         }
       }
     }
+  }
+  // The CTA's error bits, at its end (one thread).  A word per CTA and no
+  // atomic: none has to be cleared before the call.
+  static __device__ void finish(const Params& p, const Shared& s, const volatile int* abort_flag) {
+    p.status[blockIdx.x] = (*abort_flag ? STOF_DEVERR_PIPE_TIMEOUT : 0) | (s.bad ? STOF_DEVERR_BAD_LENGTH : 0);
   }
   // A worker's place on the line.
   struct Lead {
@@ -315,6 +325,15 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   const int per = p.Hkv * p.row_tiles;
   const int b = static_cast<int>(blockIdx.x) / per, item = static_cast<int>(blockIdx.x) - b * per;
   const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles, group = rt / p.row_group;
+  if (b == p.B) {  // the last blocks: the call's error bits
+    if (blockIdx.y) return;
+    dependents_wait();
+    int bits = 0;
+    for (int c = threadIdx.x; c < kTreeCtas; c += blockDim.x) bits |= __ldcg(p.status + c);
+    const int late = __syncthreads_or(bits & STOF_DEVERR_PIPE_TIMEOUT), bad = __syncthreads_or(bits & STOF_DEVERR_BAD_LENGTH);
+    if (threadIdx.x == 0) *p.word = (late ? STOF_DEVERR_PIPE_TIMEOUT : 0) | (bad ? STOF_DEVERR_BAD_LENGTH : 0);
+    return;
+  }
   const int r = static_cast<int>(blockIdx.y) * (4 / WPR) + warp / WPR, rr = rt * 128 + r, gq = rr / p.T, t = rr - gq * p.T;
   dependents_wait();
   int ctx, count;
@@ -404,6 +423,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+constexpr size_t kErrorBytes = 256 + (kTreeCtas * sizeof(int) + 255) / 256 * 256;  // the error bits: the call's, the CTAs'
 
 // Copies of Q's rows in a tile, each with a part of its keys: four or two at
 // d = 64 where the rows leave room for them.  7 rows per K/V head, 32 requests:
@@ -440,7 +460,7 @@ stof_status launch_tree(const void* q, const void* k, const void* v, const TreeP
   }
   if (st != STOF_OK) return st;
   const bool one = planes * p.rows * planes * p.row_groups >= static_cast<uint64_t>(kRowsPerShare) * p.shares;
-  const dim3 grid(static_cast<unsigned>(planes * p.row_tiles), static_cast<unsigned>(one ? (p.slot_rows + 3) / 4 : p.slot_rows));
+  const dim3 grid(static_cast<unsigned>(planes * p.row_tiles + 1), static_cast<unsigned>(one ? (p.slot_rows + 3) / 4 : p.slot_rows));
   const cudaError_t e = launch_early(one ? combine_kernel<D, BF16, 1> : combine_kernel<D, BF16, 4>, grid, 128, 0, s, p);
   return record_cuda(e) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
@@ -454,7 +474,7 @@ extern "C" size_t stof_tree_attn_workspace_bytes(int B, int H, int Hkv, int T, i
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || T < 1 || T > STOF_TREE_MAX_TOKENS || (d != 64 && d != 128)) return 0;
   const long long rows = static_cast<long long>(H / Hkv) * T;
   const size_t slots = static_cast<size_t>(2 * kWorkers) * (rows < 128 ? rows : 128);
-  return up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + (static_cast<size_t>(B) + 1) * sizeof(int32_t);
+  return kErrorBytes + up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + (static_cast<size_t>(B) + 1) * sizeof(int32_t);
 }
 
 extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H,
@@ -509,9 +529,13 @@ extern "C" stof_status stof_tree_attn_fwd(const void* q, const void* k, const vo
   p.counts = counts;
   p.tree = tree;
   p.positions = p.slopes ? positions : nullptr;
-  p.slots = static_cast<float*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.word = reinterpret_cast<long long*>(ws);
+  p.status = reinterpret_cast<int*>(ws + 256);
+  ws += kErrorBytes;
+  p.slots = reinterpret_cast<float*>(ws);
   const size_t slots = static_cast<size_t>(2 * kWorkers) * p.slot_rows;
-  uint8_t* ws = static_cast<uint8_t*>(workspace) + up256(slots * d * sizeof(float));
+  ws += up256(slots * d * sizeof(float));
   p.stats = reinterpret_cast<float2*>(ws);
   ws += up256(slots * sizeof(float2));
   p.line = reinterpret_cast<int32_t*>(ws);

@@ -447,7 +447,8 @@ def stof_tree_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens: 
                        counts: torch.Tensor | None = None, positions: torch.Tensor | None = None,
                        score: Score | None = None, device_error: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q, o: device [B, H, T, d]; k, v: the caches [B, Hkv, cap, d]; lens, counts: int32 [B]; tree: int32
-    [B, T, ceil(T / 32)] ancestor bits (None: token t sees drafted tokens 0..t); positions: int32 [B, T]."""
+    [B, T, ceil(T / 32)] ancestor bits (None: token t sees drafted tokens 0..t); positions: int32 [B, T].  The call's
+    error bits are ORed into device_error, and left in the first 8 bytes of the workspace (as int64) in any case."""
     where = "stof_tree_attn_fwd"
     slopes = score.slopes if score is not None else None
     device = _device_of(where, q, k, v, o, lens, workspace, tree, counts, positions, slopes, device_error)
