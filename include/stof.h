@@ -351,6 +351,8 @@ typedef struct {
  * shared by groups of query heads:
  *   q, o      device [B][H][Lq][d];  k, v  device [B][Hkv][Lk][d], H a
  *             multiple of Hkv; query head h reads K/V head h / (H / Hkv).
+ *             B H Lq and B Hkv Lk below 2^34, of the block-wise kernel's query
+ *             tiles (128 rows of a head) fewer than 2^31.
  *   score     HOST struct, copied at the call, or NULL for plain scores.
  *   which     as stof_mha_fwd(), but with scores capped or lowered or shared
  *             K/V heads the block-wise kernel takes 128 x 128 OTs only.

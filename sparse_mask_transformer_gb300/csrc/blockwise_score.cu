@@ -4,6 +4,8 @@
 // two-level storage format: listed tiles only, full ones without a mask test,
 // partial ones through their 8x8 inner-tile bitmaps); format_source.cuh has
 // the order and the split of the work.
+#include <climits>
+
 #include "format_source.cuh"
 
 namespace stof {
@@ -70,10 +72,14 @@ stof_status launch_d(const ScoredParams& a, cudaStream_t s) {
 
 }  // namespace
 
+bool blockwise_scored_takes(const stof_format& f, int B, int H, int d) {
+  // 128 x 128 OTs; items (and with them heads), a head's rows and its keys are counted in 32 bits
+  constexpr int kMost = INT_MAX - 128;
+  return f.bm == kBM && f.bn == 128 && (d == 64 || d == 128) && static_cast<long long>(B) * H * f.n_tr <= INT_MAX &&
+         f.lq <= kMost && f.lk <= kMost;
+}
+
 stof_status launch_blockwise_scored(const ScoredParams& p, bool bf16, cudaStream_t s) {
-  if (p.bm != kBM || p.bn != 128 || (p.d != 64 && p.d != 128)) return STOF_ERR_UNSUPPORTED;
-  // items, heads and rows are counted in 32 bits (n_tr <= L)
-  if (static_cast<long long>(p.B) * p.H * (p.L > p.Lk ? p.L : p.Lk) >= (1ll << 31)) return STOF_ERR_SHAPE;
   if (p.d == 64) return bf16 ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);
   return bf16 ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
 }

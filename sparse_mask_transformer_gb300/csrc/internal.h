@@ -227,6 +227,8 @@ stof_status mha_fwd_choice(const void* q, const void* k, const void* v, stof_dty
 cudaError_t launch_rowwise(const AttnParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_rowwise_scored(const ScoredParams& p, bool bf16, cudaStream_t s);
 stof_status launch_blockwise_scored(const ScoredParams& p, bool bf16, cudaStream_t s);
+// Whether the block-wise kernel of scored attention takes a call of these sizes.
+bool blockwise_scored_takes(const stof_format& f, int B, int H, int d);
 // Density bucket of the tuning cache.
 int tune_density_bucket(double density);
 // Returns STOF_OK or an error status (tensor-map encoding / launch).

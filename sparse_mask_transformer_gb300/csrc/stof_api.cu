@@ -391,8 +391,8 @@ static stof_status check_format(const stof_format* fmt, int B, int H, int L, int
   return STOF_OK;
 }
 
-// Every argument of an MHA call.
-static stof_status check_call(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int L,
+// Every argument of an MHA call (Hkv: K/V heads).
+static stof_status check_call(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Hkv, int L,
                               int Lk, int d, float scale, const stof_format* fmt, int64_t mask_stride_b,
                               int64_t mask_stride_h, void* o) {
   if (!q || !k || !v || !o || !fmt) return STOF_ERR_INVALID_ARG;
@@ -404,7 +404,8 @@ static stof_status check_call(const void* q, const void* k, const void* v, stof_
   const long double max_mask = static_cast<long double>(B - 1) * mask_stride_b +
                                static_cast<long double>(H - 1) * mask_stride_h;
   if (max_mask >= fmt->n_masks) return STOF_ERR_SHAPE;
-  if (static_cast<long double>(B) * H * (L > Lk ? L : Lk) >= 2147483647.0L * 8) return STOF_ERR_SHAPE;
+  const long double rows = static_cast<long double>(B) * H * L, keys = static_cast<long double>(B) * Hkv * Lk;
+  if ((rows > keys ? rows : keys) >= 2147483647.0L * 8) return STOF_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16)) return STOF_ERR_ALIGNMENT;
   return STOF_OK;
 }
@@ -516,7 +517,7 @@ stof_status mha_fwd_choice(const void* q, const void* k, const void* v, stof_dty
                            int d,
                            float scale, const stof_format* fmt, int64_t mask_stride_b, int64_t mask_stride_h,
                            const KernelChoice& c, void* o, void* stream) {
-  const stof_status st = check_call(q, k, v, dt, B, H, L, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
+  const stof_status st = check_call(q, k, v, dt, B, H, H, L, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
   if (st != STOF_OK) return st;
   if (c.kernel != STOF_KERNEL_ROWWISE && c.kernel != STOF_KERNEL_BLOCKWISE) return STOF_ERR_INVALID_ARG;
   if (c.kernel == STOF_KERNEL_BLOCKWISE && (!blockwise_tiles(*fmt) || (d != 64 && d != 128)))
@@ -564,7 +565,7 @@ stof_status stof_mha_fwd_plan(const void* q, const void* k, const void* v, stof_
 stof_status stof_mha_fwd_cross(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Lq,
                                int Lk, int d, float scale, const stof_format* fmt, int64_t mask_stride_b,
                                int64_t mask_stride_h, stof_kernel which, void* o, void* stream) {
-  stof_status st = check_call(q, k, v, dt, B, H, Lq, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
+  stof_status st = check_call(q, k, v, dt, B, H, H, Lq, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
   if (st != STOF_OK) return st;
   KernelChoice c;
   int source = 0;
@@ -583,15 +584,15 @@ stof_status stof_mha_fwd(const void* q, const void* k, const void* v, stof_dtype
 stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Hkv, int Lq,
                                int Lk, int d, float scale, const stof_score* score, const stof_format* fmt,
                                int64_t mask_stride_b, int64_t mask_stride_h, stof_kernel which, void* o, void* stream) {
-  stof_status st = check_call(q, k, v, dt, B, H, Lq, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
-  if (st != STOF_OK) return st;
   if (Hkv < 1) return STOF_ERR_INVALID_ARG;
+  stof_status st = check_call(q, k, v, dt, B, H, Hkv, Lq, Lk, d, scale, fmt, mask_stride_b, mask_stride_h, o);
+  if (st != STOF_OK) return st;
   if (H % Hkv) return STOF_ERR_SHAPE;
   if (score && (st = check_score(*score, scale)) != STOF_OK) return st;
   const bool scored = score && (score->softcap > 0.f || score->slopes);
   const bool usual = !scored && H == Hkv;  // plain scores, a K/V head each: stof_mha_fwd_cross's kernels
-  // OTs and head sizes of the block-wise kernel that would run
-  const bool blk = blockwise_tiles(*fmt) && (usual || fmt->bn == 128) && (d == 64 || d == 128);
+  // whether the block-wise kernel that would run takes the call
+  const bool blk = usual ? blockwise_tiles(*fmt) && (d == 64 || d == 128) : blockwise_scored_takes(*fmt, B, H, d);
   KernelChoice c;
   int source = 0;
   if (which == STOF_KERNEL_AUTO && !fmt->synced) {
@@ -602,7 +603,7 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
     st = plan_call(*fmt, B, H, Lq, Lk, d, which, &c, &source);
     if (st != STOF_OK) return st;
     if (c.kernel == STOF_KERNEL_BLOCKWISE && !blk) {
-      if (which == STOF_KERNEL_BLOCKWISE) return STOF_ERR_UNSUPPORTED;
+      if (which == STOF_KERNEL_BLOCKWISE) return STOF_ERR_UNSUPPORTED;  // 128 x 64 OTs, or too many query tiles
       c.kernel = STOF_KERNEL_ROWWISE;
     }
   }
