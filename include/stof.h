@@ -359,7 +359,9 @@ typedef struct {
  *             STOF_KERNEL_AUTO also takes a format that is not synced and
  *             then runs the block-wise kernel wherever it takes the sizes, else
  *             the row-wise one, so that encoding and attention need no host
- *             round trip between them.
+ *             round trip between them.  A stof_tune() result, which is one of
+ *             the plain kernels, counts for plain scores with a K/V head each
+ *             only.
  * The scores are capped and lowered in fp32 (the cap to a few 2^-24 of
  * softcap, the distance to a few 2^-24 of slope times what it exceeds that of
  * the nearest of the Lk keys by, or for a slope below 0 lacks to the
