@@ -667,7 +667,8 @@ typedef struct {
  *   positions  device int32 [B][T], any values; or NULL: token (b, t) has
  *              position rows[b] + t (t without rows).
  *   counts     device int32 [B] or NULL (all T): tokens of request b; what
- *              belongs to later tokens is neither read nor written.
+ *              belongs to later tokens is neither read nor written.  (B or T
+ *              0: nothing is done.)
  *   rows       device int32 [B] or NULL (0): K and V of token (b, t) go to
  *              row rows[b] + t of k_out and v_out, which have kv_rows rows.
  *              A row outside [0, kv_rows) is not written and sets

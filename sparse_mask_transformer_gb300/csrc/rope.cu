@@ -252,9 +252,11 @@ stof_status rope_call(const stof_rope_plan* plan, const stof_rope_rows* x, stof_
   if (!plan_ok(plan) || !x) return STOF_ERR_INVALID_ARG;
   if (dt != STOF_F16 && dt != STOF_BF16) return STOF_ERR_DTYPE;
   if (B < 0 || T < 0 || H < 0 || Hkv < 0 || d < 1 || kv_rows < 0) return STOF_ERR_INVALID_ARG;
-  if (!x->q.data != !x->q_out.data || !x->k.data != !x->k_out.data || !x->v.data != !x->v_out.data)
+  const long long tokens = static_cast<long long>(B) * T;
+  // (without tokens the inputs have no memory, and may be null beside the caches they would go to)
+  if (tokens && (!x->q.data != !x->q_out.data || !x->k.data != !x->k_out.data || !x->v.data != !x->v_out.data))
     return STOF_ERR_INVALID_ARG;
-  if (x->v.data && !x->k.data) return STOF_ERR_INVALID_ARG;  // V is moved beside K
+  if (tokens && x->v.data && !x->k.data) return STOF_ERR_INVALID_ARG;  // V is moved beside K
   if (d > 256 || d % 2) return STOF_ERR_UNSUPPORTED;
   if (plan->rot_dim > d) return STOF_ERR_SHAPE;
   RopeParams p;
@@ -271,7 +273,6 @@ stof_status rope_call(const stof_rope_plan* plan, const stof_rope_rows* x, stof_
   const uintptr_t words = reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(counts) |
                           reinterpret_cast<uintptr_t>(rows);
   if (words % 4 || reinterpret_cast<uintptr_t>(err) % 8) return STOF_ERR_ALIGNMENT;
-  const long long tokens = static_cast<long long>(B) * T;
   if (H > (1 << 20) || Hkv > (1 << 20) || tokens * (plan->rot_dim / 2) >= (1ll << 31)) return STOF_ERR_SHAPE;
   p.H = x->q.data ? H : 0;
   p.Hkv = x->k.data ? Hkv : 0;
