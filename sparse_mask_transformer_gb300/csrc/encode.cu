@@ -207,6 +207,9 @@ __device__ __forceinline__ void rank_and_lookback(const EncodeParams& p, long lo
 }
 
 // Phase 4: column indices, row pointers and bitmaps into their final slots.
+// PLAIN: plain divisions instead of reciprocals (the documents' kernels, see
+// document_tiles).
+template <bool PLAIN = false>
 __device__ __forceinline__ void write_outputs(const EncodeParams& p, long long chunk, const uint64_t* words,
                                               const ChunkGeom& g, const ChunkState& cs, int tid, int nthreads) {
   const long long ef = static_cast<long long>((cs.excl >> 31) & 0x7FFFFFFFull);
@@ -223,9 +226,9 @@ __device__ __forceinline__ void write_outputs(const EncodeParams& p, long long c
   }
   const int total = np * g.wpt;
   for (int e = tid; e < total; e += nthreads) {
-    const int r = qdiv(e, g.rcp_wpt), x = e - r * g.wpt;
+    const int r = PLAIN ? e / g.wpt : qdiv(e, g.rcp_wpt), x = e - r * g.wpt;
     const int t = cs.plist[r];
-    const int pb = qdiv(x, g.rcp_itc), qq = x - pb * g.itc;
+    const int pb = PLAIN ? x / g.itc : qdiv(x, g.rcp_itc), qq = x - pb * g.itc;
     p.bitmaps[(ep + r) * g.wpt + x] = words[pb * g.itcols + t * g.itc + qq];
   }
   if (chunk == p.n_chunks - 1 && tid == 0) {
@@ -585,8 +588,9 @@ __device__ __forceinline__ void document_tiles(const EncodeParams& p, const DocS
   // Each open OT's words over the threads: those that their groups settle are
   // written, the others (a document's edge, the diagonal) listed.  (One loop
   // over all open OTs' words, split by reciprocal division, gave every thread
-  // the first word when compiled by nvcc 13.0.88, and the right one with its
-  // indices checked.)
+  // the first word as compiled by nvcc 13.0.88, and the right one with its
+  // indices checked; why was not found, so these kernels divide plainly
+  // throughout, in write_outputs too.)
   for (int o = 0; o < dc.n_open; ++o) {
     const int col0 = dc.open[o] * g.itc;
     for (int x0 = 0; x0 < g.wpt; x0 += kThreads) {
@@ -654,7 +658,7 @@ __global__ void __launch_bounds__(kThreads) encode_documents_kernel(const Encode
   document_tiles(p, ds, g, dc, cs, s_words, tid);
   if (tid < 32) rank_and_lookback(p, chunk, g, cs, tid);
   __syncthreads();
-  write_outputs(p, chunk, s_words, g, cs, tid, kThreads);
+  write_outputs<true>(p, chunk, s_words, g, cs, tid, kThreads);
 }
 
 // Up to kDirectChunks chunks: two kernels of the same grid, neither waiting
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(kThreads) documents_write_kernel(const EncodeP
     }
   }
   __syncthreads();
-  write_outputs(p, chunk, s_words, g, cs, tid, kThreads);
+  write_outputs<true>(p, chunk, s_words, g, cs, tid, kThreads);
 }
 
 // ---------------------------------------------------------------- bit-packed masks
