@@ -420,6 +420,8 @@ class Score:
         s = self.slopes
         if s is not None and (s.dtype != torch.float32 or s.shape != (heads,) or not s.is_contiguous()):
             raise StofError(STOF_ERR_SHAPE, f"{where}: slopes must be contiguous fp32 [H]")
+        if not INT32_MIN <= self.q_start <= INT32_MAX:  # (ctypes would keep its low 32 bits)
+            raise StofError(STOF_ERR_SHAPE, f"{where}: q_start must be within 2^30 of 0")
         return stof_score(self.softcap, None if s is None else s.data_ptr(), self.q_start)
 
 
