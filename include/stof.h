@@ -365,19 +365,19 @@ typedef struct {
  * The scores are capped and lowered in fp32 (the cap to a few 2^-24 of
  * softcap, the distance to a few 2^-24 of slope times what it exceeds that of
  * the nearest of the Lk keys by, or for a slope below 0 lacks to the
- * farthest's: keys far from the query differ as near ones do).  Masked keys take no part whatever their scores; as in
- * stof_mha_fwd(), V rows inside a listed OT have to be finite (a masked key's
- * V row is multiplied by 0): a K/V cache passed as k and v starts as zeros,
- * its V at least, since rows that nothing has written yet may share an OT with
- * the prompt's last ones.  With STOF_BF16, a softcap of at most 60 and no
- * slopes the block-wise kernel and stof_tree_attn_fwd() sum exponentials of
- * the capped scores themselves, up to e^softcap: the number of keys times the
- * largest |V| has to stay below e^(88 - softcap) (2^40 for a softcap of 60), and
- * what is below e^(softcap - 87) of V (2^-39) counts as 0 in a row whose scores are
- * all at -softcap.  Plain scores with a K/V head each run
- * stof_mha_fwd_cross()'s kernels, with its condition on calls that share a
- * format; the other calls may overlap.  Other arguments, formats and errors
- * as stof_mha_fwd_cross().
+ * farthest's: keys far from the query differ as near ones do).  Masked keys
+ * take no part whatever their scores; as in stof_mha_fwd(), V rows inside a
+ * listed OT have to be finite (a masked key's V row is multiplied by 0): a
+ * K/V cache passed as k and v starts as zeros, its V at least, since rows
+ * that nothing has written yet may share an OT with the prompt's last ones.
+ * With STOF_BF16, a softcap of at most 60 and no slopes the block-wise kernel
+ * and stof_tree_attn_fwd() sum exponentials of the capped scores themselves,
+ * up to e^softcap: the number of keys times the largest |V| has to stay below
+ * e^(88 - softcap) (2^40 for a softcap of 60), and what is below e^(softcap -
+ * 87) of V (2^-39) counts as 0 in a row whose scores are all at -softcap.
+ * Plain scores with a K/V head each run stof_mha_fwd_cross()'s kernels, with
+ * its condition on calls that share a format; the other calls may overlap.
+ * Other arguments, formats and errors as stof_mha_fwd_cross().
  */
 stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Hkv, int Lq,
                                int Lk, int d, float scale, const stof_score* score, const stof_format* fmt,
@@ -418,9 +418,10 @@ stof_status stof_mha_fwd_score(const void* q, const void* k, const void* v, stof
  *   device_error  device int64 or NULL; the call ORs its error bits into it.
  * d is 64 or 128 (else STOF_ERR_UNSUPPORTED), T in [1, 1024], pointers of q,
  * k, v and o 16-byte aligned.  A row that sees nothing gives 0.  Scores and
- * precision as stof_mha_fwd_score() (distances from that of the row's nearest,
- * for a slope below 0 farthest, visible key).  Asynchronous on stream; the lengths are
- * read on the device only, so a captured call follows them.
+ * precision as stof_mha_fwd_score() (distances from that of the row's
+ * nearest, for a slope below 0 farthest, visible key).  Asynchronous on
+ * stream; the lengths are read on the device only, so a captured call follows
+ * them.
  */
 #define STOF_TREE_MAX_TOKENS 1024
 stof_status stof_tree_attn_fwd(const void* q, const void* k, const void* v, stof_dtype dt, int B, int H, int Hkv, int T,

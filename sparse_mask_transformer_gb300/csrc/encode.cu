@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 7) encode_rules_kernel(const EncodeP
 // way; the others are listed and computed a thread per row.  (A word per
 // thread over the whole chunk: 17 us a kernel on 8 masks of 2048, the chunk
 // waiting for the warps that had the diagonal; a word per thread over each open
-// OT: both kernels 11.4 us for 5 documents in 4096 tokens, now 9.6.)
+// OT: both kernels 11.4 us for 5 documents in 4096 tokens, now 9.9.)
 constexpr int kMaxChunkCols = 1024;  // ct * bn at most (encode_geometry)
 
 struct Extent {  // of documents and orders

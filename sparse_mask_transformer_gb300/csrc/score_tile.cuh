@@ -1,6 +1,6 @@
-// Capped and distance-lowered scores of a block-wise tile, on the 128 scores
-// of one query row that a softmax thread holds in registers (see score.cuh
-// for the formulas).
+// Capped and distance-lowered scores of a block-wise tile, on the scores of
+// one query row that a softmax thread holds in registers: 128 (d = 64) or 64
+// (d = 128), or a copy's share of them (see score.cuh for the formulas).
 //
 // The cap.  A tile whose products all stay within half the cap (scaled), as
 // they do in trained models (caps of 30 to 50, scores of a few units), takes

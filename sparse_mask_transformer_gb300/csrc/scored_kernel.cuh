@@ -21,20 +21,23 @@
 // While one worker loads Q, starts or finishes a segment or waits for a tile,
 // the other one's tiles go on, so that short segments (a few tiles, as
 // packed documents and short caches give) cost little more than their tiles.
-// Both workers run the same code: what bounds this kernel besides the units
-// themselves is the instruction cache, whose 32 KB the softmax's
-// straight-line code for a tile must share with the other warps' loops.
-// (With K, V, score and PV warps that served both workers in turn the loops
+// No unit is full (profiles: issue slots 48 to 57%, tensor pipe 25 to 63%): the
+// time is that of a tile's chain of steps, and every role's instructions and
+// registers count.  Both workers run the same code, since the instruction
+// cache's 32 KB hold the softmax's straight-line code for a tile and the other
+// warps' loops.  (With K, V, score and PV warps that served both workers in turn the loops
 // took 32 KB, and 92% of the instruction fetch bandwidth behind the cache:
-// 723 us instead of 485 us for 8192 causal tokens, 32 heads of 128.)
+// 723 us instead of 485 us for 8192 causal tokens, 32 heads of 128.)  The MMA
+// branch has 56 registers: code for tiles with V rows to clear, spilling 16 to
+// 90 bytes there, cost 2 to 8% where no tile took it.
 // REP > 1 (few query rows): Q's rows are in the tile REP times, 128 / REP rows
 // apart, and each copy's softmax threads take one REP-th of the tile's keys,
-// their P being 0 in the other columns: a tile then costs a thread 32 scores
-// instead of BN, in a fraction of the code.  The copies' partial rows are
+// their P being 0 in the other columns: a tile then costs a thread BN / REP
+// scores instead of BN, in a fraction of the code.  The copies' partial rows are
 // merged at the segment's end through shared memory (through a scratch in
 // global memory by all threads, a call of 32 rows took 3 us longer, one of a
-// few rows 0.2 to 1 us less).  7 rows per K/V head, 32 requests, d = 64: 26.2
-// us, with a thread a row 50.2.
+// few rows 0.2 to 1 us less).  7 rows per K/V head, 32 requests, d = 64: 26
+// to 30 us from run to run, with a thread a row 50.
 // A softmax warp whose 32 query rows are all past the tile's last one only
 // keeps the barriers' step.
 // BN is 128 for d = 64 and 64 for d = 128: S, P and O of both workers then fit

@@ -9,7 +9,8 @@ and the levelled error E on a reference of five points, move the reference to
 the extrema of the new error curve, repeat; rounded to fp32.
 
 Run as a script to print them as C++ hex-float literals.  Double precision
-suffices: the levelled error is about 3e-7.
+suffices: the levelled error is 1.28e-7, with fp32
+coefficients 1.30e-7.
 """
 import numpy as np
 

@@ -11,7 +11,7 @@
 // of a K/V head, up to kRowGroup of them, go along a share together, each
 // with a worker of its own (two workers per SM, scored_kernel.cuh): their
 // neighbours' requests for the same K/V tiles are then L2 hits.  (One row tile
-// after the other read the cache once per row tile: 524 us instead of 332
+// after the other read the cache once per row tile: 524 us instead of 337
 // for 512 rows per K/V head over 2 x 131000 keys.)  A head whose tiles lie in
 // one share is finished there; the others leave partial rows (O relative to
 // the rows' max, max and sum) in the workspace, which combine_kernel merges in
@@ -427,7 +427,7 @@ constexpr size_t kErrorBytes = 256 + (kTreeCtas * sizeof(int) + 255) / 256 * 256
 
 // Copies of Q's rows in a tile, each with a part of its keys: four or two at
 // d = 64 where the rows leave room for them.  7 rows per K/V head, 32 requests:
-// 26.2 us with four copies, 50.2 with one; two and one: 64 rows, 32 requests of
+// 26 to 30 us with four copies, 50 with one; two and one: 64 rows, 32 requests of
 // 1500, cap and slopes 51.2 and 74.8, cap 44.5 and 57.4, plain 43.9 and 44.6, 56
 // rows, 2 requests of 2200, plain 11.9 and 11.5.  At d = 128 a tile is 64 keys
 // and one copy's code fits the instruction cache; two (with two K stages) and
