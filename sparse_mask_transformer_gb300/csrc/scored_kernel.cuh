@@ -534,9 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pk[CHUNKS][16];
           float alpha = 1.f;
           // the max mt of the tile's scores (log2 units) becomes the
-          // reference when it exceeds it by more than 2^8
+          // reference when it exceeds it by more than 2^8 (their difference
+          // is exact where it counts, while m_ref + 8 is rounded: at -2^27 to
+          // m_ref + 16, and 2^16 is past fp16)
           auto raise_ref = [&](float mt) {
-            if (mt > m_ref + kRescaleThreshold) {
+            if (mt - m_ref > kRescaleThreshold) {
               alpha = ex2(m_ref - mt);  // 0 when m_ref = -inf
               m_ref = mt;
             }
