@@ -695,6 +695,98 @@ stof_status stof_rope_bwd(const stof_rope_plan* plan, const stof_rope_rows* x, s
                           int d, const int32_t* positions, const int32_t* counts, void* stream);
 
 /*
+ * Positions with several axes: a token of a video has a time, a height and a
+ * width, one of an image a row and a column, and each pair turns with the
+ * position on its own axis:
+ *   phi = positions[axis[pair]][b][t] * frequency of the pair.
+ * Text beside them has the same position on every axis, which is
+ * stof_rope_fwd()'s rotation.  The plan's frequencies are any: one progression
+ * over all pairs (stof_rope_plan_init()), or one for each axis
+ * (stof_rope_plan_custom()).
+ */
+#define STOF_ROPE_MAX_AXES 4
+typedef struct {
+  stof_rope_plan turn;
+  int32_t n_axes;
+  int32_t made; /* set by stof_rope_axes_init(); a call refuses a struct without it */
+  uint8_t axis[STOF_ROPE_MAX_PAIRS];
+} stof_rope_axes;
+
+/* Fills *axes from a plan (copied) and the axis of each of its rot_dim / 2
+ * pairs (HOST array, each in [0, n_axes)); n_axes at most STOF_ROPE_MAX_AXES
+ * (else STOF_ERR_UNSUPPORTED).  Pure host code. */
+stof_status stof_rope_axes_init(stof_rope_axes* axes, const stof_rope_plan* plan, int n_axes, const int32_t* axis_of_pair);
+
+/*
+ * stof_rope_fwd() and stof_rope_bwd() with positions on several axes:
+ *   positions  device int32 [n_axes][B][T], any values; not NULL.
+ * Other arguments and errors as there; beside the wide path, rows that are
+ * aligned to 8 bytes (strides multiples of 4) with d a multiple of 4 and
+ * rot_dim of 8 (4 if interleaved), such as heads of 72, are moved 8 bytes at
+ * a time.
+ */
+stof_status stof_rope_axes_fwd(const stof_rope_axes* axes, const stof_rope_rows* x, stof_dtype dt, int B, int H, int Hkv,
+                               int T, int d, const int32_t* positions, const int32_t* counts, const int32_t* rows,
+                               int kv_rows, int64_t* device_error, void* stream);
+stof_status stof_rope_axes_bwd(const stof_rope_axes* axes, const stof_rope_rows* x, stof_dtype dt, int B, int H, int Hkv,
+                               int T, int d, const int32_t* positions, const int32_t* counts, void* stream);
+
+/* ------------------------------------------------------------------ */
+/* Rows of K/V caches                                                   */
+/* ------------------------------------------------------------------ */
+
+/* The K and V caches of some layers, all of one shape: data[i] is device
+ * memory of [slots][heads][rows][d] 16-bit elements, contiguous, 16-byte
+ * aligned; slot b is request b's.  HOST struct and array, copied at the call. */
+#define STOF_CACHES_MAX 256
+typedef struct {
+  void* const* data;  /* [n] */
+  int32_t n;          /* at most STOF_CACHES_MAX */
+  int32_t slots, heads, rows, d; /* d a multiple of 8, at most 1024 */
+} stof_caches;
+
+/*
+ * Keeps some of the drafted rows of each request and drops the others, after
+ * their verification: in every cache and head, with n = lens[b],
+ *   row n + i <- row n + path[b][i]     for i < kept[b]
+ * (every row as it was before the call), in place.
+ *   lens      device int32 [slots]: committed rows;
+ *   path      device int32 [slots][T]: the kept drafted rows of request b,
+ *             ascending; what is behind the first kept[b] is not used;
+ *   kept      device int32 [slots], 0 <= kept[b] <= T;
+ *   new_lens  device int32 [slots] or NULL: gets lens[b] + kept[b].  Overlaps
+ *             no input.
+ * A request whose lens, kept or path is out of range (path not ascending from
+ * 0, a row outside the cache) is skipped, its new_lens too, and sets
+ * STOF_DEVERR_BAD_LENGTH in *device_error (device int64 or NULL).  Rows from
+ * lens[b] + kept[b] on that no kept row was moved to stay as they are.  T at
+ * most STOF_TREE_MAX_TOKENS.  Asynchronous on stream; no workspace.
+ */
+stof_status stof_cache_keep(const stof_caches* caches, int T, const int32_t* lens, const int32_t* path,
+                            const int32_t* kept, int32_t* new_lens, int64_t* device_error, void* stream);
+
+/*
+ * Copies requests' rows to other slots, for samples of one prompt or the
+ * beams of a step: in every cache and head, for slots b of `to` with s =
+ * src[b] >= 0,
+ *   row i of slot b of `to` <- row i of slot s of `from`     for i < lens[s].
+ *   to       caches of as many layers, heads and elements as `from`, slots and
+ *            rows of their own; apart from `from`, or the very same caches:
+ *            then slot b with src[b] = b stays as it is, and a slot that is
+ *            copied to may not be one that others are copied from.
+ *   src      device int32 [to->slots]; negative: the slot stays as it is;
+ *   lens     device int32 [from->slots]: rows of each slot;
+ *   new_lens device int32 [to->slots] or NULL: gets lens[src[b]] where src[b]
+ *            >= 0.  May be lens if `to` is `from`; else it overlaps no input.
+ * A slot whose src or lens[src] is out of range (more than either cache's
+ * rows), or that is copied to and from in the same caches, is not copied to,
+ * nor its new_lens written, and sets STOF_DEVERR_BAD_LENGTH in *device_error
+ * (device int64 or NULL).  Asynchronous on stream; no workspace.
+ */
+stof_status stof_cache_fork(const stof_caches* from, const stof_caches* to, const int32_t* src, const int32_t* lens,
+                            int32_t* new_lens, int64_t* device_error, void* stream);
+
+/*
  * Diagnostic of the failure handling (the paper has no counterpart): every
  * pipeline wait in this library's kernels is bounded in wall time and, when
  * it runs out, ORs an error bit into a device error word and lets the

@@ -16,6 +16,10 @@
 // if interleaved), computes their angles once and turns
 // those elements of every `slots`-th head, kBatch heads in flight at a time.
 // V rows and elements past rot_dim are copied by the same threads.
+//
+// With several axes (stof_rope_axes_fwd, stof_rope_axes_bwd) each pair has the
+// position of its own axis; a thread reads the position of each of its pairs,
+// most of them in the L1 cache already.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -56,6 +60,12 @@ struct RopeParams {
   uint64_t step[STOF_ROPE_MAX_PAIRS];
 };
 
+// Positions with several axes: positions is [n_axes][tokens].
+struct AxesParams : RopeParams {
+  int64_t tokens;
+  uint8_t axis[STOF_ROPE_MAX_PAIRS];  // of each pair
+};
+
 template <bool BF16>
 __device__ __forceinline__ float widen(uint32_t bits) {
   if constexpr (BF16)
@@ -90,11 +100,19 @@ __device__ __forceinline__ void angle(const RopeParams& p, int pair, int64_t pos
   s *= p.sin_amplitude;
 }
 
-// WIDE: a unit is 8 pairs (2 x 16 bytes of the two halves) or, interleaved, 4
-// pairs (16 bytes), moved by 16-byte accesses; else one pair by 2-byte ones.
-template <bool BF16, bool INTER, bool WIDE>
-__global__ void __launch_bounds__(kThreadsRope, kBlocksRope) rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int PAIRS = WIDE ? (INTER ? 4 : 8) : 1;  // pairs per unit
+// Accesses of E elements: of 8 (16 bytes) a unit is 8 pairs (one access in
+// each of the two halves) or, interleaved, 4 pairs (one access); of 4 half as
+// many pairs; of one (E = 1) one pair.
+template <int E, bool INTER>
+constexpr int kPairs = E == 1 ? 1 : (INTER ? E / 2 : E);
+template <int E>
+using Access = std::conditional_t<E == 8, uint4, std::conditional_t<E == 4, uint2, uint16_t>>;
+
+template <bool BF16, bool INTER, int E, class PARAMS>
+__global__ void __launch_bounds__(kThreadsRope, kBlocksRope) rope_kernel(const __grid_constant__ PARAMS p) {
+  constexpr bool AXES = std::is_same<PARAMS, AxesParams>::value;
+  constexpr int PAIRS = kPairs<E, INTER>;  // pairs per unit
+  using Unit = Access<E>;
   const uint32_t tid = blockIdx.x * kThreadsRope + threadIdx.x;
   if (tid >= p.n_threads) return;
   const uint32_t units = static_cast<uint32_t>(p.rot / 2) / PAIRS;
@@ -105,7 +123,7 @@ __global__ void __launch_bounds__(kThreadsRope, kBlocksRope) rope_kernel(const _
   if (p.counts && t >= __ldg(p.counts + b)) return;
   const int64_t row0 = p.rows ? __ldg(p.rows + b) : 0;
   const int64_t row = row0 + t;  // row of this token in k_out and v_out
-  const int64_t pos = p.positions ? static_cast<int64_t>(__ldg(p.positions + token)) : row;
+  const int64_t pos = !AXES && p.positions ? static_cast<int64_t>(__ldg(p.positions + token)) : row;
   int heads = p.H + p.Hkv;
   bool kv = p.Hkv > 0;
   if (kv && (row < 0 || row >= p.kv_rows)) {  // the request's K and V are not written
@@ -124,43 +142,49 @@ __global__ void __launch_bounds__(kThreadsRope, kBlocksRope) rope_kernel(const _
 
   float c[PAIRS], s[PAIRS];
 #pragma unroll
-  for (int i = 0; i < PAIRS; ++i) angle(p, unit * PAIRS + i, pos, c[i], s[i]);
+  for (int i = 0; i < PAIRS; ++i) {
+    const int pair = unit * PAIRS + i;
+    if constexpr (AXES)
+      angle(p, pair, __ldg(p.positions + p.axis[pair] * p.tokens + token), c[i], s[i]);
+    else
+      angle(p, pair, pos, c[i], s[i]);
+  }
 
-  if constexpr (WIDE) {
-    // first element of the unit's first 16 bytes, and of its second (halves)
-    const int e0 = unit * 8, e1 = p.rot / 2 + e0;
+  if constexpr (E > 1) {
+    // first element of the unit's first access, and of its second (halves)
+    const int e0 = unit * E, e1 = p.rot / 2 + e0;
     for (int h0 = slot; h0 < heads; h0 += p.slots * kBatch) {
-      uint4 x[kBatch], y[kBatch];
+      Unit x[kBatch], y[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = h0 + i * p.slots;
         if (h < heads) {
-          x[i] = *reinterpret_cast<const uint4*>(src(h) + e0);
-          if constexpr (!INTER) y[i] = *reinterpret_cast<const uint4*>(src(h) + e1);
+          x[i] = *reinterpret_cast<const Unit*>(src(h) + e0);
+          if constexpr (!INTER) y[i] = *reinterpret_cast<const Unit*>(src(h) + e1);
         }
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = h0 + i * p.slots;
         if (h >= heads) break;
-        uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t* xw = reinterpret_cast<uint32_t*>(&x[i]);  // two elements a word
         if constexpr (INTER) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < E / 2; ++w) {
             const float2 a = widen2<BF16>(xw[w]);
             xw[w] = narrow2<BF16>(a.x * c[w] - a.y * s[w], a.y * c[w] + a.x * s[w]);
           }
-          *reinterpret_cast<uint4*>(dst(h) + e0) = make_uint4(xw[0], xw[1], xw[2], xw[3]);
+          *reinterpret_cast<Unit*>(dst(h) + e0) = x[i];
         } else {
-          uint32_t yw[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+          uint32_t* yw = reinterpret_cast<uint32_t*>(&y[i]);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < E / 2; ++w) {
             const float2 a = widen2<BF16>(xw[w]), g = widen2<BF16>(yw[w]);
             xw[w] = narrow2<BF16>(a.x * c[2 * w] - g.x * s[2 * w], a.y * c[2 * w + 1] - g.y * s[2 * w + 1]);
             yw[w] = narrow2<BF16>(g.x * c[2 * w] + a.x * s[2 * w], g.y * c[2 * w + 1] + a.y * s[2 * w + 1]);
           }
-          *reinterpret_cast<uint4*>(dst(h) + e0) = make_uint4(xw[0], xw[1], xw[2], xw[3]);
-          *reinterpret_cast<uint4*>(dst(h) + e1) = make_uint4(yw[0], yw[1], yw[2], yw[3]);
+          *reinterpret_cast<Unit*>(dst(h) + e0) = x[i];
+          *reinterpret_cast<Unit*>(dst(h) + e1) = y[i];
         }
       }
     }
@@ -175,8 +199,6 @@ __global__ void __launch_bounds__(kThreadsRope, kBlocksRope) rope_kernel(const _
   }
 
   // what is only copied: the elements past rot of Q's and K's heads, and V
-  constexpr int E = WIDE ? 8 : 1;  // elements per copy
-  using Unit = std::conditional_t<WIDE, uint4, uint16_t>;
   // n copies of E elements, `from` and `to` giving the places of copy x
   auto copy_all = [&](uint32_t n, auto&& from, auto&& to) {
     for (uint32_t x0 = in_token; x0 < n; x0 += per_token * kCopies) {
@@ -206,13 +228,14 @@ __global__ void __launch_bounds__(kThreadsRope, kBlocksRope) rope_kernel(const _
   }
 }
 
-bool wide_rows(const Rows& r) {
-  return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.sb % 8 == 0 && r.sh % 8 == 0 && r.st % 8 == 0;
+// Whether a row's elements can be taken e at a time.
+bool rows_of(const Rows& r, int e) {
+  return reinterpret_cast<uintptr_t>(r.data) % (2 * e) == 0 && r.sb % e == 0 && r.sh % e == 0 && r.st % e == 0;
 }
 
-template <bool BF16, bool INTER, bool WIDE>
-cudaError_t launch(RopeParams& p, long long tokens, cudaStream_t s) {
-  constexpr int PAIRS = WIDE ? (INTER ? 4 : 8) : 1;
+template <bool BF16, bool INTER, int E, class PARAMS>
+cudaError_t launch(PARAMS& p, long long tokens, cudaStream_t s) {
+  constexpr int PAIRS = kPairs<E, INTER>;
   const long long units = p.rot / 2 / PAIRS, heads = p.H + p.Hkv;
   // Head slots per token: as few as come near the 1024 threads per SM that
   // are resident (an angle is then computed for as many heads as can be), up
@@ -231,14 +254,21 @@ cudaError_t launch(RopeParams& p, long long tokens, cudaStream_t s) {
   p.slots = static_cast<int>(slots);
   p.n_threads = static_cast<uint32_t>(tokens * units * slots);
   const unsigned grid = static_cast<unsigned>((tokens * units * slots + kThreadsRope - 1) / kThreadsRope);
-  rope_kernel<BF16, INTER, WIDE><<<grid, kThreadsRope, 0, s>>>(p);
+  rope_kernel<BF16, INTER, E><<<grid, kThreadsRope, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-template <bool BF16>
-cudaError_t launch_t(RopeParams& p, bool inter, bool wide, long long tokens, cudaStream_t s) {
-  if (inter) return wide ? launch<BF16, true, true>(p, tokens, s) : launch<BF16, true, false>(p, tokens, s);
-  return wide ? launch<BF16, false, true>(p, tokens, s) : launch<BF16, false, false>(p, tokens, s);
+template <bool BF16, bool INTER, class PARAMS>
+cudaError_t launch_e(PARAMS& p, int e, long long tokens, cudaStream_t s) {
+  if (e == 8) return launch<BF16, INTER, 8>(p, tokens, s);
+  if constexpr (std::is_same<PARAMS, AxesParams>::value)
+    if (e == 4) return launch<BF16, INTER, 4>(p, tokens, s);
+  return launch<BF16, INTER, 1>(p, tokens, s);
+}
+template <class PARAMS>
+cudaError_t launch_t(PARAMS& p, bool bf16, bool inter, int e, long long tokens, cudaStream_t s) {
+  if (bf16) return inter ? launch_e<true, true>(p, e, tokens, s) : launch_e<true, false>(p, e, tokens, s);
+  return inter ? launch_e<false, true>(p, e, tokens, s) : launch_e<false, false>(p, e, tokens, s);
 }
 
 bool plan_ok(const stof_rope_plan* plan) {
@@ -246,9 +276,10 @@ bool plan_ok(const stof_rope_plan* plan) {
          plan->rot_dim % 2 == 0 && (plan->interleaved == 0 || plan->interleaved == 1) && std::isfinite(plan->amplitude);
 }
 
-stof_status rope_call(const stof_rope_plan* plan, const stof_rope_rows* x, stof_dtype dt, int B, int H, int Hkv, int T, int d,
-                      const int32_t* positions, const int32_t* counts, const int32_t* rows, int kv_rows, bool backward,
-                      int64_t* err, void* stream) {
+// axes: null for positions with one axis.
+stof_status rope_call(const stof_rope_plan* plan, const stof_rope_axes* axes, const stof_rope_rows* x, stof_dtype dt, int B,
+                      int H, int Hkv, int T, int d, const int32_t* positions, const int32_t* counts, const int32_t* rows,
+                      int kv_rows, bool backward, int64_t* err, void* stream) {
   if (!plan_ok(plan) || !x) return STOF_ERR_INVALID_ARG;
   if (dt != STOF_F16 && dt != STOF_BF16) return STOF_ERR_DTYPE;
   if (B < 0 || T < 0 || H < 0 || Hkv < 0 || d < 1 || kv_rows < 0) return STOF_ERR_INVALID_ARG;
@@ -259,20 +290,27 @@ stof_status rope_call(const stof_rope_plan* plan, const stof_rope_rows* x, stof_
   if (tokens && x->v.data && !x->k.data) return STOF_ERR_INVALID_ARG;  // V is moved beside K
   if (d > 256 || d % 2) return STOF_ERR_UNSUPPORTED;
   if (plan->rot_dim > d) return STOF_ERR_SHAPE;
-  RopeParams p;
+  AxesParams p;
   std::memset(&p, 0, sizeof(p));
-  bool wide = d % 8 == 0 && plan->rot_dim % (plan->interleaved ? 8 : 16) == 0;
   const stof_rows* in[6] = {&x->q, &x->k, &x->v, &x->q_out, &x->k_out, &x->v_out};
   Rows* to[6] = {&p.q, &p.k, &p.v, &p.qo, &p.ko, &p.vo};
   for (int i = 0; i < 6; ++i) {
     if (!in[i]->data) continue;
     if (reinterpret_cast<uintptr_t>(in[i]->data) % 2) return STOF_ERR_ALIGNMENT;
     *to[i] = Rows{static_cast<uint16_t*>(in[i]->data), in[i]->stride_b, in[i]->stride_h, in[i]->stride_t};
-    wide = wide && wide_rows(*to[i]);
   }
   const uintptr_t words = reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(counts) |
                           reinterpret_cast<uintptr_t>(rows);
   if (words % 4 || reinterpret_cast<uintptr_t>(err) % 8) return STOF_ERR_ALIGNMENT;
+  if (tokens && axes && !positions) return STOF_ERR_INVALID_ARG;
+  // elements an access takes: 8, one, or between them (several axes) 4
+  auto takes = [&](int e) {
+    if (d % e || plan->rot_dim % (plan->interleaved ? e : 2 * e)) return false;
+    for (int i = 0; i < 6; ++i)
+      if (in[i]->data && !rows_of(*to[i], e)) return false;
+    return true;
+  };
+  const int e = takes(8) ? 8 : (axes && takes(4) ? 4 : 1);
   if (H > (1 << 20) || Hkv > (1 << 20) || tokens * (plan->rot_dim / 2) >= (1ll << 31)) return STOF_ERR_SHAPE;
   p.H = x->q.data ? H : 0;
   p.Hkv = x->k.data ? Hkv : 0;
@@ -290,9 +328,12 @@ stof_status rope_call(const stof_rope_plan* plan, const stof_rope_rows* x, stof_
   p.sin_amplitude = backward ? -plan->amplitude : plan->amplitude;
   std::memcpy(p.step, plan->step, sizeof(p.step));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool inter = plan->interleaved != 0;
-  const cudaError_t e = dt == STOF_BF16 ? launch_t<true>(p, inter, wide, tokens, s) : launch_t<false>(p, inter, wide, tokens, s);
-  return record_cuda(e) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
+  const bool inter = plan->interleaved != 0, bf16 = dt == STOF_BF16;
+  if (!axes)
+    return record_cuda(launch_t<RopeParams>(p, bf16, inter, e, tokens, s)) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
+  p.tokens = tokens;
+  std::memcpy(p.axis, axes->axis, sizeof(p.axis));
+  return record_cuda(launch_t<AxesParams>(p, bf16, inter, e, tokens, s)) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
@@ -303,6 +344,13 @@ uint64_t step_of(double radians) {
   const double turns = radians / kTwoPi;
   const double f = turns - std::floor(turns);
   return f >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(f, 64));
+}
+
+bool axes_ok(const stof_rope_axes* a) {
+  if (!a || a->made != 1 || !plan_ok(&a->turn) || a->n_axes < 1 || a->n_axes > STOF_ROPE_MAX_AXES) return false;
+  for (int i = 0; i < a->turn.rot_dim / 2; ++i)
+    if (a->axis[i] >= a->n_axes) return false;
+  return true;
 }
 
 stof_status plan_start(stof_rope_plan* plan, int rot_dim, int interleaved, double amplitude) {
@@ -373,10 +421,39 @@ extern "C" stof_status stof_rope_plan_custom(stof_rope_plan* plan, int rot_dim, 
 extern "C" stof_status stof_rope_fwd(const stof_rope_plan* plan, const stof_rope_rows* x, stof_dtype dt, int B, int H,
                                      int Hkv, int T, int d, const int32_t* positions, const int32_t* counts,
                                      const int32_t* rows, int kv_rows, int64_t* device_error, void* stream) {
-  return rope_call(plan, x, dt, B, H, Hkv, T, d, positions, counts, rows, kv_rows, false, device_error, stream);
+  return rope_call(plan, nullptr, x, dt, B, H, Hkv, T, d, positions, counts, rows, kv_rows, false, device_error, stream);
 }
 
 extern "C" stof_status stof_rope_bwd(const stof_rope_plan* plan, const stof_rope_rows* x, stof_dtype dt, int B, int H,
                                      int Hkv, int T, int d, const int32_t* positions, const int32_t* counts, void* stream) {
-  return rope_call(plan, x, dt, B, H, Hkv, T, d, positions, counts, nullptr, T, true, nullptr, stream);
+  return rope_call(plan, nullptr, x, dt, B, H, Hkv, T, d, positions, counts, nullptr, T, true, nullptr, stream);
+}
+
+extern "C" stof_status stof_rope_axes_init(stof_rope_axes* axes, const stof_rope_plan* plan, int n_axes,
+                                           const int32_t* axis_of_pair) {
+  if (!axes) return STOF_ERR_INVALID_ARG;
+  std::memset(axes, 0, sizeof(*axes));
+  if (!plan_ok(plan) || !axis_of_pair || n_axes < 1) return STOF_ERR_INVALID_ARG;
+  if (n_axes > STOF_ROPE_MAX_AXES) return STOF_ERR_UNSUPPORTED;
+  for (int i = 0; i < plan->rot_dim / 2; ++i)
+    if (axis_of_pair[i] < 0 || axis_of_pair[i] >= n_axes) return STOF_ERR_INVALID_ARG;
+  axes->turn = *plan;
+  axes->n_axes = n_axes;
+  for (int i = 0; i < plan->rot_dim / 2; ++i) axes->axis[i] = static_cast<uint8_t>(axis_of_pair[i]);
+  axes->made = 1;
+  return STOF_OK;
+}
+
+extern "C" stof_status stof_rope_axes_fwd(const stof_rope_axes* axes, const stof_rope_rows* x, stof_dtype dt, int B, int H,
+                                          int Hkv, int T, int d, const int32_t* positions, const int32_t* counts,
+                                          const int32_t* rows, int kv_rows, int64_t* device_error, void* stream) {
+  if (!axes_ok(axes)) return STOF_ERR_INVALID_ARG;
+  return rope_call(&axes->turn, axes, x, dt, B, H, Hkv, T, d, positions, counts, rows, kv_rows, false, device_error, stream);
+}
+
+extern "C" stof_status stof_rope_axes_bwd(const stof_rope_axes* axes, const stof_rope_rows* x, stof_dtype dt, int B, int H,
+                                          int Hkv, int T, int d, const int32_t* positions, const int32_t* counts,
+                                          void* stream) {
+  if (!axes_ok(axes)) return STOF_ERR_INVALID_ARG;
+  return rope_call(&axes->turn, axes, x, dt, B, H, Hkv, T, d, positions, counts, nullptr, T, true, nullptr, stream);
 }

@@ -48,6 +48,8 @@ STOF_ROPE_LINEAR = 1
 STOF_ROPE_BY_INDEX = 2
 STOF_ROPE_BY_TURNS = 3
 STOF_ROPE_MAX_PAIRS = 128
+STOF_ROPE_MAX_AXES = 4
+STOF_CACHES_MAX = 256
 
 EXPORTED = ["stof_encode_workspace_bytes", "stof_encode_mask", "stof_format_sync",
             "stof_select_kernel", "stof_mha_fwd", "stof_status_string", "stof_version",
@@ -56,7 +58,8 @@ EXPORTED = ["stof_encode_workspace_bytes", "stof_encode_mask", "stof_format_sync
             "stof_encode_rules", "stof_check_bounded_wait", "stof_mha_plan", "stof_mha_fwd_plan",
             "stof_select_kernel_heads", "stof_oproj_ln_fwd", "stof_oproj_ln_workspace_bytes", "stof_ex2_fma",
             "stof_mha_fwd_cross", "stof_rope_plan_init", "stof_rope_plan_custom", "stof_rope_fwd", "stof_rope_bwd",
-            "stof_encode_documents", "stof_mha_fwd_score", "stof_tree_attn_fwd", "stof_tree_attn_workspace_bytes"]
+            "stof_encode_documents", "stof_mha_fwd_score", "stof_tree_attn_fwd", "stof_tree_attn_workspace_bytes",
+            "stof_rope_axes_init", "stof_rope_axes_fwd", "stof_rope_axes_bwd", "stof_cache_keep", "stof_cache_fork"]
 
 STOF_MAX_RULES = 64
 INT32_MIN, INT32_MAX = -(1 << 31), (1 << 31) - 1
@@ -126,6 +129,16 @@ class stof_score(ctypes.Structure):
 class stof_rope_plan(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
                 ("made", ctypes.c_int32), ("step", ctypes.c_uint64 * STOF_ROPE_MAX_PAIRS)]
+
+
+class stof_rope_axes(ctypes.Structure):
+    _fields_ = [("turn", stof_rope_plan), ("n_axes", ctypes.c_int32), ("made", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * STOF_ROPE_MAX_PAIRS)]
+
+
+class stof_caches(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int32), ("slots", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("d", ctypes.c_int32)]
 
 
 # stof_rope_rows: data, stride_b, stride_h, stride_t of q, k, v, q_out, k_out, v_out
@@ -207,6 +220,16 @@ def load_library(path: str = LIB_PATH):
         lib.stof_rope_fwd.restype = i32
         lib.stof_rope_bwd.argtypes = [ctypes.POINTER(stof_rope_plan), P, i32, i32, i32, i32, i32, i32, P, P, P]
         lib.stof_rope_bwd.restype = i32
+        lib.stof_rope_axes_init.argtypes = [ctypes.POINTER(stof_rope_axes), ctypes.POINTER(stof_rope_plan), i32, P]
+        lib.stof_rope_axes_init.restype = i32
+        lib.stof_rope_axes_fwd.argtypes = [ctypes.POINTER(stof_rope_axes), P, i32, i32, i32, i32, i32, i32, P, P, P, i32, P, P]
+        lib.stof_rope_axes_fwd.restype = i32
+        lib.stof_rope_axes_bwd.argtypes = [ctypes.POINTER(stof_rope_axes), P, i32, i32, i32, i32, i32, i32, P, P, P]
+        lib.stof_rope_axes_bwd.restype = i32
+        lib.stof_cache_keep.argtypes = [ctypes.POINTER(stof_caches), i32, P, P, P, P, P, P]
+        lib.stof_cache_keep.restype = i32
+        lib.stof_cache_fork.argtypes = [ctypes.POINTER(stof_caches), ctypes.POINTER(stof_caches), P, P, P, P, P]
+        lib.stof_cache_fork.restype = i32
         lib.stof_tune_workspace_bytes.argtypes = [i32, i32]
         lib.stof_tune_workspace_bytes.restype = sz
         lib.stof_tune.argtypes = [P, i32, P, P, P, i32, i32, i32, i32, i32, ctypes.c_float, i64, i64, P, sz, P,
@@ -712,8 +735,9 @@ def _rope_pair(where, a, out, B, T, d, dtype):
     return (a.data_ptr(), sb, sh, st), (out.data_ptr(), ob, oh, ot), h, to[2]
 
 
-def _rope(where, plan, q, k, v, q_out, k_out, v_out, positions, counts, rows, device_error, stream):
-    """q, k, v and their outputs, [B, heads, T, d] with contiguous rows of d, any other strides."""
+def _rope(where, forward, backward, plan, q, k, v, q_out, k_out, v_out, positions, counts, rows, device_error, stream):
+    """q, k, v and their outputs, [B, heads, T, d] with contiguous rows of d, any other strides; one of the two
+    entry points (forward, backward) is given."""
     device = _device_of(where, q, k, v, q_out, k_out, v_out, positions, counts, rows, device_error)
     lead = q if q is not None else k
     if lead is None or lead.dim() != 4:
@@ -736,16 +760,21 @@ def _rope(where, plan, q, k, v, q_out, k_out, v_out, positions, counts, rows, de
         if k is None or h != Hkv or m != kv_rows:
             raise StofError(STOF_ERR_SHAPE, f"{where}: v goes with a k of its shape")
     x = _rope_rows(*qi, *ki, *vi, *qo, *ko, *vo)
-    p = None if positions is None else _int32(where, "positions", positions, (B, T))
+    at = (plan.n_axes, B, T) if isinstance(plan, stof_rope_axes) else (B, T)
+    p = None if positions is None else _int32(where, "positions", positions, at)
     n = None if counts is None else _int32(where, "counts", counts, (B,))
-    lib = load_library()
-    if where == "stof_rope_bwd":
-        _launch(where, device, stream, lib.stof_rope_bwd, plan, x, _dtype_code(lead), B, H, Hkv, T, d, p, n)
+    if backward is not None:
+        _launch(where, device, stream, backward, plan, x, _dtype_code(lead), B, H, Hkv, T, d, p, n)
     else:
-        _launch(where, device, stream, lib.stof_rope_fwd, plan, x, _dtype_code(lead), B, H, Hkv, T, d, p, n,
+        _launch(where, device, stream, forward, plan, x, _dtype_code(lead), B, H, Hkv, T, d, p, n,
                 None if rows is None else _int32(where, "rows", rows, (B,)), kv_rows,
                 None if device_error is None else _error_word(where, device_error))
     return q_out, k_out, v_out
+
+
+def _same_rows(where, dk, dk_out):
+    if dk_out is not None and dk is not None and dk_out.dim() == 4 and dk.dim() == 4 and dk_out.shape[2] != dk.shape[2]:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: dk_out must have dk's shape")
 
 
 def stof_rope_fwd(plan: stof_rope_plan, q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
@@ -755,16 +784,105 @@ def stof_rope_fwd(plan: stof_rope_plan, q: torch.Tensor | None, k: torch.Tensor 
     """q [B, H, T, d], k and v [B, Hkv, T, d] (views of a packed projection included) turned by their positions
     (int32 [B, T]; None: rows[b] + t) and written to q_out [B, H, T, d] and k_out, v_out [B, Hkv, T or more, d],
     there from row rows[b] (int32 [B]; None: 0) on.  counts (int32 [B]): tokens of each request.  Returns the outputs."""
-    return _rope("stof_rope_fwd", plan, q, k, v, q_out, k_out, v_out, positions, counts, rows, device_error, stream)
+    return _rope("stof_rope_fwd", load_library().stof_rope_fwd, None, plan, q, k, v, q_out, k_out, v_out, positions, counts,
+                 rows, device_error, stream)
 
 
 def stof_rope_bwd(plan: stof_rope_plan, dq: torch.Tensor | None, dk: torch.Tensor | None, dv: torch.Tensor | None,
                   dq_out: torch.Tensor | None, dk_out: torch.Tensor | None, dv_out: torch.Tensor | None,
                   positions: torch.Tensor | None = None, counts: torch.Tensor | None = None, stream=None):
     """Gradients of stof_rope_fwd's outputs (no rows) to those of its inputs; any strides on both sides."""
-    if dk_out is not None and dk is not None and dk_out.dim() == 4 and dk.dim() == 4 and dk_out.shape[2] != dk.shape[2]:
-        raise StofError(STOF_ERR_SHAPE, "stof_rope_bwd: dk_out must have dk's shape")
-    return _rope("stof_rope_bwd", plan, dq, dk, dv, dq_out, dk_out, dv_out, positions, counts, None, None, stream)
+    _same_rows("stof_rope_bwd", dk, dk_out)
+    return _rope("stof_rope_bwd", None, load_library().stof_rope_bwd, plan, dq, dk, dv, dq_out, dk_out, dv_out, positions,
+                 counts, None, None, stream)
+
+
+def stof_rope_axes_init(plan: stof_rope_plan, n_axes: int, axis_of_pair) -> stof_rope_axes:
+    """A rotation whose pair p turns with the position on axis axis_of_pair[p] (one number per pair of the plan)."""
+    a = [int(x) for x in axis_of_pair]
+    if len(a) != plan.rot_dim // 2:
+        raise StofError(STOF_ERR_SHAPE, "stof_rope_axes_init: one axis per pair of the plan")
+    axes = stof_rope_axes()
+    _check(load_library().stof_rope_axes_init(ctypes.byref(axes), ctypes.byref(plan), int(n_axes),
+                                              (ctypes.c_int32 * max(1, len(a)))(*a)), "stof_rope_axes_init")
+    return axes
+
+
+def stof_rope_axes_fwd(axes: stof_rope_axes, q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None,
+                       q_out: torch.Tensor | None, k_out: torch.Tensor | None, v_out: torch.Tensor | None,
+                       positions: torch.Tensor, counts: torch.Tensor | None = None, rows: torch.Tensor | None = None,
+                       device_error: torch.Tensor | None = None, stream=None):
+    """stof_rope_fwd with positions on several axes: int32 [n_axes, B, T]."""
+    return _rope("stof_rope_axes_fwd", load_library().stof_rope_axes_fwd, None, axes, q, k, v, q_out, k_out, v_out, positions,
+                 counts, rows, device_error, stream)
+
+
+def stof_rope_axes_bwd(axes: stof_rope_axes, dq: torch.Tensor | None, dk: torch.Tensor | None, dv: torch.Tensor | None,
+                       dq_out: torch.Tensor | None, dk_out: torch.Tensor | None, dv_out: torch.Tensor | None,
+                       positions: torch.Tensor, counts: torch.Tensor | None = None, stream=None):
+    """Gradients of stof_rope_axes_fwd's outputs (no rows) to those of its inputs; any strides on both sides."""
+    _same_rows("stof_rope_axes_bwd", dk, dk_out)
+    return _rope("stof_rope_axes_bwd", None, load_library().stof_rope_axes_bwd, axes, dq, dk, dv, dq_out, dk_out, dv_out,
+                 positions, counts, None, None, stream)
+
+
+class Caches:
+    """The K and V caches of some layers, made once by a program: contiguous device tensors [slots, heads, rows, d] of one
+    shape and 16-bit type (kept alive by this object)."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise StofError(STOF_ERR_INVALID_ARG, "Caches: no tensor given")
+        self.device = _device_of("Caches", *self.tensors)
+        shape, dtype = self.tensors[0].shape, self.tensors[0].dtype
+        _dtype_code(self.tensors[0])
+        if len(shape) != 4 or any(t.shape != shape or t.dtype != dtype or not t.is_contiguous() for t in self.tensors):
+            raise StofError(STOF_ERR_SHAPE, "Caches: tensors must be contiguous [slots, heads, rows, d] of one shape and type")
+        if max(shape) > INT32_MAX:  # (ctypes would keep the low 32 bits)
+            raise StofError(STOF_ERR_SHAPE, "Caches: sizes must be below 2^31")
+        self.slots, self.heads, self.rows, self.d = shape
+        self.dtype = dtype
+        self._data = (ctypes.c_void_p * len(self.tensors))(*(t.data_ptr() for t in self.tensors))
+        self.c = stof_caches(ctypes.cast(self._data, ctypes.c_void_p), len(self.tensors), *shape)
+
+
+def _caches_device(where, caches: Caches, *tensors) -> int:
+    device = _device_of(where, *tensors)
+    if device != caches.device:
+        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: the caches are on another device")
+    return device
+
+
+def stof_cache_keep(caches: Caches, lens: torch.Tensor, path: torch.Tensor, kept: torch.Tensor,
+                    new_lens: torch.Tensor | None = None, device_error: torch.Tensor | None = None, stream=None) -> None:
+    """Row lens[b] + i of every cache <- row lens[b] + path[b, i], i < kept[b], in place; new_lens <- lens + kept (not in
+    place).  lens, kept, new_lens: int32 [slots]; path: int32 [slots, T], ascending."""
+    where = "stof_cache_keep"
+    device = _caches_device(where, caches, lens, path, kept, new_lens, device_error)
+    if path.dim() != 2:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: path must be [slots, T]")
+    one = (caches.slots,)
+    _launch(where, device, stream, load_library().stof_cache_keep, caches.c, path.shape[1], _int32(where, "lens", lens, one),
+            _int32(where, "path", path, (caches.slots, path.shape[1])), _int32(where, "kept", kept, one),
+            _int32(where, "new_lens", new_lens, one), _error_word(where, device_error))
+
+
+def stof_cache_fork(from_caches: Caches, to_caches: Caches, src: torch.Tensor, lens: torch.Tensor,
+                    new_lens: torch.Tensor | None = None, device_error: torch.Tensor | None = None, stream=None) -> None:
+    """Rows 0 .. lens[s] of slot s = src[b] of from_caches -> slot b of to_caches (src[b] < 0: left); new_lens[b] <-
+    lens[s].  The two may be the same caches if no slot is both copied to and from.  src, new_lens: int32 [slots of
+    to_caches]; lens: int32 [slots of from_caches]."""
+    where = "stof_cache_fork"
+    device = _caches_device(where, from_caches, src, lens, new_lens, device_error)
+    if to_caches.device != device:
+        raise StofError(STOF_ERR_INVALID_ARG, f"{where}: the caches are on different devices")
+    if to_caches.dtype != from_caches.dtype:
+        raise StofError(STOF_ERR_DTYPE, f"{where}: the caches have different types")
+    to = (to_caches.slots,)
+    _launch(where, device, stream, load_library().stof_cache_fork, from_caches.c, to_caches.c, _int32(where, "src", src, to),
+            _int32(where, "lens", lens, (from_caches.slots,)), _int32(where, "new_lens", new_lens, to),
+            _error_word(where, device_error))
 
 
 def stof_tune_workspace_bytes(n_masks: int, L: int) -> int:
