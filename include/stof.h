@@ -432,6 +432,47 @@ stof_status stof_tree_attn_fwd(const void* q, const void* k, const void* v, stof
 /* Workspace bytes of stof_tree_attn_fwd(); 0 for invalid sizes. */
 size_t stof_tree_attn_workspace_bytes(int B, int H, int Hkv, int T, int d);
 
+/*
+ * Attention over a prefix that requests share and over their own caches: the
+ * samples of one prompt, requests behind one instruction or document.  B
+ * requests are n_prefixes groups of n = B / n_prefixes, request b of group p =
+ * b / n:
+ *   O[b,h,t,:] = sum_{j visible} softmax_j(score(scale * Q[b,h,t,:].K_j)) V_j
+ * over the first prefix_lens[p] rows of prefix p and the rows of request b's
+ * own cache that stof_tree_attn_fwd() gives it (lens[b] committed ones, then
+ * drafted ones by its tree row).  A prefix is read once for its group, not
+ * once per request.
+ *   q, o       device [B][H][T][d], dt; o is written and overlaps no input.
+ *   k_prefix, v_prefix  device [n_prefixes][Hkv][prefix_cap][d], dt.  Rows
+ *              from prefix_lens[p] on are not used, whatever they hold.
+ *   k, v, lens, cap  the requests' own caches as in stof_tree_attn_fwd(), [B]
+ *              [Hkv][cap][d]; or k, v and lens all NULL: the prefix alone, for
+ *              instance cross attention to an encoder's states (n_prefixes =
+ *              B, or fewer where beams share a source), every token seeing all
+ *              prefix_lens[p] rows; tree, positions and slopes do not apply
+ *              (STOF_ERR_INVALID_ARG, STOF_ERR_UNSUPPORTED).
+ *   prefix_lens  device int32 [n_prefixes], in [0, prefix_cap]; one that is
+ *              not skips its requests and sets STOF_DEVERR_BAD_LENGTH.
+ *   positions  device int32 [B][T] or NULL (prefix_lens[p] + lens[b] + t): the
+ *              drafted tokens' positions, read only with slopes; row j of the
+ *              prefix has position j, committed row j of a request position
+ *              prefix_lens[p] + j.
+ *   workspace  device, >= stof_prefix_attn_workspace_bytes(...) bytes, as in
+ *              stof_tree_attn_fwd(), with the call's error bits in its first
+ *              8 bytes.
+ * Other arguments, sizes, finite V rows, precision and errors as
+ * stof_tree_attn_fwd(); prefix_cap + cap below 2^31.  Asynchronous on stream;
+ * all lengths are read on the device only.
+ */
+stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                                 stof_dtype dt, int B, int n_prefixes, int H, int Hkv, int T, int d, int prefix_cap,
+                                 int cap, const int32_t* prefix_lens, const int32_t* lens, const int32_t* counts,
+                                 const uint32_t* tree, const int32_t* positions, float scale, const stof_score* score,
+                                 void* o, void* workspace, size_t ws_bytes, int64_t* device_error, void* stream);
+
+/* Workspace bytes of stof_prefix_attn_fwd(); 0 for invalid sizes. */
+size_t stof_prefix_attn_workspace_bytes(int B, int n_prefixes, int H, int Hkv, int T, int d);
+
 /* Where a plan's choice came from. */
 #define STOF_PLAN_FORCED 0    /* the caller named the kernel */
 #define STOF_PLAN_ANALYTIC 1  /* stof_select_kernel() on the format's density [SEL] */

@@ -34,7 +34,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 
 STOF_SOURCES = ["stof_api.cu", "encode.cu", "rowwise.cu", "blockwise.cu", "blockwise_persist.cu", "tune.cu",
                 "oproj.cu", "waitcheck.cu", "rope.cu", "tree_attn.cu", "blockwise_score.cu",
-                "blockwise_score_split.cu", "cache_rows.cu"]
+                "blockwise_score_split.cu", "cache_rows.cu", "prefix_attn.cu"]
 SYNTH_SOURCES = ["synth_mask.cu"]
 
 

@@ -467,12 +467,12 @@ namespace {
 struct MapKey {
   int dev;
   const void* base;
-  uint64_t heads, L;
-  int D, box_rows;
+  uint64_t outer, heads, L;  // outer 0: no such dimension
+  int D, box_rows, box_outer;
   bool bf16;
   bool operator==(const MapKey& o) const {
-    return dev == o.dev && base == o.base && heads == o.heads && L == o.L && D == o.D && box_rows == o.box_rows &&
-           bf16 == o.bf16;
+    return dev == o.dev && base == o.base && outer == o.outer && heads == o.heads && L == o.L && D == o.D &&
+           box_rows == o.box_rows && box_outer == o.box_outer && bf16 == o.bf16;
   }
 };
 struct MapEntry {
@@ -486,10 +486,9 @@ MapEntry g_maps[kMapCache];
 int g_map_next = 0;
 }  // namespace
 
-bool make_bw_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t L, int D, int box_rows, bool bf16) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
-  const MapKey key{dev, base, heads, L, D, box_rows, bf16};
+namespace {
+bool cached_map(CUtensorMap* m, MapKey key) {
+  if (cudaGetDevice(&key.dev) != cudaSuccess) key.dev = -1;
   {
     std::lock_guard<std::mutex> lock(g_map_mu);
     for (const MapEntry& e : g_maps)
@@ -498,11 +497,15 @@ bool make_bw_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t L, i
         return true;
       }
   }
-  if (!encode_tensor_map_3d(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base,
-                            static_cast<uint64_t>(D), L, heads, static_cast<uint64_t>(D) * 2,
-                            L * static_cast<uint64_t>(D) * 2, 64, static_cast<uint32_t>(box_rows),
-                            CU_TENSOR_MAP_SWIZZLE_128B))
-    return false;
+  const CUtensorMapDataType dt = key.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const uint64_t row = static_cast<uint64_t>(key.D) * 2;
+  const bool made =
+      key.outer ? encode_tensor_map_4d(m, dt, key.base, static_cast<uint64_t>(key.D), key.L, key.heads, key.outer, row,
+                                       key.L * row, key.heads * key.L * row, 64, static_cast<uint32_t>(key.box_rows),
+                                       static_cast<uint32_t>(key.box_outer), CU_TENSOR_MAP_SWIZZLE_128B)
+                : encode_tensor_map_3d(m, dt, key.base, static_cast<uint64_t>(key.D), key.L, key.heads, row, key.L * row, 64,
+                                       static_cast<uint32_t>(key.box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!made) return false;
   std::lock_guard<std::mutex> lock(g_map_mu);
   MapEntry& e = g_maps[g_map_next];
   g_map_next = (g_map_next + 1) % kMapCache;
@@ -510,6 +513,15 @@ bool make_bw_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t L, i
   e.key = key;
   e.used = true;
   return true;
+}
+}  // namespace
+
+bool make_bw_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t L, int D, int box_rows, bool bf16) {
+  return cached_map(m, MapKey{-1, base, 0, heads, L, D, box_rows, 1, bf16});
+}
+bool make_requests_map(CUtensorMap* m, const void* base, uint64_t B, uint64_t heads, uint64_t L, int D, int box_rows,
+                       int box_requests, bool bf16) {
+  return cached_map(m, MapKey{-1, base, B, heads, L, D, box_rows, box_requests, bf16});
 }
 
 namespace {
@@ -620,6 +632,19 @@ bool encode_tensor_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* ba
   cuuint32_t box[3] = {box_inner, box_rows, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tensor_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+                          uint64_t planes, uint64_t outer, uint64_t row_bytes, uint64_t plane_bytes, uint64_t outer_bytes,
+                          uint32_t box_inner, uint32_t box_rows, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {inner, rows, planes, outer};
+  cuuint64_t strides[3] = {row_bytes, plane_bytes, outer_bytes};
+  cuuint32_t box[4] = {box_inner, box_rows, 1, box_outer};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, dt, 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

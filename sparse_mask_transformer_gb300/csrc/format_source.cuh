@@ -40,7 +40,7 @@ struct FormatParams : CommonParams {
 template <bool SPLIT>
 struct FormatSource {
   using Params = FormatParams;
-  static constexpr bool kClearsV = false, kSplit = SPLIT;
+  static constexpr bool kClearsV = false, kSplit = SPLIT, kTwoPlaces = false;
   struct Item {
     int head;
     int t0;      // SPLIT: the part's first tile
@@ -233,9 +233,9 @@ struct FormatSource {
                                float slope, uint32_t base) {
     lower_by_distance(sr, c, slope, row.pos, key, base);
   }
-  static __device__ bool whole(const Item&) { return true; }
-  static __device__ float* partial_o(const Params&, const Item&, int, int, int) { return nullptr; }
-  static __device__ void put_stats(const Params&, const Item&, int, int, float, float) {}
+  static __device__ bool whole(const Params&, const Item&) { return true; }
+  static __device__ float* partial_o(const Params&, const Item&, const Row&, int, int, int) { return nullptr; }
+  static __device__ void put_stats(const Params&, const Item&, const Row&, int, int, float, float) {}
 };
 
 // The call's kernel over one of the sources.

@@ -20,6 +20,10 @@ bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ba
 bool encode_tensor_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner,
                           uint64_t rows, uint64_t planes, uint64_t row_bytes, uint64_t plane_bytes,
                           uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+// [outer][planes][rows][inner] tensor, boxes of box_inner x box_rows x 1 x box_outer.
+bool encode_tensor_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+                          uint64_t planes, uint64_t outer, uint64_t row_bytes, uint64_t plane_bytes, uint64_t outer_bytes,
+                          uint32_t box_inner, uint32_t box_rows, uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
@@ -240,5 +244,8 @@ stof_status launch_blockwise_persist64(const AttnParams& p, bool bf16, cudaStrea
 // Maps are kept in a small per-process cache keyed by (device, base, rows,
 // D, box_rows, type), so repeated calls on the same tensors do no driver call.
 bool make_bw_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t L, int D, int box_rows, bool bf16);
+// The same of a [B][heads][L][D] tensor with boxes of box_rows rows of one head of box_requests requests.
+bool make_requests_map(CUtensorMap* m, const void* base, uint64_t B, uint64_t heads, uint64_t L, int D, int box_rows,
+                       int box_requests, bool bf16);
 
 }  // namespace stof

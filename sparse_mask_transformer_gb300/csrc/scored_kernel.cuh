@@ -1,9 +1,11 @@
 // The block-wise kernel of scored attention (TMA + tcgen05 + TMEM, sm_103a),
-// shared by its two sources of tiles:
+// shared by its sources of tiles:
 //   FormatSource  the listed outer tiles of the query tiles of a mask format
 //                 (format_source.cuh, stof_mha_fwd_score);
-//   CacheSource   the tiles of the requests' K/V caches (tree_attn.cu,
-//                 stof_tree_attn_fwd).
+//   CacheSource   the tiles of the requests' K/V caches (cache_source.cuh,
+//                 stof_tree_attn_fwd);
+//   PrefixSource  those and the tiles of the prefixes that requests share
+//                 (prefix_attn.cu, stof_prefix_attn_fwd).
 // A segment is a run of K/V tiles of BN keys for one tile of 128 query rows;
 // its online softmax gives the rows' O, or a partial O with the rows' max and
 // sum where other workers hold the rest.
@@ -297,6 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&s.tmem_base, 512);
     tmem_relinquish();
   }
+  if constexpr (SRC::kTwoPlaces) {
+    // Q's rows that no copy fills: what they hold would choose the way that
+    // whole warps take, and with it the other rows' roundings
+    if (p.fill * REP < kBM || p.own_fill * REP < kBM) {
+      for (int i = threadIdx.x; i < 2 * kBM * D / 8; i += kThreads) reinterpret_cast<uint4*>(s.q)[i] = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+    }
+  }
   SRC::prologue(p, s.src);  // all threads; may use __syncthreads
   tc_fence_before();
   __syncthreads();
@@ -345,6 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i >= depth && !mbar_wait((is_k ? w.k_free : w.v_free) + st, ph ^ 1, abort_flag, kWaitNs)) return false;
         uint8_t* to = is_k ? s.k[g][st] : s.v[g][st];
         const CUtensorMap* map = is_k ? &tmK : &tmV;
+        if constexpr (SRC::kTwoPlaces)
+          if (!seg.item.prefix) map = is_k ? &p.own_k : &p.own_v;
         if (MODE == MODE_DISTANCE && is_k) w.key[i & 7] = row;
         mbar_arrive_expect_tx(full, Sh::STAGE);
 #pragma unroll
@@ -376,12 +388,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         ++nq;
-        mbar_arrive_expect_tx(&w.q_full, kBM * D * 2);
+        if constexpr (SRC::kTwoPlaces) {  // the rows of one request or several, fewer than fill a copy
+          const CUtensorMap* map = seg.item.prefix ? &tmQ : &p.own_q;
+          mbar_arrive_expect_tx(&w.q_full, (seg.item.prefix ? p.fill : p.own_fill) * REP * D * 2);
 #pragma unroll
-        for (int r = 0; r < REGIONS; ++r)
+          for (int r = 0; r < REGIONS; ++r)
 #pragma unroll
-          for (int x = 0; x < REP; ++x)
-            tma_load_3d(s.q[g] + r * Q_ATOM + x * ROWS * 128, &tmQ, &w.q_full, 64 * r, seg.q_row, seg.q_plane);
+            for (int x = 0; x < REP; ++x)
+              tma_load_4d(s.q[g] + r * Q_ATOM + x * ROWS * 128, map, &w.q_full, 64 * r, seg.q_row, seg.item.hk, seg.q_plane);
+        } else {
+          mbar_arrive_expect_tx(&w.q_full, kBM * D * 2);
+#pragma unroll
+          for (int r = 0; r < REGIONS; ++r)
+#pragma unroll
+            for (int x = 0; x < REP; ++x)
+              tma_load_3d(s.q[g] + r * Q_ATOM + x * ROWS * 128, &tmQ, &w.q_full, 64 * r, seg.q_row, seg.q_plane);
+        }
         // K_0, K_1, V_0, K_2, V_1, ...
 #pragma unroll 1
         for (int x = 0; ok && x < 2 * seg.n; ++x) {
@@ -685,12 +707,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a[k] = ex2(st[k].x - ref);
                 sum = fmaf(a[k], st[k].y, sum);
               }
-              if (SRC::whole(seg.item)) {
+              if (SRC::whole(p, seg.item)) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
                 for (int k = 0; k < REP; ++k) a[k] *= inv;
               } else if (live) {
-                SRC::put_stats(p, seg.item, g, rr, m, sum);
+                SRC::put_stats(p, seg.item, row, g, rr, m, sum);
               }
             }
             float y[32];
@@ -707,14 +729,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 y[4 * i + 3] = fmaf(a[k], x.w, y[4 * i + 3]);
               }
             if (live) {
-              if (SRC::whole(seg.item)) {
+              if (SRC::whole(p, seg.item)) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row.out * D + cc * 32);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   dst[i] = make_uint4(pack2<BF16>(y[8 * i], y[8 * i + 1]), pack2<BF16>(y[8 * i + 2], y[8 * i + 3]),
                                       pack2<BF16>(y[8 * i + 4], y[8 * i + 5]), pack2<BF16>(y[8 * i + 6], y[8 * i + 7]));
               } else {
-                float4* dst = reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, g, rr, D) + cc * 32);
+                float4* dst = reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, row, g, rr, D) + cc * 32);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
               }
@@ -748,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         continue;
       }
-      const bool whole = SRC::whole(seg.item);
+      const bool whole = SRC::whole(p, seg.item);
       const float scale = whole ? 1.f / l : 1.f;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
@@ -769,13 +791,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst[i] = make_uint4(pack2<BF16>(x[8 * i], x[8 * i + 1]), pack2<BF16>(x[8 * i + 2], x[8 * i + 3]),
                                   pack2<BF16>(x[8 * i + 4], x[8 * i + 5]), pack2<BF16>(x[8 * i + 6], x[8 * i + 7]));
           } else {
-            float4* dst = reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, g, r, D) + cc * 32);
+            float4* dst = reinterpret_cast<float4*>(SRC::partial_o(p, seg.item, row, g, r, D) + cc * 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         }
       }
-      if (live && !whole) SRC::put_stats(p, seg.item, g, r, m_ref, l);
+      if (live && !whole) SRC::put_stats(p, seg.item, row, g, r, m_ref, l);
       tc_fence_before();  // O is read before the next segment's first p_full lets it be overwritten
     }
     if (!ok && lane == 0) fail();

@@ -59,7 +59,8 @@ EXPORTED = ["stof_encode_workspace_bytes", "stof_encode_mask", "stof_format_sync
             "stof_select_kernel_heads", "stof_oproj_ln_fwd", "stof_oproj_ln_workspace_bytes", "stof_ex2_fma",
             "stof_mha_fwd_cross", "stof_rope_plan_init", "stof_rope_plan_custom", "stof_rope_fwd", "stof_rope_bwd",
             "stof_encode_documents", "stof_mha_fwd_score", "stof_tree_attn_fwd", "stof_tree_attn_workspace_bytes",
-            "stof_rope_axes_init", "stof_rope_axes_fwd", "stof_rope_axes_bwd", "stof_cache_keep", "stof_cache_fork"]
+            "stof_rope_axes_init", "stof_rope_axes_fwd", "stof_rope_axes_bwd", "stof_cache_keep", "stof_cache_fork",
+            "stof_prefix_attn_fwd", "stof_prefix_attn_workspace_bytes"]
 
 STOF_MAX_RULES = 64
 INT32_MIN, INT32_MAX = -(1 << 31), (1 << 31) - 1
@@ -210,6 +211,11 @@ def load_library(path: str = LIB_PATH):
         lib.stof_tree_attn_fwd.restype = i32
         lib.stof_tree_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
         lib.stof_tree_attn_workspace_bytes.restype = sz
+        lib.stof_prefix_attn_fwd.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, P, P, P, P, P,
+                                             ctypes.c_float, ctypes.POINTER(stof_score), P, P, sz, P, P]
+        lib.stof_prefix_attn_fwd.restype = i32
+        lib.stof_prefix_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.stof_prefix_attn_workspace_bytes.restype = sz
         lib.stof_rope_plan_init.argtypes = [ctypes.POINTER(stof_rope_plan), i32, i32, ctypes.c_double, i32,
                                             ctypes.c_double, i64, ctypes.c_double, ctypes.c_double, ctypes.c_double]
         lib.stof_rope_plan_init.restype = i32
@@ -480,6 +486,49 @@ def stof_tree_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens: 
     B, H, T, d, Hkv, cap = _heads_of(where, q, k, v, o)
     _launch(where, device, stream, load_library().stof_tree_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             _dtype_code(q), B, H, Hkv, T, d, cap, _int32(where, "lens", lens, (B,)),
+            None if counts is None else _int32(where, "counts", counts, (B,)),
+            None if tree is None else _int32(where, "tree", tree, (B, T, (T + 31) // 32)),
+            None if positions is None else _int32(where, "positions", positions, (B, T)), float(scale),
+            None if score is None else ctypes.byref(score.as_c(where, H)), o.data_ptr(), workspace.data_ptr(),
+            workspace.nbytes, None if device_error is None else _error_word(where, device_error))
+    return o
+
+
+def stof_prefix_attn_workspace_bytes(B: int, n_prefixes: int, H: int, Hkv: int, T: int, d: int) -> int:
+    return int(load_library().stof_prefix_attn_workspace_bytes(int(B), int(n_prefixes), int(H), int(Hkv), int(T), int(d)))
+
+
+def stof_prefix_attn_fwd(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, prefix_lens: torch.Tensor,
+                         k: torch.Tensor | None, v: torch.Tensor | None, lens: torch.Tensor | None, scale: float,
+                         o: torch.Tensor, workspace: torch.Tensor, tree: torch.Tensor | None = None,
+                         counts: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                         score: Score | None = None, device_error: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q, o: device [B, H, T, d]; k_prefix, v_prefix: [P, Hkv, prefix rows, d], prefix b // (B / P) being request b's;
+    prefix_lens: int32 [P].  k, v [B, Hkv, cap, d], lens and the rest as stof_tree_attn_fwd; k, v and lens None: the
+    prefix alone (cross attention).  The call's error bits are also left in the workspace's first 8 bytes."""
+    where = "stof_prefix_attn_fwd"
+    slopes = score.slopes if score is not None else None
+    device = _device_of(where, q, k_prefix, v_prefix, prefix_lens, k, v, lens, o, workspace, tree, counts, positions, slopes,
+                        device_error)
+    if len(q.shape) != 4 or len(k_prefix.shape) != 4:
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q [B, H, T, d] and k_prefix [P, Hkv, rows, d]")
+    B, H, T, d = q.shape
+    n, Hkv, prefix_cap, pd = k_prefix.shape
+    if (pd != d or v_prefix.shape != k_prefix.shape or o.shape != q.shape or k_prefix.dtype != q.dtype
+            or v_prefix.dtype != q.dtype or o.dtype != q.dtype
+            or not (q.is_contiguous() and k_prefix.is_contiguous() and v_prefix.is_contiguous() and o.is_contiguous())):
+        raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, T, d] and k_prefix, v_prefix [P, Hkv, rows, d], contiguous, one dtype")
+    cap, k_ptr, v_ptr = 0, None, None
+    if k is not None or v is not None or lens is not None:
+        if k is None or v is None or lens is None:
+            raise StofError(STOF_ERR_INVALID_ARG, f"{where}: own caches are k, v and lens, or none of them")
+        _, _, _, _, own_heads, cap = _heads_of(where, q, k, v, o)
+        if own_heads != Hkv:
+            raise StofError(STOF_ERR_SHAPE, f"{where}: k and k_prefix must have the same heads")
+        k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
+    _launch(where, device, stream, load_library().stof_prefix_attn_fwd, q.data_ptr(), k_prefix.data_ptr(),
+            v_prefix.data_ptr(), k_ptr, v_ptr, _dtype_code(q), B, n, H, Hkv, T, d, prefix_cap, cap,
+            _int32(where, "prefix_lens", prefix_lens, (n,)), None if lens is None else _int32(where, "lens", lens, (B,)),
             None if counts is None else _int32(where, "counts", counts, (B,)),
             None if tree is None else _int32(where, "tree", tree, (B, T, (T + 31) // 32)),
             None if positions is None else _int32(where, "positions", positions, (B, T)), float(scale),
