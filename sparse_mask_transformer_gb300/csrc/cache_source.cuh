@@ -238,6 +238,7 @@ struct CacheSource {
         out[cc] = __funnelshift_r(seen(p, row, x, u0 >> 5), seen(p, row, x, (u0 >> 5) + 1), u0 & 31);
     }
   }
+  static __device__ float slope(const Params& p, const Row& row) { return __ldg(p.slopes + row.head); }
   // Distance of the row's nearest (far: farthest) visible key.  Without
   // positions a bound on it does as well: it is 1024 away from it at most.
   static __device__ uint32_t reference(const Params& p, const Row& row, const Item& x, bool far) {

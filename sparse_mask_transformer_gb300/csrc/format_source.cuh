@@ -224,6 +224,7 @@ struct FormatSource {
     for (int cc = 0; cc < BN / 32; ++cc)
       b[cc] = row.nb[4 * cc] | (row.nb[4 * cc + 1] << 8) | (row.nb[4 * cc + 2] << 16) | (row.nb[4 * cc + 3] << 24);
   }
+  static __device__ float slope(const Params& p, const Row& row) { return __ldg(p.slopes + row.head); }
   // Distance of the nearest (far: farthest) key.
   static __device__ uint32_t reference(const Params& p, const Row& row, const Item&, bool far) {
     return reference_distance(row.pos, p.n_tc * 128 - 1, far);

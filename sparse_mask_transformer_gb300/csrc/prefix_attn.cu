@@ -35,64 +35,58 @@ struct PrefixParams : TreeParams {
   int fill, own_fill;               // rows of a tile: of a prefix's, of a request's
   int prow_tiles, prow_group, prow_groups;  // as row_tiles, ..., of a prefix
   const int32_t* plens;
-  int32_t* pline;                   // [NP + 1], as line
-  int32_t* meta;                    // [2] shares of the prefixes' line, of the requests'
-  float* part_o;                    // [2][B H T][d]: parts of runs that lie in one share, of prefixes and requests
-  float2* part_stats;               // [2][B H T]
+  int32_t* pline;                   // [NP], as line [B]: places of the items on their lines
+  int32_t* meta;                    // [4] first worker of the requests' line; share lengths of the prefixes' line, of the requests'
+  float* part_o;                    // [2][copies][B H T][d]: parts of runs that lie in one share, of prefixes and requests
+  float2* part_stats;               // [2][copies][B H T]
   int64_t out_rows;                 // B H T
 };
 
-// Rows of prefix np; -1: out of range.
-__device__ __forceinline__ int prefix_rows(const PrefixParams& p, int np) {
-  const int x = __ldg(p.plens + np);
-  return x >= 0 && x <= p.pcap ? x : -1;
+// Whether a prefix's rows, a request's committed and drafted tokens, are what
+// the call takes.
+__device__ __forceinline__ bool prefix_ok(const PrefixParams& p, int plen) { return plen >= 0 && plen <= p.pcap; }
+__device__ __forceinline__ bool request_ok(const PrefixParams& p, int ctx, int count) {
+  return ctx >= 0 && count >= 1 && count <= p.T && (!p.lens || ctx <= p.cap - count);
 }
-// Prefix rows, committed and drafted tokens of request b; false for one that
-// breaks the bounds or has no token.
-__device__ __forceinline__ bool request_of(const PrefixParams& p, int b, int& plen, int& ctx, int& count) {
-  plen = prefix_rows(p, b / p.n);
-  ctx = p.lens ? __ldg(p.lens + b) : 0;
-  count = p.counts ? __ldg(p.counts + b) : p.T;
-  return plen >= 0 && ctx >= 0 && count >= 1 && count <= p.T && (!p.lens || ctx <= p.cap - count);
-}
-
-// One of the two lines: runs of key tiles of its items.
-struct Line {
-  int row_tiles, row_group, row_groups;
-};
-__device__ __forceinline__ Line line_of(const PrefixParams& p, bool prefix) {
-  return prefix ? Line{p.prow_tiles, p.prow_group, p.prow_groups} : Line{p.row_tiles, p.row_group, p.row_groups};
-}
-// Length of a run of prefix i or request i (0: none).
-__device__ __forceinline__ int run_length(const PrefixParams& p, bool prefix, int i) {
-  if (prefix) {
-    const int rows = prefix_rows(p, i);
-    return rows > 0 ? tiles_of(p, rows) + kItemCost : 0;
-  }
+struct Lengths {
   int plen, ctx, count;
-  return p.lens && request_of(p, i, plen, ctx, count) ? tiles_of(p, ctx + count) + kItemCost : 0;
+};
+// Of request b, three loads at once.
+__device__ __forceinline__ Lengths lengths_of(const PrefixParams& p, int b) {
+  Lengths x;
+  x.plen = __ldg(p.plens + static_cast<unsigned>(b) / static_cast<unsigned>(p.n));
+  x.ctx = p.lens ? __ldg(p.lens + b) : 0;
+  x.count = p.counts ? __ldg(p.counts + b) : p.T;
+  return x;
 }
+// Length of a run of key tiles on its line (0: none).
+__device__ __forceinline__ int prefix_run(const PrefixParams& p, int plen) {
+  return prefix_ok(p, plen) && plen > 0 ? tiles_of(p, plen) + kItemCost : 0;
+}
+__device__ __forceinline__ int request_run(const PrefixParams& p, const Lengths& x) {
+  return p.lens && prefix_ok(p, x.plen) && request_ok(p, x.ctx, x.count) ? tiles_of(p, x.ctx + x.count) + kItemCost : 0;
+}
+// a / b of small numbers (a < 2^15)
+__device__ __forceinline__ int small_div(int a, int b) { return __float2int_rd(__fdividef(a + 0.5f, static_cast<float>(b))); }
 __device__ __forceinline__ int share_length(int all, int shares) { return max(1, (all + shares - 1) / max(1, shares)); }
 
 // Shares of the two lines, of lengths lp and lo: as many workers for each as
 // bring the later end forward.
 __device__ __forceinline__ void divide(const PrefixParams& p, int lp, int lo, int& sp, int& so) {
-  sp = lp > 0 ? kWorkers / p.prow_group : 0;
-  so = lo > 0 ? kWorkers / p.row_group : 0;
-  if (lp == 0 || lo == 0) return;
   const float wp = static_cast<float>(lp) * p.prow_group, wo = static_cast<float>(lo) * p.row_group;
-  const int most = (kWorkers - p.row_group) / p.prow_group;
-  int best = 0x7fffffff;
-  const int x0 = max(1, min(most, static_cast<int>(kWorkers * (wp / (wp + wo)) / p.prow_group)));
-  for (int x = x0; x <= min(most, x0 + 1); ++x) {
-    const int y = (kWorkers - x * p.prow_group) / p.row_group;
-    const int end = max(share_length(lp, x), share_length(lo, y));
-    if (end < best) {
-      best = end;
-      sp = x;
-      so = y;
+  const int most = small_div(kWorkers - (lo > 0 ? p.row_group : 0), p.prow_group);
+  int x = lp == 0 ? 0 : most;
+  if (lp > 0 && lo > 0) x = max(1, min(most, small_div(static_cast<int>(kWorkers * __fdividef(wp, wp + wo)), p.prow_group)));
+  int y = small_div(kWorkers - x * p.prow_group, p.row_group);
+  if (lp > 0 && lo > 0 && x < most) {  // one share more?
+    const int y1 = small_div(kWorkers - (x + 1) * p.prow_group, p.row_group);
+    if (fmaxf(__fdividef(lp, x + 1), __fdividef(lo, y1)) < fmaxf(__fdividef(lp, x), __fdividef(lo, y))) {
+      ++x;
+      y = y1;
     }
   }
+  sp = x;
+  so = y;
 }
 
 struct PrefixSource : CacheSource {
@@ -103,7 +97,7 @@ struct PrefixSource : CacheSource {
     int base;  // position of the item's first key: 0, or the prefix's rows
   };
   struct Shared {
-    int sums[kThreads / 32];
+    int2 sums[kThreads / 32];
     bool prefix[2];        // the workers' lines
     int row[2];            // their row tiles within a group
     int begin[2], end[2];  // and shares
@@ -112,91 +106,113 @@ struct PrefixSource : CacheSource {
   };
   struct Row : CacheSource::Row {
     int b, plen, ctx, count;  // the row's request
+    uint32_t self;            // the word of its tree row that has its own bit
+    float given_slope;
   };
 
   static __device__ void init(Shared& s) { s.bad = 0; }
 
-  // Place of thread's item in the round that begins with item i0 (all threads).
-  static __device__ int place(const Params& p, Shared& s, bool prefix, int i0, int before, int& v, int& total) {
-    const Line l = line_of(p, prefix);
-    const int i = i0 + static_cast<int>(threadIdx.x);
-    v = i < (prefix ? p.NP : p.B) ? run_length(p, prefix, i) * p.Hkv * l.row_groups : 0;
-    return before + block_prefix(v, s.sums, total);
-  }
-  // Length of a line; CTA 0 leaves the items' places for merge_kernel and
-  // reports bad lengths.
-  static __device__ int measure(const Params& p, Shared& s, bool prefix, int& v, int& at) {
-    const int items = prefix ? p.NP : p.B;
-    int32_t* line = prefix ? p.pline : p.line;
-    int all = 0;
-    v = at = 0;
-    for (int i0 = 0; i0 < items; i0 += kThreads) {
-      int total;
-      at = place(p, s, prefix, i0, all, v, total);
-      const int i = i0 + static_cast<int>(threadIdx.x);
-      if (blockIdx.x == 0 && i < items) {
-        line[i] = at;
-        bool bad;
-        if (prefix) {
-          bad = prefix_rows(p, i) < 0;
-        } else {
-          int plen, ctx, count;
-          bad = !request_of(p, i, plen, ctx, count) && plen >= 0 &&
-                !(count == 0 && ctx >= 0 && (!p.lens || ctx <= p.cap));
-        }
-        if (bad) {
-          s.bad = 1;
-          if (p.err) raise_error(p.err, STOF_DEVERR_BAD_LENGTH);
-        }
+  // Lengths of prefix i's and request i's runs on their lines; CTA 0 reports
+  // lengths out of range.
+  static __device__ int2 item_lengths(const Params& p, Shared& s, int i, bool report) {
+    const int plen = i < p.NP ? __ldg(p.plens + i) : 0;
+    Lengths x{0, 0, 0};
+    if (i < p.B) x = lengths_of(p, i);
+    if (report && blockIdx.x == 0) {
+      const bool none = x.count == 0 && x.ctx >= 0 && (!p.lens || x.ctx <= p.cap);  // a request without tokens
+      if (!prefix_ok(p, plen) || (i < p.B && !request_ok(p, x.ctx, x.count) && !none)) {
+        s.bad = 1;
+        if (p.err) raise_error(p.err, STOF_DEVERR_BAD_LENGTH);
       }
-      all += total;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) line[items] = all;
-    return all;
+    return make_int2(i < p.NP ? prefix_run(p, plen) * p.Hkv * p.prow_groups : 0,
+                     i < p.B ? request_run(p, x) * p.Hkv * p.row_groups : 0);
   }
+  // Exclusive prefixes of v over the block's threads, and the totals.
+  static __device__ int2 both_prefixes(int2 v, int2* sums, int2& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int2 x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x.x, off), z = __shfl_up_sync(0xffffffffu, x.y, off);
+      if (lane >= off) {
+        x.x += y;
+        x.y += z;
+      }
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int2 before = make_int2(0, 0);
+    total = make_int2(0, 0);
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int2 y = sums[w];
+      if (w < warp) before = make_int2(before.x + y.x, before.y + y.y);
+      total = make_int2(total.x + y.x, total.y + y.y);
+    }
+    return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
+  }
+  // Both lines at once: a thread has prefix i and request i.
   static __device__ void prologue(const Params& p, Shared& s) {
     dependents_launch();  // merge_kernel may be set up
-    int v[2], at[2], all[2], shares[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) all[x] = measure(p, s, x == 0, v[x], at[x]);
-    divide(p, all[0], all[1], shares[0], shares[1]);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.meta[0] = shares[0];
-      p.meta[1] = shares[1];
+    const int items = max(p.NP, p.B);
+    int2 v, at, all = make_int2(0, 0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < items; i0 += kThreads) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      v = item_lengths(p, s, i, true);
+      if (i0) __syncthreads();  // the sums have been read
+      int2 total;
+      at = both_prefixes(v, s.sums, total);
+      at = make_int2(all.x + at.x, all.y + at.y);
+      if (blockIdx.x == 0) {  // for merge_kernel
+        if (i < p.NP) p.pline[i] = at.x;
+        if (i < p.B) p.line[i] = at.y;
+      }
+      all = make_int2(all.x + total.x, all.y + total.y);
     }
+    int shares[2];
+    divide(p, all.x, all.y, shares[0], shares[1]);
     const int first_own = shares[0] * p.prow_group;  // workers before it are the prefixes'
+    const int length[2] = {share_length(all.x, shares[0]), share_length(all.y, shares[1])};
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.meta[0] = first_own;
+      p.meta[1] = length[0];
+      p.meta[2] = length[1];
+    }
     bool mine[2];
     int begin[2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int w = worker(g), x = w < first_own ? 0 : 1;
-      const int in = w - x * first_own, group = x ? p.row_group : p.prow_group;
-      const int length = share_length(all[x], shares[x]), nth = in / group;
-      mine[g] = x == 0;
-      begin[g] = nth < shares[x] ? min(nth * length, all[x]) : all[x];
+      const int w = worker(g);
+      mine[g] = w < first_own;
+      const int in = mine[g] ? w : w - first_own, group = mine[g] ? p.prow_group : p.row_group, nth = small_div(in, group);
+      const int line = mine[g] ? all.x : all.y, len = mine[g] ? length[0] : length[1];
+      begin[g] = nth < (mine[g] ? shares[0] : shares[1]) ? min(nth * len, line) : line;
       if (threadIdx.x == 0) {
         s.prefix[g] = mine[g];
         s.row[g] = in - nth * group;
         s.begin[g] = begin[g];
-        s.end[g] = begin[g] + min(length, all[x] - begin[g]);
+        s.end[g] = begin[g] + min(len, line - begin[g]);
       }
     }
+    int2 base = make_int2(0, 0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < items; i0 += kThreads) {
+      if (items > kThreads) {  // else v and at are those of the one round above
+        v = item_lengths(p, s, i0 + threadIdx.x, false);
+        __syncthreads();
+        int2 total;
+        at = both_prefixes(v, s.sums, total);
+        at = make_int2(base.x + at.x, base.y + at.y);
+        base = make_int2(base.x + total.x, base.y + total.y);
+      }
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int items = x == 0 ? p.NP : p.B;
-      int base = 0;
-      for (int i0 = 0; i0 < items; i0 += kThreads) {
-        if (items > kThreads) {  // else v and at are those of the one round above
-          int total;
-          at[x] = place(p, s, x == 0, i0, base, v[x], total);
-          base += total;
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (mine[g] == (x == 0) && at[x] <= begin[g] && begin[g] < at[x] + v[x]) {
-            s.i[g] = i0 + threadIdx.x;
-            s.base[g] = at[x];
-          }
+      for (int g = 0; g < 2; ++g) {
+        const int from = mine[g] ? at.x : at.y, to = from + (mine[g] ? v.x : v.y);
+        if (from <= begin[g] && begin[g] < to) {
+          s.i[g] = i0 + threadIdx.x;
+          s.base[g] = from;
         }
       }
     }
@@ -223,18 +239,20 @@ struct PrefixSource : CacheSource {
       }
     }
     __device__ void load(const Params& p) {
-      len = run_length(p, prefix, i);
       if (prefix) {
-        ctx = prefix_rows(p, i);
-        count = 0;
-        plen = 0;
+        ctx = __ldg(p.plens + i);
+        len = prefix_run(p, ctx);
       } else {
-        request_of(p, i, plen, ctx, count);
+        const Lengths x = lengths_of(p, i);
+        plen = x.plen;
+        ctx = x.ctx;
+        count = x.count;
+        len = request_run(p, x);
       }
     }
     __device__ Next next(const Params& p, Shared&, const volatile int*, Segment<Item>& seg) {
-      const Line l = line_of(p, prefix);
-      const int per = p.Hkv * l.row_groups;
+      const int row_tiles = prefix ? p.prow_tiles : p.row_tiles, row_group = prefix ? p.prow_group : p.row_group;
+      const int row_groups = prefix ? p.prow_groups : p.row_groups, per = p.Hkv * row_groups;
 #pragma unroll 1
       while (w < end) {
 #pragma unroll 1
@@ -247,8 +265,8 @@ struct PrefixSource : CacheSource {
         const int to = min(end - base - item * len, len);  // the share's part of the run: [at, to)
         w += to - at;
         const int t0 = max(0, at - kItemCost), t1 = max(0, to - kItemCost);
-        const int hk = item / l.row_groups, rt = (item - hk * l.row_groups) * l.row_group + row;
-        if (t1 <= t0 || rt >= l.row_tiles) continue;
+        const int hk = item / row_groups, rt = (item - hk * row_groups) * row_group + row;
+        if (t1 <= t0 || rt >= row_tiles) continue;
         if (prefix) {
           const int x = rt / p.per_request;
           seg.q_plane = i * p.n + (p.nb > 1 ? rt * p.nb : x);
@@ -289,16 +307,34 @@ struct PrefixSource : CacheSource {
     const int gq = rr / p.T;
     row.t = rr - gq * p.T;
     row.head = x.hk * p.group + gq;
-    live = live && rr < p.rows && request_of(p, row.b, row.plen, row.ctx, row.count) && row.t < row.count;
-    const size_t token = static_cast<size_t>(row.b) * p.T + row.t;
-    row.pos = live && p.positions ? __ldg(p.positions + token) : (live ? row.plen + row.ctx + row.t : 0);
+    // what is loaded is loaded at once
+    const int b = min(row.b, p.B - 1);
+    const size_t token = static_cast<size_t>(b) * p.T + row.t;
+    Lengths y{x.base, x.ctx, x.count};
+    if (x.prefix) {
+      y.plen = x.ctx;
+      y.ctx = p.lens ? __ldg(p.lens + b) : 0;
+      y.count = p.counts ? __ldg(p.counts + b) : p.T;
+    }
+    row.tree = p.tree ? p.tree + token * p.words : nullptr;
+    row.self = p.positions && p.tree ? __ldg(row.tree + (row.t >> 5)) : ~0u;
+    const int given = p.positions ? __ldg(p.positions + token) : 0;
+    row.given_slope = p.slopes ? __ldg(p.slopes + min(row.head, p.H - 1)) : 0.f;
+    live = live && rr < p.rows && request_ok(p, y.ctx, y.count) && row.t < y.count;
+    if (!live) y = Lengths{0, 0, 0};
+    row.plen = y.plen;
+    row.ctx = y.ctx;
+    row.count = y.count;
+    row.pos = p.positions ? given : y.plen + y.ctx + row.t;
     row.out = (static_cast<size_t>(row.b) * p.H + row.head) * p.T + row.t;
-    row.tree = live && p.tree ? p.tree + token * p.words : nullptr;
+    if (!live) row.tree = nullptr;
     return live;
   }
+  static __device__ float slope(const Params&, const Row& row) { return row.given_slope; }
   // Distance of the nearest (far: farthest) key that the row sees, in the
   // prefix or of the request's own: the parts of a row have one reference.
   static __device__ uint32_t reference(const Params& p, const Row& row, const Item&, bool far) {
+    if (!far && row.self >> (row.t & 31) & 1u) return 0u;  // it sees itself
     CacheSource::Item own;
     own.b = row.b;
     own.count = row.count;
@@ -320,28 +356,41 @@ struct PrefixSource : CacheSource {
       lower_by_distance(sr, c, slope, row.pos, x.base + j0, base);
     }
   }
-  // The run is all that its rows see, and lies in one share.
-  static __device__ bool whole(const Params& p, const Item& x) { return x.whole && (x.prefix ? !p.lens : x.base == 0); }
-  // Parts of whole runs by the row of O; of others by the worker, as CacheSource.
+  // The run is all that its rows see, and lies in one share and one copy.
+  static __device__ bool whole(const Params& p, const Item& x) {
+    return x.whole && p.copies == 1 && (x.prefix ? !p.lens : x.base == 0);
+  }
+  // Parts of whole runs by the row of O; of others by the worker, as
+  // CacheSource; those of the copies (r: the row of the tile) one after the other.
   static __device__ size_t slot_row(const Params& p, const Item& x, int g, int r) {
     return static_cast<size_t>(2 * worker(g) + (x.t0 == 0 ? 1 : 0)) * p.slot_rows + r;
   }
   static __device__ float* partial_o(const Params& p, const Item& x, const Row& row, int g, int r, int d) {
-    return x.whole ? p.part_o + ((x.prefix ? 0 : p.out_rows) + row.out) * d : p.slots + slot_row(p, x, g, r) * d;
+    return x.whole ? p.part_o + part_row(p, x, row, r) * d : p.slots + slot_row(p, x, g, r) * d;
   }
   static __device__ void put_stats(const Params& p, const Item& x, const Row& row, int g, int r, float m, float l) {
-    (x.whole ? p.part_stats[(x.prefix ? 0 : p.out_rows) + row.out] : p.stats[slot_row(p, x, g, r)]) = make_float2(m, l);
+    (x.whole ? p.part_stats[part_row(p, x, row, r)] : p.stats[slot_row(p, x, g, r)]) = make_float2(m, l);
+  }
+  static __device__ size_t part_row(const Params& p, const Item& x, const Row& row, int r) {
+    return ((x.prefix ? 0 : p.copies) + r * p.copies / kBM) * p.out_rows + row.out;
   }
 };
 
-// Merges the parts of the rows, those of the prefix first.  WPR warps per row,
-// warp x of a row the parts x, x + WPR, ..., kBatch of them in flight; four
-// rows of one warp, or one row of four, a block.  (Launched while the main
-// kernel still runs, it begins when that has ended.)
+__device__ __forceinline__ void add_part(float4& o, float& l, float w, const float4& y, float sum) {
+  l = fmaf(w, sum, l);
+  o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
+}
+
+// Merges the parts of the rows, those of the prefix first.  WPR warps per row;
+// a part takes D / 4 lanes, four columns each, so that a warp takes one (d =
+// 128) or two (d = 64) parts at a time, kBatch times that in flight.  Four rows
+// of one warp, or one row of four, a block.  (Launched while the main kernel
+// still runs, it begins when that has ended.)
 template <int D, bool BF16, int WPR>
 __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ PrefixParams p) {
-  constexpr int E = D / 32, kBatch = 8;
-  __shared__ float s_o[4][D], s_m[4], s_l[4];
+  constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes, kBatch = 8;
+  __shared__ float4 s_o[4][kLanes];
+  __shared__ float s_m[4], s_l[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
   if (blockIdx.x == gridDim.x - 1) {  // the last block: the call's error bits
     dependents_wait();
@@ -351,71 +400,67 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
     if (threadIdx.x == 0) *p.word = (late ? STOF_DEVERR_PIPE_TIMEOUT : 0) | (bad ? STOF_DEVERR_BAD_LENGTH : 0);
     return;
   }
-  const int64_t out = static_cast<int64_t>(blockIdx.x) * (4 / WPR) + warp / WPR;
+  const unsigned out = blockIdx.x * (4 / WPR) + warp / WPR;
   if (out >= p.out_rows) return;  // (one row: the whole block)
-  const int x = static_cast<int>(out / p.T), t = static_cast<int>(out - static_cast<int64_t>(x) * p.T);
-  const int b = x / p.H, h = x - b * p.H, hk = h / p.group, rr = (h - hk * p.group) * p.T + t;
-  int plen, ctx, count;
-  if (!request_of(p, b, plen, ctx, count) || t >= count) return;
+  const unsigned bh = out / p.T, b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
+  const int t = static_cast<int>(out - bh * p.T), rr = static_cast<int>(h - hk * p.group) * p.T + t;
+  const Lengths x = lengths_of(p, b);
+  if (!prefix_ok(p, x.plen) || !request_ok(p, x.ctx, x.count) || t >= x.count) return;
+  // the row's tile of its prefix's run and place in it
+  const unsigned np = b / p.n, in = b - np * p.n;
+  int prt = p.nb > 1 ? in / p.nb : in * p.per_request + rr / 128;
+  const int pr = p.nb > 1 ? (in - prt * p.nb) * p.rows + rr : rr % 128;
+  const int lens[2] = {prefix_run(p, x.plen), request_run(p, x)};
   dependents_wait();
-  const int sp = __ldcg(p.meta), so = __ldcg(p.meta + 1);
+  const int first_own = __ldcg(p.meta), share[2] = {__ldcg(p.meta + 1), __ldcg(p.meta + 2)};
+  const int place0[2] = {__ldcg(p.pline + np), __ldcg(p.line + b)};
   // a run's parts; the slot of its row in the share of the first of them, slots from share to share
   struct Run {
     int n;
     int64_t slot, step;
   };
-  auto run_of = [&](bool prefix) {
-    const int item = prefix ? b / p.n : b, len = run_length(p, prefix, item);
+  auto run_of = [&](int y, int rt, int r, int row_group, int row_groups, int worker0) {
+    const int len = lens[y];
     if (len == 0) return Run{0, 0, 0};
-    const Line l = line_of(p, prefix);
-    int rt = rr / 128, r = rr - rt * 128;  // the row's tile of the run and place in it
-    if (prefix) {
-      const int in = b - item * p.n;
-      rt = p.nb > 1 ? in / p.nb : in * p.per_request + rt;
-      if (p.nb > 1) r = (in - rt * p.nb) * p.rows + rr;
-    }
-    const int32_t* line = prefix ? p.pline : p.line;
-    const int share = share_length(__ldcg(line + (prefix ? p.NP : p.B)), prefix ? sp : so), group = rt / l.row_group;
-    const int at = __ldcg(line + item) + (hk * l.row_groups + group) * len, w0 = (at + kItemCost) / share;
-    const int64_t worker = (prefix ? 0 : sp * p.prow_group) + w0 * l.row_group + rt - group * l.row_group;
-    return Run{(at + len - 1) / share - w0 + 1, 2 * worker * p.slot_rows + r, 2 * static_cast<int64_t>(l.row_group) * p.slot_rows};
+    const int group = rt / row_group, at = place0[y] + (static_cast<int>(hk) * row_groups + group) * len;
+    const int w0 = (at + kItemCost) / share[y];
+    const int64_t worker = worker0 + w0 * row_group + rt - group * row_group;
+    return Run{(at + len - 1) / share[y] - w0 + 1, 2 * worker * p.slot_rows + r, 2 * static_cast<int64_t>(row_group) * p.slot_rows};
   };
-  const Run pre = run_of(true), own = run_of(false);
-  const int parts = pre.n + own.n;
+  const Run pre = run_of(0, prt, pr, p.prow_group, p.prow_groups, 0);
+  const Run own = run_of(1, rr / 128, rr % 128, p.row_group, p.row_groups, first_own);
+  const int copies = p.copies, shift = copies >> 1;  // 1, 2, 4: shifts of 0, 1, 2
+  const int parts = (pre.n + own.n) * copies;
   if (parts == 1) return;  // finished by its one worker (none: a row that sees nothing, 0)
   auto place = [&](int i, const float*& o, const float2*& st) {
+    const int copy = i & (copies - 1);
+    i >>= shift;
     const bool prefix = i < pre.n;
     const Run u = prefix ? pre : own;
     if (!prefix) i -= pre.n;
     // a whole run: by the row; else the first share's part is its worker's last segment, the others' their first
-    const int64_t at = u.n == 1 ? (prefix ? 0 : p.out_rows) + out : u.slot + i * u.step + (i == 0 ? p.slot_rows : 0);
+    const int64_t at = u.n == 1 ? ((prefix ? 0 : copies) + copy) * p.out_rows + static_cast<int64_t>(out)
+                                : u.slot + i * u.step + (i == 0 ? p.slot_rows : 0) + copy * (kBM / copies);
     o = (u.n == 1 ? p.part_o : p.slots) + at * D;
     st = (u.n == 1 ? p.part_stats : p.stats) + at;
   };
-  float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int i0 = part; i0 < parts; i0 += WPR * kBatch) {
+  for (int i0 = part * kAtOnce + lane / kLanes; i0 < parts; i0 += WPR * kAtOnce * kBatch) {
     float2 st[kBatch];
-    float y[kBatch][E];
+    float4 y[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int k = i0 + i * WPR;
+      const int k = i0 + i * WPR * kAtOnce;
       st[i] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[i][e] = 0.f;
+      y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k < parts) {
         const float* src;
         const float2* stats;
         place(k, src, stats);
         st[i] = __ldcg(stats);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 z = __ldcg(reinterpret_cast<const float2*>(src + lane * E + e));
-          y[i][e] = z.x;
-          y[i][e + 1] = z.y;
-        }
+        y[i] = __ldcg(reinterpret_cast<const float4*>(src) + lane % kLanes);
       }
     }
     float mn = m;
@@ -423,47 +468,42 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
     for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, st[i].x);
     const float ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref);
     l *= a;
+    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= a;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float w = ex2(st[i].x - ref);
-      l = fmaf(w, st[i].y, l);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(w, y[i][e], o[e]);
-    }
+    for (int i = 0; i < kBatch; ++i) add_part(o, l, ex2(st[i].x - ref), y[i], st[i].y);
     m = mn;
   }
-  uint32_t* to = static_cast<uint32_t*>(p.o) + ((static_cast<size_t>(out) * D) >> 1);
-  if constexpr (WPR == 1) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) to[(lane * E + e) >> 1] = pack2<BF16>(o[e] * inv, o[e + 1] * inv);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+  if constexpr (kAtOnce == 2) {  // the two halves of the warp
+    const float other = __shfl_xor_sync(0xffffffffu, m, 16), mn = fmaxf(m, other), ref = mn == -INFINITY ? 0.f : mn;
+    const float a = ex2(m - ref);
+    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+    l *= a;
+    m = mn;
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+  }
+  if constexpr (WPR > 1) {
+    if (lane < kLanes) s_o[warp][lane] = o;
     if (lane == 0) {
       s_m[warp] = m;
       s_l[warp] = l;
     }
     __syncthreads();
-    float mm = -INFINITY, sum = 0.f;
+    if (warp) return;
+    float ref = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    if (ref == -INFINITY) ref = 0.f;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_m[w]);
-    if (mm == -INFINITY) mm = 0.f;
-    const int c = 2 * threadIdx.x;  // two columns a thread
-    if (c >= D) return;
-    float y0 = 0.f, y1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float a = ex2(s_m[w] - mm);
-      sum = fmaf(a, s_l[w], sum);
-      y0 = fmaf(a, s_o[w][c], y0);
-      y1 = fmaf(a, s_o[w][c + 1], y1);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    to[c >> 1] = pack2<BF16>(y0 * inv, y1 * inv);
+    for (int w = 0; w < 4; ++w) add_part(o, l, ex2(s_m[w] - ref), s_o[w][lane % kLanes], s_l[w]);
   }
+  if (lane >= kLanes) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  static_cast<uint2*>(p.o)[static_cast<size_t>(out) * kLanes + lane] =
+      make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
 }
 
 template <int D, bool BF16, int MODE>
@@ -498,9 +538,14 @@ stof_status launch_prefix(const void* q, const void* kp, const void* vp, const v
     default: st = launch_mode<D, BF16, MODE_DISTANCE>(mq, mk, mv, p, s); break;
   }
   if (st != STOF_OK) return st;
-  // one warp a row where the rows are many for their parts, as in tree_attn.cu
-  const int64_t runs = static_cast<int64_t>(p.NP) * p.Hkv * p.prow_tiles;
-  const bool one = p.out_rows >= 128 * (1 + kWorkers / (runs < kWorkers ? runs : kWorkers));
+  // A row is merged by one warp where the rows are many for their parts (of
+  // which the host knows the most that a prefix's run may have), else by four.
+  // One and four, the whole call: d = 128, 128 rows 20.8 and 16.6 us, 512 rows
+  // of 39 parts 34.0 and 28.9, 1024 41.0 and 37.4, 1536 of 20 45.2 and 45.5, 4096
+  // of 5 54.0 and 73.2; d = 64, 256 rows of 39 22.4 and 18.6, 512 18.5 and 18.6, 1024
+  // 20.1 and 22.5.
+  const int64_t runs = static_cast<int64_t>(p.NP) * p.Hkv * p.prow_tiles, parts = 1 + kWorkers / (runs < kWorkers ? runs : kWorkers);
+  const bool one = p.out_rows >= (D == 128 ? 64 : 24) * parts;
   const unsigned grid = static_cast<unsigned>(one ? (p.out_rows + 3) / 4 : p.out_rows) + 1;
   const cudaError_t e = launch_early(one ? merge_kernel<D, BF16, 1> : merge_kernel<D, BF16, 4>, dim3(grid), 128, 0, s, p);
   return record_cuda(e) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
@@ -509,7 +554,7 @@ stof_status launch_prefix(const void* q, const void* kp, const void* vp, const v
 // The sizes that follow from a call's.
 struct Sizes {
   int64_t rows, slot_rows, out_rows;
-  int nb, per_request;
+  int nb, per_request, fill, copies;
 };
 // False for sizes that the call does not take.
 bool sizes_of(int B, int n_prefixes, int H, int Hkv, int T, int d, Sizes* z) {
@@ -520,7 +565,9 @@ bool sizes_of(int B, int n_prefixes, int H, int Hkv, int T, int d, Sizes* z) {
   const int64_t n = B / n_prefixes, fit = z->rows < 128 ? 128 / z->rows : 1;
   z->nb = static_cast<int>(n < fit ? n : fit);
   z->per_request = static_cast<int>((z->rows + 127) / 128);
-  z->slot_rows = z->rows < 128 ? z->rows * z->nb : 128;
+  z->fill = static_cast<int>(z->rows < 128 ? z->rows * z->nb : 128);
+  z->copies = copies_of(d, z->fill);
+  z->slot_rows = z->copies > 1 ? kBM : z->fill;
   z->out_rows = static_cast<int64_t>(B) * H * T;
   return true;
 }
@@ -533,7 +580,7 @@ using namespace stof;
 extern "C" size_t stof_prefix_attn_workspace_bytes(int B, int n_prefixes, int H, int Hkv, int T, int d) {
   Sizes z;
   if (!sizes_of(B, n_prefixes, H, Hkv, T, d, &z) || z.out_rows >= (1ll << 31)) return 0;
-  const size_t slots = static_cast<size_t>(2 * kWorkers) * z.slot_rows, parts = 2 * static_cast<size_t>(z.out_rows);
+  const size_t slots = static_cast<size_t>(2 * kWorkers) * z.slot_rows, parts = 2 * static_cast<size_t>(z.copies) * z.out_rows;
   return kErrorBytes + up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + up256(parts * d * sizeof(float)) +
          up256(parts * sizeof(float2)) + (static_cast<size_t>(B) + n_prefixes + 4) * sizeof(int32_t);
 }
@@ -614,12 +661,12 @@ extern "C" stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix,
   p.nb = z.nb;
   p.per_request = z.per_request;
   p.own_fill = static_cast<int>(z.rows < 128 ? z.rows : 128);
-  p.fill = p.own_fill * p.nb;
+  p.fill = z.fill;
   p.plens = prefix_lens;
   p.out_rows = z.out_rows;
-  p.copies = copies_of(d, p.fill);
+  p.copies = z.copies;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t slots = static_cast<size_t>(2 * kWorkers) * p.slot_rows, parts = 2 * static_cast<size_t>(z.out_rows);
+  const size_t slots = static_cast<size_t>(2 * kWorkers) * p.slot_rows, parts = 2 * static_cast<size_t>(z.copies) * z.out_rows;
   p.word = reinterpret_cast<long long*>(ws);
   p.status = reinterpret_cast<int*>(ws + 256);
   ws += kErrorBytes;
@@ -632,8 +679,8 @@ extern "C" stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix,
   p.part_stats = reinterpret_cast<float2*>(ws);
   ws += up256(parts * sizeof(float2));
   p.line = reinterpret_cast<int32_t*>(ws);
-  p.pline = p.line + B + 1;
-  p.meta = p.pline + n_prefixes + 1;
+  p.pline = p.line + B;
+  p.meta = p.pline + n_prefixes;
   const int mode = mode_of(scale, softcap, p.slopes != nullptr);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dt == STOF_BF16;

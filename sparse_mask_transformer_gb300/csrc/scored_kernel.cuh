@@ -114,10 +114,15 @@ constexpr int kReaders = 5;  // the MMA warp, four softmax warps
 enum class Next { segment, none, lost };  // lost: a wait ran out
 
 // What one worker has in shared memory.
+// (SRC::kTwoPlaces: the copies' rows are parts that the source's own merging
+// puts together.)
+template <class SRC, int REP>
+constexpr bool kMerges = REP > 1 && !SRC::kTwoPlaces;
 template <class SRC, int D, int REP>
 struct Worker {
+  using Sh = Shape<D, kMerges<SRC, REP> ? REP : 1>;
   uint64_t q_full, q_done;  // Q is in place; the segment's score MMAs are done
-  uint64_t k_full[Shape<D, REP>::K], k_free[Shape<D, REP>::K], v_full[Shape<D, REP>::V], v_free[Shape<D, REP>::V];
+  uint64_t k_full[Sh::K], k_free[Sh::K], v_full[Sh::V], v_free[Sh::V];
   uint64_t s_full, s_free, p_full, pv_done, merge, drain;
   uint64_t ring_full[kRing], ring_free[kRing];
   Segment<typename SRC::Item> ring[kRing];  // n < 0: no more segments
@@ -128,13 +133,13 @@ struct Worker {
 
 template <class SRC, int D, int REP>
 struct alignas(1024) Smem {
-  using Sh = Shape<D, REP>;
+  using Sh = typename Worker<SRC, D, REP>::Sh;
   uint8_t q[2][kBM * D * 2];
   uint8_t k[2][Sh::K][Sh::STAGE];
   uint8_t v[2][Sh::V][Sh::STAGE];
-  // REP > 1: 32 columns of O of the copies but the first, and their (max, sum)
-  float4 merge[2][REP > 1 ? (REP - 1) * (kBM / REP) * 8 : 1];
-  float2 merge_stats[2][REP > 1 ? (REP - 1) * (kBM / REP) : 1];
+  // 32 columns of O of the copies but the first, and their (max, sum)
+  float4 merge[2][kMerges<SRC, REP> ? (REP - 1) * (kBM / REP) * 8 : 1];
+  float2 merge_stats[2][kMerges<SRC, REP> ? (REP - 1) * (kBM / REP) : 1];
   Worker<SRC, D, REP> w[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -260,7 +265,7 @@ template <class SRC, int D, bool BF16, int MODE, int REP>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ typename SRC::Params p) {
-  using Sh = Shape<D, REP>;
+  using Sh = typename Worker<SRC, D, REP>::Sh;
   constexpr int BN = Sh::BN, REGIONS = D / 64, Q_ATOM = kBM * 128;
   constexpr int KEYS = BN / REP, CHUNKS = KEYS / 32, ROWS = kBM / REP;  // a thread's keys; rows of one copy of Q
   using Shared = Smem<SRC, D, REP>;
@@ -300,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if constexpr (SRC::kTwoPlaces) {
+    dependents_wait();  // launched while the stream's last kernel may still run
     // Q's rows that no copy fills: what they hold would choose the way that
     // whole warps take, and with it the other rows' roundings
     if (p.fill * REP < kBM || p.own_fill * REP < kBM) {
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float slope = 0.f;
       uint32_t base = 0;  // the row's reference distance
       if (MODE == MODE_DISTANCE && p.slopes && live) {
-        slope = __ldg(p.slopes + row.head) * kLog2e;
+        slope = SRC::slope(p, row) * kLog2e;
         base = SRC::reference(p, row, seg.item, slope < 0.f);
       }
       float m_ref = -INFINITY, l = 0.f;
@@ -660,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
-      if constexpr (REP > 1) {
+      if constexpr (kMerges<SRC, REP>) {
         // A warp has rows of one copy: the first copy's warps merge the
         // others' rows with their own, 32 columns at a time through shared
         // memory.  (The next segment's rows come after barriers of its tiles.)
@@ -863,6 +869,8 @@ stof_status launch_scored(const CUtensorMap& mq, const CUtensorMap& mk, const CU
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, p), last = cudaGetLastError();
     return record_cuda(e != cudaSuccess ? e : last) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
   }
+  if constexpr (SRC::kTwoPlaces)
+    return record_cuda(launch_early(kernel, dim3(grid), kThreads, smem, s, mq, mk, mv, p)) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
   kernel<<<grid, kThreads, smem, s>>>(mq, mk, mv, p);
   return record_cuda(cudaGetLastError()) == cudaSuccess ? STOF_OK : STOF_ERR_CUDA;
 }
