@@ -90,6 +90,7 @@ struct CacheSource {
     int b[2], base[2];     // request that holds a share's begin, its place on the line
     int bad;               // CTA 0: a request breaks the bounds
   };
+  struct Loads {};
   struct Row {
     int head, t, pos;
     size_t out;
@@ -199,7 +200,7 @@ struct CacheSource {
 
   static __device__ int tile_key(const Params&, const Item& x, int t) { return (x.t0 + t) * x.tile; }
   static __device__ int tile_end(const Item& x, int t) { return min(x.tile, x.ctx + x.count - (x.t0 + t) * x.tile); }
-  static __device__ bool begin_row(const Params& p, Row& row, const Segment<Item>& seg, int r) {
+  static __device__ bool begin_row(const Params& p, Row& row, const Loads&, const Segment<Item>& seg, int r) {
     const Item& x = seg.item;
     const int rr = seg.q_row + r, gq = rr / p.T;
     row.t = rr - gq * p.T;

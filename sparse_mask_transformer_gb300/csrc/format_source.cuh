@@ -55,6 +55,7 @@ struct FormatSource {
     int asked;                 // requests so far; under the lock
     int done;                  // a request was refused: none follows
   };
+  struct Loads {};
   struct Row {
     int head;
     int pos;                 // the row's position among the keys
@@ -198,7 +199,7 @@ struct FormatSource {
     }
     return J * 128 + 64 * (t & two);
   }
-  static __device__ bool begin_row(const Params& p, Row& row, const Segment<Item>& seg, int r) {
+  static __device__ bool begin_row(const Params& p, Row& row, const Loads&, const Segment<Item>& seg, int r) {
     row.head = seg.item.head;
     row.i = seg.q_row + r;
     row.pos = row.i + p.q_start;

@@ -37,8 +37,8 @@ struct PrefixParams : TreeParams {
   const int32_t* plens;
   int32_t* pline;                   // [NP], as line [B]: places of the items on their lines
   int32_t* meta;                    // [4] first worker of the requests' line; share lengths of the prefixes' line, of the requests'
-  float* part_o;                    // [2][copies][B H T][d]: parts of runs that lie in one share, of prefixes and requests
-  float2* part_stats;               // [2][copies][B H T]
+  // behind the workers' slots: [2][copies][B H T] parts of runs that lie in one share, of prefixes and of requests
+  int64_t parts;                    // their first row
   int64_t out_rows;                 // B H T
 };
 
@@ -103,6 +103,11 @@ struct PrefixSource : CacheSource {
     int begin[2], end[2];  // and shares
     int i[2], base[2];     // the prefix or request that holds a share's begin, its place on the line
     int bad;               // CTA 0: a length breaks the bounds
+  };
+  struct Loads {
+    int ctx, count, position;
+    uint32_t self;
+    float slope;
   };
   struct Row : CacheSource::Row {
     int b, plen, ctx, count;  // the row's request
@@ -293,41 +298,54 @@ struct PrefixSource : CacheSource {
     __device__ void drain(Shared&) {}
   };
 
-  static __device__ bool begin_row(const Params& p, Row& row, const Segment<Item>& seg, int r) {
+  // Request, head and token of row r of a segment's tile; whether the call has
+  // such a row, its lengths aside.
+  static __device__ bool place_row(const Params& p, const Segment<Item>& seg, int r, int& b, int& head, int& t) {
     const Item& x = seg.item;
     int rr = seg.q_row + r;
-    row.b = seg.q_plane;
-    bool live = true;
+    b = seg.q_plane;
+    bool is = true;
     if (x.prefix && p.nb > 1) {
       const int in = r / p.rows;
       rr = r - in * p.rows;
-      row.b += in;
-      live = in < p.nb && row.b < (x.b + 1) * p.n;
+      b += in;
+      is = in < p.nb && b < (x.b + 1) * p.n;
     }
     const int gq = rr / p.T;
-    row.t = rr - gq * p.T;
-    row.head = x.hk * p.group + gq;
-    // what is loaded is loaded at once
-    const int b = min(row.b, p.B - 1);
-    const size_t token = static_cast<size_t>(b) * p.T + row.t;
-    Lengths y{x.base, x.ctx, x.count};
+    t = rr - gq * p.T;
+    head = x.hk * p.group + gq;
+    return is && rr < p.rows;
+  }
+  // What is loaded for a row, all of it at once.
+  static __device__ void load_row(const Params& p, Loads& y, const Segment<Item>& seg, int r) {
+    const Item& x = seg.item;
+    int b, head, t;
+    place_row(p, seg, r, b, head, t);
+    b = min(b, p.B - 1);
+    const size_t token = static_cast<size_t>(b) * p.T + t;
+    y.ctx = x.ctx;
+    y.count = x.count;
     if (x.prefix) {
-      y.plen = x.ctx;
       y.ctx = p.lens ? __ldg(p.lens + b) : 0;
       y.count = p.counts ? __ldg(p.counts + b) : p.T;
     }
-    row.tree = p.tree ? p.tree + token * p.words : nullptr;
-    row.self = p.positions && p.tree ? __ldg(row.tree + (row.t >> 5)) : ~0u;
-    const int given = p.positions ? __ldg(p.positions + token) : 0;
-    row.given_slope = p.slopes ? __ldg(p.slopes + min(row.head, p.H - 1)) : 0.f;
-    live = live && rr < p.rows && request_ok(p, y.ctx, y.count) && row.t < y.count;
-    if (!live) y = Lengths{0, 0, 0};
-    row.plen = y.plen;
-    row.ctx = y.ctx;
-    row.count = y.count;
-    row.pos = p.positions ? given : y.plen + y.ctx + row.t;
+    if (p.positions) {
+      y.position = __ldg(p.positions + token);
+      if (p.tree) y.self = __ldg(p.tree + token * p.words + (t >> 5));
+    }
+    if (p.slopes) y.slope = __ldg(p.slopes + min(head, p.H - 1));
+  }
+  static __device__ bool begin_row(const Params& p, Row& row, const Loads& y, const Segment<Item>& seg, int r) {
+    const Item& x = seg.item;
+    const bool live = place_row(p, seg, r, row.b, row.head, row.t) && request_ok(p, y.ctx, y.count) && row.t < y.count;
+    row.plen = live ? (x.prefix ? x.ctx : x.base) : 0;
+    row.ctx = live ? y.ctx : 0;
+    row.count = live ? y.count : 0;
+    row.self = p.positions && p.tree ? y.self : ~0u;
+    row.given_slope = y.slope;
+    row.pos = p.positions ? y.position : row.plen + row.ctx + row.t;
     row.out = (static_cast<size_t>(row.b) * p.H + row.head) * p.T + row.t;
-    if (!live) row.tree = nullptr;
+    row.tree = live && p.tree ? p.tree + (static_cast<size_t>(row.b) * p.T + row.t) * p.words : nullptr;
     return live;
   }
   static __device__ float slope(const Params&, const Row& row) { return row.given_slope; }
@@ -366,13 +384,13 @@ struct PrefixSource : CacheSource {
     return static_cast<size_t>(2 * worker(g) + (x.t0 == 0 ? 1 : 0)) * p.slot_rows + r;
   }
   static __device__ float* partial_o(const Params& p, const Item& x, const Row& row, int g, int r, int d) {
-    return x.whole ? p.part_o + part_row(p, x, row, r) * d : p.slots + slot_row(p, x, g, r) * d;
+    return p.slots + part_row(p, x, row, g, r) * d;
   }
   static __device__ void put_stats(const Params& p, const Item& x, const Row& row, int g, int r, float m, float l) {
-    (x.whole ? p.part_stats[part_row(p, x, row, r)] : p.stats[slot_row(p, x, g, r)]) = make_float2(m, l);
+    p.stats[part_row(p, x, row, g, r)] = make_float2(m, l);
   }
-  static __device__ size_t part_row(const Params& p, const Item& x, const Row& row, int r) {
-    return ((x.prefix ? 0 : p.copies) + r * p.copies / kBM) * p.out_rows + row.out;
+  static __device__ size_t part_row(const Params& p, const Item& x, const Row& row, int g, int r) {
+    return x.whole ? p.parts + ((x.prefix ? 0 : p.copies) + r * p.copies / kBM) * p.out_rows + row.out : slot_row(p, x, g, r);
   }
 };
 
@@ -391,7 +409,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
   constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes, kBatch = 8;
   __shared__ float4 s_o[4][kLanes];
   __shared__ float s_m[4], s_l[4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), part = warp % WPR;
   if (blockIdx.x == gridDim.x - 1) {  // the last block: the call's error bits
     dependents_wait();
     int bits = 0;
@@ -414,35 +432,33 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
   dependents_wait();
   const int first_own = __ldcg(p.meta), share[2] = {__ldcg(p.meta + 1), __ldcg(p.meta + 2)};
   const int place0[2] = {__ldcg(p.pline + np), __ldcg(p.line + b)};
-  // a run's parts; the slot of its row in the share of the first of them, slots from share to share
+  // A run's parts, and where they are: the first, the others, from one to the
+  // next, from copy to copy.  A whole run's is by the row; else the first
+  // share's part is its worker's last segment, the others' their first.
+  const int copies = p.copies, shift = copies >> 1;  // 1, 2, 4: shifts of 0, 1, 2
   struct Run {
-    int n;
-    int64_t slot, step;
+    int n, step;
+    int64_t first, rest, copy;
   };
   auto run_of = [&](int y, int rt, int r, int row_group, int row_groups, int worker0) {
     const int len = lens[y];
-    if (len == 0) return Run{0, 0, 0};
+    if (len == 0) return Run{0, 0, 0, 0, 0};
     const int group = rt / row_group, at = place0[y] + (static_cast<int>(hk) * row_groups + group) * len;
-    const int w0 = (at + kItemCost) / share[y];
-    const int64_t worker = worker0 + w0 * row_group + rt - group * row_group;
-    return Run{(at + len - 1) / share[y] - w0 + 1, 2 * worker * p.slot_rows + r, 2 * static_cast<int64_t>(row_group) * p.slot_rows};
+    const int w0 = (at + kItemCost) / share[y], n = (at + len - 1) / share[y] - w0 + 1;
+    if (n == 1) return Run{1, 0, p.parts + y * copies * p.out_rows + static_cast<int64_t>(out), 0, p.out_rows};
+    const int rest = 2 * (worker0 + w0 * row_group + rt - group * row_group) * p.slot_rows + r;
+    return Run{n, 2 * row_group * p.slot_rows, rest + p.slot_rows, rest, kBM / copies};
   };
   const Run pre = run_of(0, prt, pr, p.prow_group, p.prow_groups, 0);
   const Run own = run_of(1, rr / 128, rr % 128, p.row_group, p.row_groups, first_own);
-  const int copies = p.copies, shift = copies >> 1;  // 1, 2, 4: shifts of 0, 1, 2
   const int parts = (pre.n + own.n) * copies;
   if (parts == 1) return;  // finished by its one worker (none: a row that sees nothing, 0)
-  auto place = [&](int i, const float*& o, const float2*& st) {
+  auto place = [&](int i) {
     const int copy = i & (copies - 1);
     i >>= shift;
-    const bool prefix = i < pre.n;
-    const Run u = prefix ? pre : own;
-    if (!prefix) i -= pre.n;
-    // a whole run: by the row; else the first share's part is its worker's last segment, the others' their first
-    const int64_t at = u.n == 1 ? ((prefix ? 0 : copies) + copy) * p.out_rows + static_cast<int64_t>(out)
-                                : u.slot + i * u.step + (i == 0 ? p.slot_rows : 0) + copy * (kBM / copies);
-    o = (u.n == 1 ? p.part_o : p.slots) + at * D;
-    st = (u.n == 1 ? p.part_stats : p.stats) + at;
+    if (i < pre.n) return (i ? pre.rest + i * pre.step : pre.first) + copy * pre.copy;
+    i -= pre.n;
+    return (i ? own.rest + i * own.step : own.first) + copy * own.copy;
   };
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -456,11 +472,9 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
       st[i] = make_float2(-INFINITY, 0.f);
       y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k < parts) {
-        const float* src;
-        const float2* stats;
-        place(k, src, stats);
-        st[i] = __ldcg(stats);
-        y[i] = __ldcg(reinterpret_cast<const float4*>(src) + lane % kLanes);
+        const int64_t at = place(k);
+        st[i] = __ldcg(p.stats + at);
+        y[i] = __ldcg(reinterpret_cast<const float4*>(p.slots) + at * kLanes + lane % kLanes);
       }
     }
     float mn = m;
@@ -580,9 +594,9 @@ using namespace stof;
 extern "C" size_t stof_prefix_attn_workspace_bytes(int B, int n_prefixes, int H, int Hkv, int T, int d) {
   Sizes z;
   if (!sizes_of(B, n_prefixes, H, Hkv, T, d, &z) || z.out_rows >= (1ll << 31)) return 0;
-  const size_t slots = static_cast<size_t>(2 * kWorkers) * z.slot_rows, parts = 2 * static_cast<size_t>(z.copies) * z.out_rows;
-  return kErrorBytes + up256(slots * d * sizeof(float)) + up256(slots * sizeof(float2)) + up256(parts * d * sizeof(float)) +
-         up256(parts * sizeof(float2)) + (static_cast<size_t>(B) + n_prefixes + 4) * sizeof(int32_t);
+  const size_t rows = static_cast<size_t>(2 * kWorkers) * z.slot_rows + 2 * static_cast<size_t>(z.copies) * z.out_rows;
+  return kErrorBytes + up256(rows * d * sizeof(float)) + up256(rows * sizeof(float2)) +
+         (static_cast<size_t>(B) + n_prefixes + 4) * sizeof(int32_t);
 }
 
 extern "C" stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
@@ -666,18 +680,15 @@ extern "C" stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix,
   p.out_rows = z.out_rows;
   p.copies = z.copies;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t slots = static_cast<size_t>(2 * kWorkers) * p.slot_rows, parts = 2 * static_cast<size_t>(z.copies) * z.out_rows;
+  p.parts = static_cast<int64_t>(2 * kWorkers) * p.slot_rows;
+  const size_t rows = p.parts + 2 * static_cast<size_t>(z.copies) * z.out_rows;
   p.word = reinterpret_cast<long long*>(ws);
   p.status = reinterpret_cast<int*>(ws + 256);
   ws += kErrorBytes;
   p.slots = reinterpret_cast<float*>(ws);
-  ws += up256(slots * d * sizeof(float));
+  ws += up256(rows * d * sizeof(float));
   p.stats = reinterpret_cast<float2*>(ws);
-  ws += up256(slots * sizeof(float2));
-  p.part_o = reinterpret_cast<float*>(ws);
-  ws += up256(parts * d * sizeof(float));
-  p.part_stats = reinterpret_cast<float2*>(ws);
-  ws += up256(parts * sizeof(float2));
+  ws += up256(rows * sizeof(float2));
   p.line = reinterpret_cast<int32_t*>(ws);
   p.pline = p.line + B;
   p.meta = p.pline + n_prefixes;

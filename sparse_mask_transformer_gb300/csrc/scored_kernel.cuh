@@ -528,14 +528,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < BN / 32; ++x) tmem_st16(tP + lane_off + 16 * x, zero);
       tmem_st_wait();
     }
+    // kTwoPlaces: the next segment and what its rows load, asked for before the
+    // end of the one before, whose wait and stores hide the loads
+    Segment<typename SRC::Item> ahead{};
+    typename SRC::Loads loads;
+    Next got = Next::none;
+    auto look_ahead = [&](int handed) {
+      got = read_ring(handed, ahead);
+      if constexpr (SRC::kTwoPlaces)
+        if (got == Next::segment) SRC::load_row(p, loads, ahead, r % ROWS);
+    };
+    if constexpr (SRC::kTwoPlaces) look_ahead(0);
 #pragma unroll 1
     for (int handed = 0;; ++handed) {
-      const Next got = read_ring(handed, seg);
+      if constexpr (SRC::kTwoPlaces)
+        seg = ahead;
+      else
+        got = read_ring(handed, seg);
       if (got != Next::segment) {
         ok = got == Next::none;
         break;
       }
-      const bool live = SRC::begin_row(p, row, seg, r % ROWS);   // the row is one of the call's
+      const bool live = SRC::begin_row(p, row, loads, seg, r % ROWS);   // the row is one of the call's
       const bool alive = __any_sync(0xffffffffu, live);   // the warp has such a row
       float slope = 0.f;
       uint32_t base = 0;  // the row's reference distance
@@ -662,6 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&w.p_full);
       }
       // ---- the segment's end
+      if constexpr (SRC::kTwoPlaces)
+        if (ok) look_ahead(handed + 1);
       if (!ok || (seg.n > 0 && !warp_wait(&w.pv_done, (j - 1) & 1, abort_flag))) {
         ok = false;
         break;
