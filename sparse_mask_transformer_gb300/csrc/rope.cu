@@ -241,7 +241,10 @@ cudaError_t launch(PARAMS& p, long long tokens, cudaStream_t s) {
   // are resident (an angle is then computed for as many heads as can be), up
   // to a thread per head when there are few tokens.  16384 tokens, 40 heads of
   // 128: 1 slot 71.6 us, 2 slots 67.5, 4 slots 69.8, 8 slots 73.8.
-  const long long want = 870ll * device_sm_count();
+  // Accesses of 8 bytes want four times as many threads: 16384 tokens, 48 heads
+  // of 80, half of each turned, 2 slots 102 us, 8 slots 60; of 72, all turned, 2
+  // slots 49.2, 4 slots 51.4.
+  const long long want = (E == 4 ? 4 : 1) * 870ll * device_sm_count();
   long long slots = (want + tokens * units - 1) / (tokens * units);
   if (slots > heads) slots = heads;
   // as many heads for every slot where a number up to twice as large divides them (3 slots for 32 heads: 41.5 us, 4: 36.2)
@@ -250,6 +253,13 @@ cudaError_t launch(PARAMS& p, long long tokens, cudaStream_t s) {
       slots = more;
       break;
     }
+  }
+  if (std::is_same<PARAMS, AxesParams>::value) {
+    // no second round of a few blocks behind the first (608 are resident): 9805
+    // tokens of 32 heads of 64, 4 slots on 613 blocks 28.0 us, 3 slots 25.3; 16384
+    // of 32 heads of 80, 2 slots on 640 blocks 55.3, one 53.5, 3 slots 48.8
+    const long long fit = static_cast<long long>(kThreadsRope) * kBlocksRope * device_sm_count(), n = tokens * units * slots;
+    if (n > fit && n < fit + fit / 16) slots += slots > 2 ? -1 : (slots < heads ? 1 : 0);
   }
   p.slots = static_cast<int>(slots);
   p.n_threads = static_cast<uint32_t>(tokens * units * slots);
