@@ -34,6 +34,7 @@ struct PrefixParams : TreeParams {
   int per_request;                  // row tiles of a request there (nb = 1)
   int fill, own_fill;               // rows of a tile: of a prefix's, of a request's
   int prow_tiles, prow_group, prow_groups;  // as row_tiles, ..., of a prefix
+  float per_row_group, per_prow_group;      // 1 / row_group, 1 / prow_group
   const int32_t* plens;
   int32_t* pline;                   // [NP], as line [B]: places of the items on their lines
   int32_t* meta;                    // [4] first worker of the requests' line; share lengths of the prefixes' line, of the requests'
@@ -66,27 +67,24 @@ __device__ __forceinline__ int prefix_run(const PrefixParams& p, int plen) {
 __device__ __forceinline__ int request_run(const PrefixParams& p, const Lengths& x) {
   return p.lens && prefix_ok(p, x.plen) && request_ok(p, x.ctx, x.count) ? tiles_of(p, x.ctx + x.count) + kItemCost : 0;
 }
-// a / b of small numbers (a < 2^15)
-__device__ __forceinline__ int small_div(int a, int b) { return __float2int_rd(__fdividef(a + 0.5f, static_cast<float>(b))); }
+// a / b of small numbers (a < 2^15), per_b = 1 / b
+__device__ __forceinline__ int small_div(int a, float per_b) { return __float2int_rd((a + 0.5f) * per_b); }
 __device__ __forceinline__ int share_length(int all, int shares) { return max(1, (all + shares - 1) / max(1, shares)); }
 
 // Shares of the two lines, of lengths lp and lo: as many workers for each as
 // bring the later end forward.
 __device__ __forceinline__ void divide(const PrefixParams& p, int lp, int lo, int& sp, int& so) {
-  const float wp = static_cast<float>(lp) * p.prow_group, wo = static_cast<float>(lo) * p.row_group;
-  const int most = small_div(kWorkers - (lo > 0 ? p.row_group : 0), p.prow_group);
-  int x = lp == 0 ? 0 : most;
-  if (lp > 0 && lo > 0) x = max(1, min(most, small_div(static_cast<int>(kWorkers * __fdividef(wp, wp + wo)), p.prow_group)));
-  int y = small_div(kWorkers - x * p.prow_group, p.row_group);
-  if (lp > 0 && lo > 0 && x < most) {  // one share more?
-    const int y1 = small_div(kWorkers - (x + 1) * p.prow_group, p.row_group);
-    if (fmaxf(__fdividef(lp, x + 1), __fdividef(lo, y1)) < fmaxf(__fdividef(lp, x), __fdividef(lo, y))) {
-      ++x;
-      y = y1;
-    }
+  sp = lp > 0 ? small_div(kWorkers, p.per_prow_group) : 0;
+  if (lp > 0 && lo > 0) {
+    const float wp = static_cast<float>(lp) * p.prow_group, wo = static_cast<float>(lo) * p.row_group;
+    const int most = small_div(kWorkers - p.row_group, p.per_prow_group);
+    sp = max(1, min(most, small_div(static_cast<int>(kWorkers * __fdividef(wp, wp + wo)), p.per_prow_group)));
+    // one share more?
+    const int y = small_div(kWorkers - sp * p.prow_group, p.per_row_group);
+    const int y1 = small_div(kWorkers - (sp + 1) * p.prow_group, p.per_row_group);
+    if (sp < most && fmaxf(__fdividef(lp, sp + 1), __fdividef(lo, y1)) < fmaxf(__fdividef(lp, sp), __fdividef(lo, y))) ++sp;
   }
-  sp = x;
-  so = y;
+  so = small_div(kWorkers - sp * p.prow_group, p.per_row_group);
 }
 
 struct PrefixSource : CacheSource {
@@ -102,6 +100,7 @@ struct PrefixSource : CacheSource {
     int row[2];            // their row tiles within a group
     int begin[2], end[2];  // and shares
     int i[2], base[2];     // the prefix or request that holds a share's begin, its place on the line
+    Lengths lengths[2];    // its rows (of a prefix: plen)
     int bad;               // CTA 0: a length breaks the bounds
   };
   struct Loads {
@@ -117,21 +116,29 @@ struct PrefixSource : CacheSource {
 
   static __device__ void init(Shared& s) { s.bad = 0; }
 
-  // Lengths of prefix i's and request i's runs on their lines; CTA 0 reports
-  // lengths out of range.
-  static __device__ int2 item_lengths(const Params& p, Shared& s, int i, bool report) {
-    const int plen = i < p.NP ? __ldg(p.plens + i) : 0;
-    Lengths x{0, 0, 0};
-    if (i < p.B) x = lengths_of(p, i);
-    if (report && blockIdx.x == 0) {
-      const bool none = x.count == 0 && x.ctx >= 0 && (!p.lens || x.ctx <= p.cap);  // a request without tokens
-      if (!prefix_ok(p, plen) || (i < p.B && !request_ok(p, x.ctx, x.count) && !none)) {
-        s.bad = 1;
-        if (p.err) raise_error(p.err, STOF_DEVERR_BAD_LENGTH);
-      }
+  // What a thread has of both lines: prefix i's rows, request i's lengths.
+  struct Mine {
+    int plen;
+    Lengths x;
+  };
+  static __device__ Mine load_items(const Params& p, int i) {
+    Mine m{0, Lengths{0, 0, 0}};
+    if (i < p.NP) m.plen = __ldg(p.plens + i);
+    if (i < p.B) m.x = lengths_of(p, i);
+    return m;
+  }
+  // Lengths of their runs on the lines.
+  static __device__ int2 item_lengths(const Params& p, const Mine& m, int i) {
+    return make_int2(i < p.NP ? prefix_run(p, m.plen) * p.Hkv * p.prow_groups : 0,
+                     i < p.B ? request_run(p, m.x) * p.Hkv * p.row_groups : 0);
+  }
+  // Reports lengths out of range.
+  static __device__ void report(const Params& p, Shared& s, const Mine& m, int i) {
+    const bool none = m.x.count == 0 && m.x.ctx >= 0 && (!p.lens || m.x.ctx <= p.cap);  // a request without tokens
+    if (!prefix_ok(p, m.plen) || (i < p.B && !request_ok(p, m.x.ctx, m.x.count) && !none)) {
+      s.bad = 1;
+      if (p.err) raise_error(p.err, STOF_DEVERR_BAD_LENGTH);
     }
-    return make_int2(i < p.NP ? prefix_run(p, plen) * p.Hkv * p.prow_groups : 0,
-                     i < p.B ? request_run(p, x) * p.Hkv * p.row_groups : 0);
   }
   // Exclusive prefixes of v over the block's threads, and the totals.
   static __device__ int2 both_prefixes(int2 v, int2* sums, int2& total) {
@@ -158,15 +165,22 @@ struct PrefixSource : CacheSource {
     return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
   }
   // Both lines at once: a thread has prefix i and request i.
-  static __device__ void prologue(const Params& p, Shared& s) {
+  template <class MEANWHILE>
+  static __device__ void prologue(const Params& p, Shared& s, MEANWHILE meanwhile) {
     dependents_launch();  // merge_kernel may be set up
     const int items = max(p.NP, p.B);
+    Mine m = load_items(p, threadIdx.x);
+    meanwhile();
     int2 v, at, all = make_int2(0, 0);
 #pragma unroll 1
     for (int i0 = 0; i0 < items; i0 += kThreads) {
       const int i = i0 + static_cast<int>(threadIdx.x);
-      v = item_lengths(p, s, i, true);
-      if (i0) __syncthreads();  // the sums have been read
+      if (i0) {
+        m = load_items(p, i);
+        __syncthreads();  // the sums have been read
+      }
+      v = item_lengths(p, m, i);
+      if (blockIdx.x == 0) report(p, s, m, i);
       int2 total;
       at = both_prefixes(v, s.sums, total);
       at = make_int2(all.x + at.x, all.y + at.y);
@@ -191,7 +205,8 @@ struct PrefixSource : CacheSource {
     for (int g = 0; g < 2; ++g) {
       const int w = worker(g);
       mine[g] = w < first_own;
-      const int in = mine[g] ? w : w - first_own, group = mine[g] ? p.prow_group : p.row_group, nth = small_div(in, group);
+      const int in = mine[g] ? w : w - first_own, group = mine[g] ? p.prow_group : p.row_group;
+      const int nth = small_div(in, mine[g] ? p.per_prow_group : p.per_row_group);
       const int line = mine[g] ? all.x : all.y, len = mine[g] ? length[0] : length[1];
       begin[g] = nth < (mine[g] ? shares[0] : shares[1]) ? min(nth * len, line) : line;
       if (threadIdx.x == 0) {
@@ -205,7 +220,8 @@ struct PrefixSource : CacheSource {
 #pragma unroll 1
     for (int i0 = 0; i0 < items; i0 += kThreads) {
       if (items > kThreads) {  // else v and at are those of the one round above
-        v = item_lengths(p, s, i0 + threadIdx.x, false);
+        m = load_items(p, i0 + threadIdx.x);
+        v = item_lengths(p, m, i0 + threadIdx.x);
         __syncthreads();
         int2 total;
         at = both_prefixes(v, s.sums, total);
@@ -218,6 +234,7 @@ struct PrefixSource : CacheSource {
         if (from <= begin[g] && begin[g] < to) {
           s.i[g] = i0 + threadIdx.x;
           s.base[g] = from;
+          s.lengths[g] = mine[g] ? Lengths{m.plen, 0, 0} : m.x;
         }
       }
     }
@@ -240,20 +257,14 @@ struct PrefixSource : CacheSource {
       if (w < end) {
         i = s.i[g];
         base = s.base[g];
-        load(p);
+        take(p, s.lengths[g]);
       }
     }
-    __device__ void load(const Params& p) {
-      if (prefix) {
-        ctx = __ldg(p.plens + i);
-        len = prefix_run(p, ctx);
-      } else {
-        const Lengths x = lengths_of(p, i);
-        plen = x.plen;
-        ctx = x.ctx;
-        count = x.count;
-        len = request_run(p, x);
-      }
+    __device__ void take(const Params& p, const Lengths& x) {
+      plen = prefix ? 0 : x.plen;
+      ctx = prefix ? x.plen : x.ctx;
+      count = x.count;
+      len = prefix ? prefix_run(p, x.plen) : request_run(p, x);
     }
     __device__ Next next(const Params& p, Shared&, const volatile int*, Segment<Item>& seg) {
       const int row_tiles = prefix ? p.prow_tiles : p.row_tiles, row_group = prefix ? p.prow_group : p.row_group;
@@ -264,16 +275,16 @@ struct PrefixSource : CacheSource {
         while (w >= base + len * per) {  // on to the next item on the line
           base += len * per;
           ++i;
-          load(p);
+          take(p, prefix ? Lengths{__ldg(p.plens + i), 0, 0} : lengths_of(p, i));
         }
         const int off = w - base, item = off / len, at = off - item * len;
         const int to = min(end - base - item * len, len);  // the share's part of the run: [at, to)
         w += to - at;
         const int t0 = max(0, at - kItemCost), t1 = max(0, to - kItemCost);
-        const int hk = item / row_groups, rt = (item - hk * row_groups) * row_group + row;
+        const int hk = row_groups == 1 ? item : item / row_groups, rt = (item - hk * row_groups) * row_group + row;
         if (t1 <= t0 || rt >= row_tiles) continue;
         if (prefix) {
-          const int x = rt / p.per_request;
+          const int x = p.per_request == 1 ? rt : rt / p.per_request;
           seg.q_plane = i * p.n + (p.nb > 1 ? rt * p.nb : x);
           seg.q_row = p.nb > 1 ? 0 : (rt - x * p.per_request) * 128;
         } else {
@@ -664,6 +675,8 @@ extern "C" stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix,
   p.prow_tiles = static_cast<int>(prow_tiles);
   p.prow_groups = static_cast<int>((prow_tiles + kRowGroup - 1) / kRowGroup);
   p.prow_group = (p.prow_tiles + p.prow_groups - 1) / p.prow_groups;
+  p.per_row_group = 1.f / static_cast<float>(p.row_group);
+  p.per_prow_group = 1.f / static_cast<float>(p.prow_group);
   p.slot_rows = static_cast<int>(z.slot_rows);
   p.lens = lens;
   p.counts = counts;

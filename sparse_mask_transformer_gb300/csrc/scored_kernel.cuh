@@ -306,14 +306,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if constexpr (SRC::kTwoPlaces) {
     dependents_wait();  // launched while the stream's last kernel may still run
-    // Q's rows that no copy fills: what they hold would choose the way that
-    // whole warps take, and with it the other rows' roundings
-    if (p.fill * REP < kBM || p.own_fill * REP < kBM) {
-      for (int i = threadIdx.x; i < 2 * kBM * D / 8; i += kThreads) reinterpret_cast<uint4*>(s.q)[i] = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-    }
+    // all threads; may use __syncthreads.  While its first loads are on their
+    // way: Q's rows that no copy fills become 0, since what they hold would
+    // choose the way that whole warps take, and with it the other rows' roundings
+    SRC::prologue(p, s.src, [&]() {
+      if (p.fill * REP < kBM || p.own_fill * REP < kBM) {
+        for (int i = threadIdx.x; i < 2 * kBM * D / 8; i += kThreads) reinterpret_cast<uint4*>(s.q)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+    });
+  } else {
+    SRC::prologue(p, s.src);  // all threads; may use __syncthreads
   }
-  SRC::prologue(p, s.src);  // all threads; may use __syncthreads
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
