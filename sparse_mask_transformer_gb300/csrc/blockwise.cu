@@ -461,8 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // swizzle; a box that runs past row L of its head reads zeros there.
 // A tensor map holds only the address, sizes, strides and box of a tensor,
 // so a map made once stays right for every later call with the same key;
-// the cache (round-robin over kMapCache entries) spares the driver call that
-// otherwise dominates a short launch's host time.
+// the cache (kMapSets sets of kMapWays entries, round-robin within a set) spares
+// the driver call that otherwise dominates a short launch's host time, and has
+// room for the caches of all layers of a decoder (up to seven maps a call).
 namespace {
 struct MapKey {
   int dev;
@@ -480,18 +481,28 @@ struct MapEntry {
   MapKey key;
   bool used;
 };
-constexpr int kMapCache = 64;
+constexpr int kMapSets = 256, kMapWays = 4;
+struct MapSet {
+  MapEntry entry[kMapWays];
+  int next;
+};
 std::mutex g_map_mu;
-MapEntry g_maps[kMapCache];
-int g_map_next = 0;
-}  // namespace
+MapSet g_maps[kMapSets];
 
-namespace {
+MapSet& set_of(const MapKey& k) {
+  uint64_t h = reinterpret_cast<uintptr_t>(k.base) >> 4;
+  for (const uint64_t x : {static_cast<uint64_t>(k.dev), k.outer, k.heads, k.L, static_cast<uint64_t>(k.D),
+                           static_cast<uint64_t>(k.box_rows), static_cast<uint64_t>(k.box_outer)})
+    h = (h ^ x) * 0x9E3779B97F4A7C15ull;  // 2^64 / golden ratio: the products' high bits mix all of it
+  return g_maps[h >> 56];
+}
+
 bool cached_map(CUtensorMap* m, MapKey key) {
   if (cudaGetDevice(&key.dev) != cudaSuccess) key.dev = -1;
+  MapSet& set = set_of(key);
   {
     std::lock_guard<std::mutex> lock(g_map_mu);
-    for (const MapEntry& e : g_maps)
+    for (const MapEntry& e : set.entry)
       if (e.used && e.key == key) {
         *m = e.map;
         return true;
@@ -507,8 +518,8 @@ bool cached_map(CUtensorMap* m, MapKey key) {
                                        static_cast<uint32_t>(key.box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
   if (!made) return false;
   std::lock_guard<std::mutex> lock(g_map_mu);
-  MapEntry& e = g_maps[g_map_next];
-  g_map_next = (g_map_next + 1) % kMapCache;
+  MapEntry& e = set.entry[set.next];
+  set.next = (set.next + 1) % kMapWays;
   e.map = *m;
   e.key = key;
   e.used = true;

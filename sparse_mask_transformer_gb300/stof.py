@@ -510,22 +510,23 @@ def stof_prefix_attn_fwd(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torc
     slopes = score.slopes if score is not None else None
     device = _device_of(where, q, k_prefix, v_prefix, prefix_lens, k, v, lens, o, workspace, tree, counts, positions, slopes,
                         device_error)
-    if len(q.shape) != 4 or len(k_prefix.shape) != 4:
+    qs, ps, dt = q.shape, k_prefix.shape, q.dtype
+    if len(qs) != 4 or len(ps) != 4:
         raise StofError(STOF_ERR_SHAPE, f"{where}: q [B, H, T, d] and k_prefix [P, Hkv, rows, d]")
-    B, H, T, d = q.shape
-    n, Hkv, prefix_cap, pd = k_prefix.shape
-    if (pd != d or v_prefix.shape != k_prefix.shape or o.shape != q.shape or k_prefix.dtype != q.dtype
-            or v_prefix.dtype != q.dtype or o.dtype != q.dtype
+    B, H, T, d = qs
+    n, Hkv, prefix_cap, pd = ps
+    if (pd != d or v_prefix.shape != ps or o.shape != qs or k_prefix.dtype != dt or v_prefix.dtype != dt or o.dtype != dt
             or not (q.is_contiguous() and k_prefix.is_contiguous() and v_prefix.is_contiguous() and o.is_contiguous())):
         raise StofError(STOF_ERR_SHAPE, f"{where}: q, o [B, H, T, d] and k_prefix, v_prefix [P, Hkv, rows, d], contiguous, one dtype")
     cap, k_ptr, v_ptr = 0, None, None
     if k is not None or v is not None or lens is not None:
         if k is None or v is None or lens is None:
             raise StofError(STOF_ERR_INVALID_ARG, f"{where}: own caches are k, v and lens, or none of them")
-        _, _, _, _, own_heads, cap = _heads_of(where, q, k, v, o)
-        if own_heads != Hkv:
-            raise StofError(STOF_ERR_SHAPE, f"{where}: k and k_prefix must have the same heads")
-        k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
+        own = k.shape
+        if (len(own) != 4 or own[0] != B or own[1] != Hkv or own[3] != d or v.shape != own or k.dtype != dt or v.dtype != dt
+                or not (k.is_contiguous() and v.is_contiguous())):
+            raise StofError(STOF_ERR_SHAPE, f"{where}: k, v [B, Hkv, rows, d], contiguous, of q's dtype")
+        cap, k_ptr, v_ptr = own[2], k.data_ptr(), v.data_ptr()
     _launch(where, device, stream, load_library().stof_prefix_attn_fwd, q.data_ptr(), k_prefix.data_ptr(),
             v_prefix.data_ptr(), k_ptr, v_ptr, _dtype_code(q), B, n, H, Hkv, T, d, prefix_cap, cap,
             _int32(where, "prefix_lens", prefix_lens, (n,)), None if lens is None else _int32(where, "lens", lens, (B,)),
@@ -890,6 +891,8 @@ class Caches:
             raise StofError(STOF_ERR_SHAPE, "Caches: tensors must be contiguous [slots, heads, rows, d] of one shape and type")
         if max(shape) > INT32_MAX:  # (ctypes would keep the low 32 bits)
             raise StofError(STOF_ERR_SHAPE, "Caches: sizes must be below 2^31")
+        if len({t.data_ptr() for t in self.tensors}) != len(self.tensors):
+            raise StofError(STOF_ERR_INVALID_ARG, "Caches: a tensor is given twice")
         self.slots, self.heads, self.rows, self.d = shape
         self.dtype = dtype
         self._data = (ctypes.c_void_p * len(self.tensors))(*(t.data_ptr() for t in self.tensors))

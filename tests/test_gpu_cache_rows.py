@@ -228,6 +228,9 @@ def test_caches_of_different_shapes_are_refused(gpu_lib):
         assert e.value.status == stof.STOF_ERR_SHAPE
     with pytest.raises(stof.StofError):
         stof.Caches([x.float()])
+    with pytest.raises(stof.StofError) as e:
+        stof.Caches([x, x])
+    assert e.value.status == stof.STOF_ERR_INVALID_ARG
     c = stof.Caches([x])
     with pytest.raises(stof.StofError) as e:
         stof.stof_cache_keep(c, i32([0, 0, 0]), i32([[0], [0]]), i32([0, 0]))
