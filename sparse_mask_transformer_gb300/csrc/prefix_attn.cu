@@ -53,7 +53,9 @@ struct PrefixParams : TreeParams {
   float per_row_group, per_prow_group;      // 1 / row_group, 1 / prow_group
   const int32_t* plens;
   int32_t* pline;                   // [NP], as line [B]: places of the items on their lines
-  int32_t* meta;                    // [4] first worker of the requests' line; share lengths of the prefixes' line, of the requests'
+  // [kTreeCtas] first worker of the requests' line; share lengths of the prefixes' line, of the requests'; -.  Every
+  // CTA leaves them: the warps of merge_kernel, each of which reads them first, would wait 1 to 3 us for one place
+  int4* meta;
   // behind the workers' slots: [2][copies][B H T] parts of runs that lie in one share, of prefixes and of requests
   int64_t parts;                    // their first row
   int64_t out_rows;                 // B H T
@@ -210,11 +212,7 @@ struct PrefixSource : CacheSource {
     divide(p, all.x, all.y, shares[0], shares[1]);
     const int first_own = shares[0] * p.prow_group;  // workers before it are the prefixes'
     const int length[2] = {share_length(all.x, shares[0]), share_length(all.y, shares[1])};
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.meta[0] = first_own;
-      p.meta[1] = length[0];
-      p.meta[2] = length[1];
-    }
+    if (threadIdx.x == 0) p.meta[blockIdx.x] = make_int4(first_own, length[0], length[1], 0);
     bool mine[2];
     int begin[2];
 #pragma unroll
@@ -457,8 +455,9 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
   const int pr = p.nb > 1 ? (in - prt * p.nb) * p.rows + rr : rr % 128;
   const int lens[2] = {prefix_run(p, x.plen), request_run(p, x)};
   dependents_wait();
-  const int first_own = __ldcg(p.meta), share[2] = {__ldcg(p.meta + 1), __ldcg(p.meta + 2)};
-  const int place0[2] = {__ldcg(p.pline + np), __ldcg(p.line + b)};
+  const int4 meta = __ldcg(p.meta + blockIdx.x % kTreeCtas);
+  const int first_own = meta.x, share[2] = {meta.y, meta.z};
+  const int place0[2] = {np ? __ldcg(p.pline + np) : 0, b ? __ldcg(p.line + b) : 0};  // the first items' places are 0
   // A run's parts, and where they are: the first, the others, from one to the
   // next, from copy to copy.  A whole run's is by the row; else the first
   // share's part is its worker's last segment, the others' their first.
@@ -623,7 +622,7 @@ extern "C" size_t stof_prefix_attn_workspace_bytes(int B, int n_prefixes, int H,
   if (!sizes_of(B, n_prefixes, H, Hkv, T, d, &z) || z.out_rows >= (1ll << 31)) return 0;
   const size_t rows = static_cast<size_t>(2 * kWorkers) * z.slot_rows + 2 * static_cast<size_t>(z.copies) * z.out_rows;
   return kErrorBytes + up256(rows * d * sizeof(float)) + up256(rows * sizeof(float2)) +
-         (static_cast<size_t>(B) + n_prefixes + 4) * sizeof(int32_t);
+         kTreeCtas * sizeof(int4) + (static_cast<size_t>(B) + n_prefixes) * sizeof(int32_t);
 }
 
 extern "C" stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
@@ -718,9 +717,9 @@ extern "C" stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix,
   ws += up256(rows * d * sizeof(float));
   p.stats = reinterpret_cast<float2*>(ws);
   ws += up256(rows * sizeof(float2));
-  p.line = reinterpret_cast<int32_t*>(ws);
+  p.meta = reinterpret_cast<int4*>(ws);
+  p.line = reinterpret_cast<int32_t*>(p.meta + kTreeCtas);
   p.pline = p.line + B;
-  p.meta = p.pline + n_prefixes;
   const int mode = mode_of(scale, softcap, p.slopes != nullptr);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dt == STOF_BF16;
