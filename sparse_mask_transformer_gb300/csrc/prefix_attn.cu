@@ -419,11 +419,6 @@ struct PrefixSource : CacheSource {
   }
 };
 
-__device__ __forceinline__ void add_part(float4& o, float& l, float w, const float4& y, float sum) {
-  l = fmaf(w, sum, l);
-  o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
-}
-
 // Merges the parts of the rows, those of the prefix first.  WPR warps per row;
 // a part takes D / 4 lanes, four columns each, so that a warp takes one (d =
 // 128) or two (d = 64) parts at a time, kBatch times that in flight.  Four rows
@@ -455,9 +450,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
   const int pr = p.nb > 1 ? (in - prt * p.nb) * p.rows + rr : rr % 128;
   const int lens[2] = {prefix_run(p, x.plen), request_run(p, x)};
   dependents_wait();
-  const int4 meta = __ldcg(p.meta + blockIdx.x % kTreeCtas);
+  // (through the L1 cache, which nothing has filled with these: an SM's warps read few different ones)
+  const int4 meta = p.meta[blockIdx.x % kTreeCtas];
   const int first_own = meta.x, share[2] = {meta.y, meta.z};
-  const int place0[2] = {np ? __ldcg(p.pline + np) : 0, b ? __ldcg(p.line + b) : 0};  // the first items' places are 0
+  const int place0[2] = {np ? p.pline[np] : 0, b ? p.line[b] : 0};  // the first items' places are 0
   // A run's parts, and where they are: the first, the others, from one to the
   // next, from copy to copy.  A whole run's is by the row; else the first
   // share's part is its worker's last segment, the others' their first.
@@ -486,40 +482,50 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
     i -= pre.n;
     return (i ? own.rest + i * own.step : own.first) + copy * own.copy;
   };
+  // A round takes up to 32 parts of the warp: lane i has the place, the weight
+  // and the sum of part i, and all lanes add the parts' columns.
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int i0 = part * kAtOnce + lane / kLanes; i0 < parts; i0 += WPR * kAtOnce * kBatch) {
-    float2 st[kBatch];
-    float4 y[kBatch];
+  for (int k0 = part; k0 < parts; k0 += 32 * WPR) {
+    const int k = k0 + lane * WPR, n = min(32, (parts - k0 + WPR - 1) / WPR);
+    int64_t at = 0;
+    float2 st = make_float2(-INFINITY, 0.f);
+    if (k < parts) {
+      at = place(k);
+      st = __ldcg(p.stats + at);
+    }
+    float w = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kBatch * kAtOnce) {
+      float4 y[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int k = i0 + i * WPR * kAtOnce;
-      st[i] = make_float2(-INFINITY, 0.f);
-      y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k < parts) {
-        const int64_t at = place(k);
-        st[i] = __ldcg(p.stats + at);
-        y[i] = __ldcg(reinterpret_cast<const float4*>(p.slots) + at * kLanes + lane % kLanes);
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = i0 + i * kAtOnce + lane / kLanes;
+        const int64_t row = __shfl_sync(0xffffffffu, at, j & 31);
+        y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < n) y[i] = __ldcg(reinterpret_cast<const float4*>(p.slots) + row * kLanes + lane % kLanes);
+      }
+      if (i0 == 0) {  // the first columns are on their way
+        float mn = fmaxf(m, st.x);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+        const float ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref);
+        w = ex2(st.x - ref);
+        l = fmaf(w, st.y, l * a);
+        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+        m = mn;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float x = __shfl_sync(0xffffffffu, w, (i0 + i * kAtOnce + lane / kLanes) & 31);
+        o = make_float4(fmaf(x, y[i].x, o.x), fmaf(x, y[i].y, o.y), fmaf(x, y[i].z, o.z), fmaf(x, y[i].w, o.w));
       }
     }
-    float mn = m;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, st[i].x);
-    const float ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref);
-    l *= a;
-    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) add_part(o, l, ex2(st[i].x - ref), y[i], st[i].y);
-    m = mn;
   }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   if constexpr (kAtOnce == 2) {  // the two halves of the warp
-    const float other = __shfl_xor_sync(0xffffffffu, m, 16), mn = fmaxf(m, other), ref = mn == -INFINITY ? 0.f : mn;
-    const float a = ex2(m - ref);
-    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
-    l *= a;
-    m = mn;
-    l += __shfl_xor_sync(0xffffffffu, l, 16);
     o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
     o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
     o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
@@ -538,7 +544,12 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) add_part(o, l, ex2(s_m[w] - ref), s_o[w][lane % kLanes], s_l[w]);
+    for (int w = 0; w < 4; ++w) {
+      const float a = ex2(s_m[w] - ref);
+      const float4 y = s_o[w][lane % kLanes];
+      l = fmaf(a, s_l[w], l);
+      o = make_float4(fmaf(a, y.x, o.x), fmaf(a, y.y, o.y), fmaf(a, y.z, o.z), fmaf(a, y.w, o.w));
+    }
   }
   if (lane >= kLanes) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
