@@ -591,10 +591,10 @@ stof_status launch_prefix(const void* q, const void* kp, const void* vp, const v
   if (st != STOF_OK) return st;
   // A row is merged by one warp where the rows are many for their parts (of
   // which the host knows the most that a prefix's run may have), else by four.
-  // One and four, the whole call: d = 128, 128 rows 20.8 and 16.6 us, 512 rows
-  // of 39 parts 34.0 and 28.9, 1024 41.0 and 37.4, 1536 of 20 45.2 and 45.5, 4096
-  // of 5 54.0 and 73.2; d = 64, 256 rows of 39 22.4 and 18.6, 512 18.5 and 18.6, 1024
-  // 20.1 and 22.5.
+  // One and four, the whole call: d = 128, 64 rows 26.9 and 22.6 us, 512 rows of
+  // 39 parts 28.9 and 24.6, 1024 35.1 and 31.3, 1536 of 20 40.5 and 41.0, 4096 of
+  // 5 49.3 and 66.7; d = 64, 256 rows of 39 20.4 and 16.5, 512 16.5 and 16.6, 1024
+  // 18.6 and 19.5.
   const int64_t runs = static_cast<int64_t>(p.NP) * p.Hkv * p.prow_tiles, parts = 1 + kWorkers / (runs < kWorkers ? runs : kWorkers);
   const bool one = p.out_rows >= (D == 128 ? 64 : 24) * parts;
   const unsigned grid = static_cast<unsigned>(one ? (p.out_rows + 3) / 4 : p.out_rows) + 1;

@@ -345,3 +345,40 @@ def test_the_most_drafted_tokens(gpu_lib):
     T = stof.STOF_TREE_MAX_TOKENS
     Case(1, 2, 1, T, 64, [100], [100], seed=29, counts=[T - 1]).run(planes={(0, 1)})
     Case(1, 1, 1, T, 128, [33], [0], seed=30, sees="chain").run()
+
+
+def test_calls_in_a_row_that_share_a_workspace(gpu_lib):
+    """Each call is set up while the one before it and the copies between them still run: what is written just before a
+    call is what it reads, and what is overwritten just after it is not."""
+    cs = [Case(3, 8, 2, 2, 64, [700, 90], [30, 0, 5, 200, 1, 64], seed=31),
+          Case(2, 16, 8, 1, 128, [1200], [100, 3], seed=32)]
+    size = max(stof.stof_prefix_attn_workspace_bytes(c.B, c.NP, c.H, c.Hkv, c.T, c.d) for c in cs)
+    ws = torch.full((size,), 0xCD, dtype=torch.uint8, device="cuda")
+    want, aa, kept = [], [], []
+    for c in cs:
+        a = c.args()
+        o = torch.full(c.q.shape, 5.0, dtype=c.dtype, device="cuda")
+        c.call(a, o)
+        c.check(o)
+        a["ws"] = ws
+        want.append(o)
+        aa.append(a)
+        kept.append({n: a[n].clone() for n in ("q", "kp", "vp", "k", "v")})
+    got = []
+    for i in range(24):
+        c, a, keep = cs[i % 2], aa[i % 2], kept[i % 2]
+        for n in ("q", "kp", "vp", "k", "v"):
+            a[n].copy_(keep[n])
+        got.append(torch.full(c.q.shape, 5.0, dtype=c.dtype, device="cuda"))
+        c.call(a, got[-1])
+        for n in ("q", "kp", "vp", "k", "v"):
+            a[n].fill_(float("nan"))
+        if i % 3 == 0:  # and straight after one another
+            for n in ("q", "kp", "vp", "k", "v"):
+                a[n].copy_(keep[n])
+            got.append(torch.full_like(got[-1], 5.0))
+            c.call(a, got[-1])
+            c.call(a, got[-1])
+    torch.cuda.synchronize()
+    for o in got:
+        assert torch.equal(o, want[0] if o.shape == want[0].shape else want[1])
