@@ -31,9 +31,9 @@
 //
 // Measured (a call among others; of the memory's copy rate, of the bf16 rate):
 // 64 requests with 100 to 1500 rows of their own behind one prefix of 16384, 32
-// heads of 128 on 8: 62.7 us, 67%, the main kernel 53 of them, the first tile's
-// arrival 4.5; 16 requests of up to 16 tokens behind 131072 rows 438 us, 57%; 4
-// beams of 24 sources, 16 heads of 64, 25.9 us, 47%.
+// heads of 128 on 8: 59.9 us, 70%, the main kernel 53 of them, the first tile's
+// arrival 4.2; 16 requests of up to 16 tokens behind 131072 rows 433 us, 58%; 4
+// beams of 24 sources, 16 heads of 64, 24.8 us, 49%.
 #include <cmath>
 
 #include "cache_source.cuh"
