@@ -382,3 +382,32 @@ def test_calls_in_a_row_that_share_a_workspace(gpu_lib):
     torch.cuda.synchronize()
     for o in got:
         assert torch.equal(o, want[0] if o.shape == want[0].shape else want[1])
+
+
+def random_case(seed):
+    rng = np.random.default_rng(seed)
+    pick = lambda *xs: xs[rng.integers(len(xs))]
+    Hkv = pick(1, 1, 2, 3)
+    H = Hkv * pick(1, 2, 3, 5, 8)
+    T = int(np.exp(rng.uniform(0, np.log(150))))
+    n = int(np.exp(rng.uniform(0, np.log(60))))
+    NP = int(np.exp(rng.uniform(0, np.log(12))))
+    while NP * n * H * T > 6000:                     # rows of the definition in 64 bits
+        n, NP = (n + 1) // 2, (NP + 1) // 2
+        T = max(1, T - T // 3)
+    cross = rng.random() < 0.25
+    most = int(np.exp(rng.uniform(0, np.log(1500))))
+    plens = rng.integers(0, most + 1, NP)
+    lens = None if cross else rng.integers(0, int(np.exp(rng.uniform(0, np.log(400)))) + 1, NP * n)
+    softcap = pick(0.0, 0.0, 25.0, 80.0)
+    slopes = None
+    if not cross and rng.random() < 0.4:
+        slopes = (np.array(head_slopes(H)) * pick(1.0, 1.0, -0.05)).tolist()
+    counts = rng.integers(0, T + 1, NP * n) if rng.random() < 0.5 else None
+    return Case(n, H, Hkv, T, pick(64, 128), plens, lens, pick(torch.float16, torch.bfloat16), counts=counts,
+                sees=pick("tree", "chain"), softcap=softcap, slopes=slopes, seed=seed, slack=int(rng.integers(0, 200)))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_cases(gpu_lib, seed):
+    random_case(seed).run()
