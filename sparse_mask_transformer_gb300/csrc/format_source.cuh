@@ -56,6 +56,10 @@ struct FormatSource {
     int done;                  // a request was refused: none follows
   };
   struct Loads {};
+  struct Lane {  // what a softmax thread knows of its row in every tile
+    int r;
+    __device__ Lane(const Params&, const Shared&, int, int row) : r(row) {}
+  };
   struct Row {
     int head;
     int pos;                 // the row's position among the keys
@@ -199,7 +203,8 @@ struct FormatSource {
     }
     return J * 128 + 64 * (t & two);
   }
-  static __device__ bool begin_row(const Params& p, Row& row, const Loads&, const Segment<Item>& seg, int r) {
+  static __device__ bool begin_row(const Params& p, Row& row, const Loads&, const Segment<Item>& seg, const Lane& lane) {
+    const int r = lane.r;
     row.head = seg.item.head;
     row.i = seg.q_row + r;
     row.pos = row.i + p.q_start;

@@ -323,29 +323,42 @@ struct PrefixSource : CacheSource {
     __device__ void drain(Shared&) {}
   };
 
-  // Request, head and token of row r of a segment's tile; whether the call has
-  // such a row, its lengths aside.
-  static __device__ bool place_row(const Params& p, const Segment<Item>& seg, int r, int& b, int& head, int& t) {
-    const Item& x = seg.item;
-    int rr = seg.q_row + r;
-    b = seg.q_plane;
-    bool is = true;
-    if (x.prefix && p.nb > 1) {
-      const int in = r / p.rows;
-      rr = r - in * p.rows;
-      b += in;
-      is = in < p.nb && b < (x.b + 1) * p.n;
+  // What a softmax thread knows of its row in every tile: a worker has tiles of
+  // one line only, and tiles that begin with a request's first row have the same
+  // requests, heads and tokens in the same rows.
+  struct Lane {
+    int r, in, head, t;  // the row; its request and head in the tile, its token
+    bool is;
+    __device__ Lane(const Params& p, const Shared& s, int g, int row) : r(row) {
+      in = s.prefix[g] && p.nb > 1 ? r / p.rows : 0;
+      const int rr = r - in * p.rows;
+      head = rr / p.T;
+      t = rr - head * p.T;
+      is = rr < p.rows && in < p.nb;
     }
-    const int gq = rr / p.T;
-    t = rr - gq * p.T;
-    head = x.hk * p.group + gq;
-    return is && rr < p.rows;
+  };
+  // Request, head and token of a segment's row; whether the call has such a
+  // row, its lengths aside.
+  static __device__ bool place_row(const Params& p, const Segment<Item>& seg, const Lane& lane, int& b, int& head, int& t) {
+    const Item& x = seg.item;
+    b = seg.q_plane + lane.in;
+    t = lane.t;
+    head = lane.head;
+    bool is = lane.is;
+    if (seg.q_row > 0) {  // a later tile of a request's rows
+      const int rr = seg.q_row + lane.r;
+      head = rr / p.T;
+      t = rr - head * p.T;
+      is = rr < p.rows;
+    }
+    head += x.hk * p.group;
+    return is && (!x.prefix || b < (x.b + 1) * p.n);
   }
   // What is loaded for a row, all of it at once.
-  static __device__ void load_row(const Params& p, Loads& y, const Segment<Item>& seg, int r) {
+  static __device__ void load_row(const Params& p, Loads& y, const Segment<Item>& seg, const Lane& lane) {
     const Item& x = seg.item;
     int b, head, t;
-    place_row(p, seg, r, b, head, t);
+    place_row(p, seg, lane, b, head, t);
     b = min(b, p.B - 1);
     const size_t token = static_cast<size_t>(b) * p.T + t;
     y.ctx = x.ctx;
@@ -360,9 +373,9 @@ struct PrefixSource : CacheSource {
     }
     if (p.slopes) y.slope = __ldg(p.slopes + min(head, p.H - 1));
   }
-  static __device__ bool begin_row(const Params& p, Row& row, const Loads& y, const Segment<Item>& seg, int r) {
+  static __device__ bool begin_row(const Params& p, Row& row, const Loads& y, const Segment<Item>& seg, const Lane& lane) {
     const Item& x = seg.item;
-    const bool live = place_row(p, seg, r, row.b, row.head, row.t) && request_ok(p, y.ctx, y.count) && row.t < y.count;
+    const bool live = place_row(p, seg, lane, row.b, row.head, row.t) && request_ok(p, y.ctx, y.count) && row.t < y.count;
     row.plen = live ? (x.prefix ? x.ctx : x.base) : 0;
     row.ctx = live ? y.ctx : 0;
     row.count = live ? y.count : 0;

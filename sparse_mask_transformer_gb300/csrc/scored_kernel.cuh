@@ -537,10 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segment<typename SRC::Item> ahead{};
     typename SRC::Loads loads;
     Next got = Next::none;
+    const typename SRC::Lane lane_of(p, s.src, g, r % ROWS);
     auto look_ahead = [&](int handed) {
       got = read_ring(handed, ahead);
       if constexpr (SRC::kTwoPlaces)
-        if (got == Next::segment) SRC::load_row(p, loads, ahead, r % ROWS);
+        if (got == Next::segment) SRC::load_row(p, loads, ahead, lane_of);
     };
     if constexpr (SRC::kTwoPlaces) look_ahead(0);
 #pragma unroll 1
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = got == Next::none;
         break;
       }
-      const bool live = SRC::begin_row(p, row, loads, seg, r % ROWS);   // the row is one of the call's
+      const bool live = SRC::begin_row(p, row, loads, seg, lane_of);   // the row is one of the call's
       const bool alive = __any_sync(0xffffffffu, live);   // the warp has such a row
       float slope = 0.f;
       uint32_t base = 0;  // the row's reference distance
