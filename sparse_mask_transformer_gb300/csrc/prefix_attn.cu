@@ -412,10 +412,8 @@ struct PrefixSource : CacheSource {
       lower_by_distance(sr, c, slope, row.pos, x.base + j0, base);
     }
   }
-  // The run is all that its rows see, and lies in one share and one copy.
-  static __device__ bool whole(const Params& p, const Item& x) {
-    return x.whole && p.copies == 1 && (x.prefix ? !p.lens : x.base == 0);
-  }
+  // The run is all that its rows see, and lies in one share (and the tile has one copy of its rows).
+  static __device__ bool whole(const Params& p, const Item& x) { return x.whole && (x.prefix ? !p.lens : x.base == 0); }
   // Parts of whole runs by the row of O; of others by the worker, as
   // CacheSource; those of the copies (r: the row of the tile) one after the other.
   static __device__ size_t slot_row(const Params& p, const Item& x, int g, int r) {
