@@ -130,6 +130,7 @@ struct PrefixSource : CacheSource {
     int b, plen, ctx, count;  // the row's request
     uint32_t self;            // the word of its tree row that has its own bit
     float given_slope;
+    bool listed;              // drafted keys' positions are read from the list (one value per warp)
   };
 
   static __device__ void init(Shared& s) { s.bad = 0; }
@@ -381,6 +382,8 @@ struct PrefixSource : CacheSource {
     row.count = live ? y.count : 0;
     row.self = p.positions && p.tree ? y.self : ~0u;
     row.given_slope = y.slope;
+    // one token at the place behind its request's rows needs no list
+    row.listed = p.positions && __any_sync(0xffffffffu, live && !(y.count == 1 && y.position == row.plen + row.ctx));
     row.pos = p.positions ? y.position : row.plen + row.ctx + row.t;
     row.out = (static_cast<size_t>(row.b) * p.H + row.head) * p.T + row.t;
     row.tree = live && p.tree ? p.tree + (static_cast<size_t>(row.b) * p.T + row.t) * p.words : nullptr;
@@ -400,7 +403,7 @@ struct PrefixSource : CacheSource {
   template <int BN, int CHUNKS>
   static __device__ void lower(const Params& p, const Row& row, const Item& x, int t, int j0, uint32_t (&sr)[CHUNKS][32],
                                float c, float slope, uint32_t base) {
-    if (p.positions && !x.prefix && partial(x, t)) {
+    if (row.listed && !x.prefix && partial(x, t)) {
       int at[CHUNKS];  // position of key 32 i + lane of the tile
 #pragma unroll
       for (int i = 0; i < CHUNKS; ++i) {
