@@ -91,6 +91,7 @@ struct CacheSource {
     int bad;               // CTA 0: a request breaks the bounds
   };
   struct Loads {};
+  template <bool>
   struct Lane {  // what a softmax thread knows of its row in every tile
     int r;
     __device__ Lane(const Params&, const Shared&, int, int row) : r(row) {}
@@ -204,7 +205,8 @@ struct CacheSource {
 
   static __device__ int tile_key(const Params&, const Item& x, int t) { return (x.t0 + t) * x.tile; }
   static __device__ int tile_end(const Item& x, int t) { return min(x.tile, x.ctx + x.count - (x.t0 + t) * x.tile); }
-  static __device__ bool begin_row(const Params& p, Row& row, const Loads&, const Segment<Item>& seg, const Lane& lane) {
+  template <bool KEEP>
+  static __device__ bool begin_row(const Params& p, Row& row, const Loads&, const Segment<Item>& seg, const Lane<KEEP>& lane) {
     const int r = lane.r;
     const Item& x = seg.item;
     const int rr = seg.q_row + r, gq = rr / p.T;

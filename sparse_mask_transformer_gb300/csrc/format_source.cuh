@@ -56,6 +56,7 @@ struct FormatSource {
     int done;                  // a request was refused: none follows
   };
   struct Loads {};
+  template <bool>
   struct Lane {  // what a softmax thread knows of its row in every tile
     int r;
     __device__ Lane(const Params&, const Shared&, int, int row) : r(row) {}
@@ -203,7 +204,8 @@ struct FormatSource {
     }
     return J * 128 + 64 * (t & two);
   }
-  static __device__ bool begin_row(const Params& p, Row& row, const Loads&, const Segment<Item>& seg, const Lane& lane) {
+  template <bool KEEP>
+  static __device__ bool begin_row(const Params& p, Row& row, const Loads&, const Segment<Item>& seg, const Lane<KEEP>& lane) {
     const int r = lane.r;
     row.head = seg.item.head;
     row.i = seg.q_row + r;

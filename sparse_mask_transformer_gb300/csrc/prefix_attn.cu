@@ -324,39 +324,51 @@ struct PrefixSource : CacheSource {
     __device__ void drain(Shared&) {}
   };
 
-  // What a softmax thread knows of its row in every tile: a worker has tiles of
-  // one line only, and tiles that begin with a request's first row have the same
-  // requests, heads and tokens in the same rows.
+  // A row's request and head in a tile that begins with a request's first row,
+  // and its token.
+  struct Place {
+    int in, head, t;
+    bool is;  // there is one
+  };
+  static __device__ Place place_in_tile(const Params& p, bool prefix, int r) {
+    const int in = prefix && p.nb > 1 ? r / p.rows : 0, rr = r - in * p.rows, head = rr / p.T;
+    return Place{in, head, rr - head * p.T, rr < p.rows && in < p.nb};
+  }
+  // What a softmax thread knows of its row r in every tile.  A worker has tiles
+  // of one line only, so where runs are short (KEEP: with copies) the place is
+  // found once: 8 prefixes of 16 requests, d = 64, 50.6 -> 48.9 us.  Kept where
+  // runs are long (d = 128, 131072 rows) it costs registers: 403 -> 428 us.
+  template <bool KEEP>
   struct Lane {
-    int r, in, head, t;  // the row; its request and head in the tile, its token
-    bool is;
-    __device__ Lane(const Params& p, const Shared& s, int g, int row) : r(row) {
-      in = s.prefix[g] && p.nb > 1 ? r / p.rows : 0;
-      const int rr = r - in * p.rows;
-      head = rr / p.T;
-      t = rr - head * p.T;
-      is = rr < p.rows && in < p.nb;
+    int r;
+    Place place;
+    __device__ Lane(const Params& p, const Shared& s, int g, int row) : r(row), place{} {
+      if (KEEP) place = place_in_tile(p, s.prefix[g], r);
     }
   };
   // Request, head and token of a segment's row; whether the call has such a
   // row, its lengths aside.
-  static __device__ bool place_row(const Params& p, const Segment<Item>& seg, const Lane& lane, int& b, int& head, int& t) {
+  template <bool KEEP>
+  static __device__ bool place_row(const Params& p, const Segment<Item>& seg, const Lane<KEEP>& lane, int& b, int& head, int& t) {
     const Item& x = seg.item;
-    b = seg.q_plane + lane.in;
-    t = lane.t;
-    head = lane.head;
-    bool is = lane.is;
+    Place y;
     if (seg.q_row > 0) {  // a later tile of a request's rows
       const int rr = seg.q_row + lane.r;
-      head = rr / p.T;
-      t = rr - head * p.T;
-      is = rr < p.rows;
+      y.in = 0;
+      y.head = rr / p.T;
+      y.t = rr - y.head * p.T;
+      y.is = rr < p.rows;
+    } else {
+      y = KEEP ? lane.place : place_in_tile(p, x.prefix, lane.r);
     }
-    head += x.hk * p.group;
-    return is && (!x.prefix || b < (x.b + 1) * p.n);
+    b = seg.q_plane + y.in;
+    head = x.hk * p.group + y.head;
+    t = y.t;
+    return y.is && (!x.prefix || b < (x.b + 1) * p.n);
   }
   // What is loaded for a row, all of it at once.
-  static __device__ void load_row(const Params& p, Loads& y, const Segment<Item>& seg, const Lane& lane) {
+  template <bool KEEP>
+  static __device__ void load_row(const Params& p, Loads& y, const Segment<Item>& seg, const Lane<KEEP>& lane) {
     const Item& x = seg.item;
     int b, head, t;
     place_row(p, seg, lane, b, head, t);
@@ -374,7 +386,8 @@ struct PrefixSource : CacheSource {
     }
     if (p.slopes) y.slope = __ldg(p.slopes + min(head, p.H - 1));
   }
-  static __device__ bool begin_row(const Params& p, Row& row, const Loads& y, const Segment<Item>& seg, const Lane& lane) {
+  template <bool KEEP>
+  static __device__ bool begin_row(const Params& p, Row& row, const Loads& y, const Segment<Item>& seg, const Lane<KEEP>& lane) {
     const Item& x = seg.item;
     const bool live = place_row(p, seg, lane, row.b, row.head, row.t) && request_ok(p, y.ctx, y.count) && row.t < y.count;
     row.plen = live ? (x.prefix ? x.ctx : x.base) : 0;

@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segment<typename SRC::Item> ahead{};
     typename SRC::Loads loads;
     Next got = Next::none;
-    const typename SRC::Lane lane_of(p, s.src, g, r % ROWS);
+    const typename SRC::template Lane<(REP > 1)> lane_of(p, s.src, g, r % ROWS);
     auto look_ahead = [&](int handed) {
       got = read_ring(handed, ahead);
       if constexpr (SRC::kTwoPlaces)
