@@ -20,11 +20,12 @@
 // at the same time; each line is cut into equal shares.  What a worker finds
 // of a row is a part: in the worker's own two slots if the run goes on in
 // another share, in a buffer of the rows if it does not; merge_kernel puts a
-// row's parts together in a fixed order.  A run that is all a row sees (no own
-// rows, or an empty prefix) and lies in one share is finished there.  With few
-// rows at d = 64 the copies of the tile's rows (scored_kernel.cuh) are parts
-// too: merging them inside the kernel cost 1 us at every run's end (8 prefixes
-// of 16 requests, caps and slopes: 61.6 us instead of 50.2 without the merge).
+// row's parts together in a fixed order.  (Runs that are all a row sees, without
+// own rows, could be finished by their worker: the code for it, in the kernel of
+// every call, cost 7 to 10% where runs are short, d = 128, and gained nothing.)
+// With few rows at d = 64 the copies of the tile's rows (scored_kernel.cuh) are
+// parts too: merging them inside the kernel cost 1 us at every run's end (8
+// prefixes of 16 requests, caps and slopes: 61.6 us instead of 50.2 without).
 // An SM's two workers are numbered far apart, so that one of them reads
 // prefixes and the other own rows where both lines are long: 64 requests of a
 // 16384-row prefix 81.6 -> 74.8 us.
@@ -32,8 +33,9 @@
 // Measured (a call among others; of the memory's copy rate, of the bf16 rate):
 // 64 requests with 100 to 1500 rows of their own behind one prefix of 16384, 32
 // heads of 128 on 8: 59.9 us, 70%, the main kernel 53 of them, the first tile's
-// arrival 4.2; 16 requests of up to 16 tokens behind 131072 rows 433 us, 58%; 4
-// beams of 24 sources, 16 heads of 64, 24.8 us, 49%.
+// arrival 4.2; 8 prefixes of 16 requests with cap and slopes, 12 heads of 64, 50.4
+// us, 56%; 16 requests of up to 16 tokens behind 131072 rows 433 us, 58%; 4 beams
+// of 24 sources, 16 heads of 64, 24.7 us, 50%.
 #include <cmath>
 
 #include "cache_source.cuh"
@@ -428,8 +430,6 @@ struct PrefixSource : CacheSource {
       lower_by_distance(sr, c, slope, row.pos, x.base + j0, base);
     }
   }
-  // The run is all that its rows see, and lies in one share (and the tile has one copy of its rows).
-  static __device__ bool whole(const Params& p, const Item& x) { return x.whole && (x.prefix ? !p.lens : x.base == 0); }
   // Parts of whole runs by the row of O; of others by the worker, as
   // CacheSource; those of the copies (r: the row of the tile) one after the other.
   static __device__ size_t slot_row(const Params& p, const Item& x, int g, int r) {
@@ -501,7 +501,6 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
   const Run pre = run_of(0, prt, pr, p.prow_group, p.prow_groups, 0);
   const Run own = run_of(1, rr / 128, rr % 128, p.row_group, p.row_groups, first_own);
   const int parts = (pre.n + own.n) * copies;
-  if (parts == 1) return;  // finished by its one worker (none: a row that sees nothing, 0)
   auto place = [&](int i) {
     const int copy = i & (copies - 1);
     i >>= shift;

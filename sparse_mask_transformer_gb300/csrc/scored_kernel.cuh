@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         continue;
       }
-      const bool whole = !(SRC::kTwoPlaces && REP > 1) && SRC::whole(p, seg.item);  // (a copy's row is a part)
+      const bool whole = !SRC::kTwoPlaces && SRC::whole(p, seg.item);  // (there every row is a part)
       const float scale = whole ? 1.f / l : 1.f;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
