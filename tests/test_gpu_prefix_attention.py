@@ -411,3 +411,47 @@ def random_case(seed):
 @pytest.mark.parametrize("seed", range(40))
 def test_random_cases(gpu_lib, seed):
     random_case(seed).run()
+
+
+def test_copies_from_the_host_and_events_come_before_a_call(gpu_lib):
+    """What a copy from pinned memory, or another stream behind an event, writes just before a call is what it reads."""
+    c = Case(2, 8, 2, 2, 128, [700, 90], [30, 0, 5, 200], seed=33)
+    a = c.args()
+    for name in ("kp", "vp", "k", "v", "q"):
+        a[name][~torch.isfinite(a[name])] = 0.0
+    settings = [([700, 90], [30, 0, 5, 200]), ([3, 120], [100, 7, 230, 0]), ([0, 1], [0, 0, 64, 65])]
+    want, pinned = [], []
+    for plens, lens in settings:
+        a["plens"].copy_(i32(plens))
+        a["lens"].copy_(i32(lens))
+        o = torch.full(c.q.shape, 5.0, dtype=c.dtype, device="cuda")
+        c.call(a, o)
+        want.append(o)
+        pinned.append([torch.tensor(x, dtype=torch.int32).pin_memory() for x in (plens, lens)])
+    q_host, side = a["q"].cpu().pin_memory(), torch.cuda.Stream()
+    big = torch.zeros(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for i in range(60):
+        n = i % 3
+        o = torch.full(c.q.shape, 5.0, dtype=c.dtype, device="cuda")
+        if i % 2:
+            a["q"].zero_()
+            a["q"].copy_(q_host, non_blocking=True)
+            for name, x in zip(("plens", "lens"), pinned[n]):
+                a[name].copy_(x, non_blocking=True)
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                a["q"].zero_()
+                big.add_(1.0)                            # some 80 us
+                a["q"].copy_(q_host, non_blocking=True)
+                for name, x in zip(("plens", "lens"), pinned[n]):
+                    a[name].copy_(x, non_blocking=True)
+                done = side.record_event()
+            torch.cuda.current_stream().wait_event(done)
+        c.call(a, o)
+        got.append((n, o))
+    torch.cuda.synchronize()
+    for n, o in got:
+        assert torch.equal(o, want[n])
