@@ -813,8 +813,9 @@ stof_status stof_cache_keep(const stof_caches* caches, int T, const int32_t* len
  * src[b] >= 0,
  *   row i of slot b of `to` <- row i of slot s of `from`     for i < lens[s].
  *   to       caches of as many layers, heads and elements as `from`, slots and
- *            rows of their own; apart from `from`, or the very same caches:
- *            then slot b with src[b] = b stays as it is, and a slot that is
+ *            rows of their own; sharing no memory with `from`, or the very
+ *            same caches in the same order (else STOF_ERR_INVALID_ARG): then
+ *            slot b with src[b] = b stays as it is, and a slot that is
  *            copied to may not be one that others are copied from.
  *   src      device int32 [to->slots]; negative: the slot stays as it is;
  *   lens     device int32 [from->slots]: rows of each slot;

@@ -891,8 +891,9 @@ class Caches:
             raise StofError(STOF_ERR_SHAPE, "Caches: tensors must be contiguous [slots, heads, rows, d] of one shape and type")
         if max(shape) > INT32_MAX:  # (ctypes would keep the low 32 bits)
             raise StofError(STOF_ERR_SHAPE, "Caches: sizes must be below 2^31")
-        if len({t.data_ptr() for t in self.tensors}) != len(self.tensors):
-            raise StofError(STOF_ERR_INVALID_ARG, "Caches: a tensor is given twice")
+        at = sorted(t.data_ptr() for t in self.tensors)
+        if any(b - a < self.tensors[0].nbytes for a, b in zip(at, at[1:])):
+            raise StofError(STOF_ERR_INVALID_ARG, "Caches: tensors overlap, or one is given twice")
         self.slots, self.heads, self.rows, self.d = shape
         self.dtype = dtype
         self._data = (ctypes.c_void_p * len(self.tensors))(*(t.data_ptr() for t in self.tensors))

@@ -69,6 +69,23 @@ def test_bad_forks_are_refused(lib):
         assert call(**kw) == stof.STOF_ERR_ALIGNMENT, kw
 
 
+def test_forks_between_overlapping_caches_are_refused(lib):
+    size = 4 * 2 * 64 * 64 * 2  # bytes of a cache
+    a = caches()
+    for data in ((2 * FAKE, FAKE), (8 * FAKE, FAKE + size - 16), (2 * FAKE - size + 16, 8 * FAKE)):
+        assert lib.stof_cache_fork(a, caches(data), FAKE, 2 * FAKE, None, None, None) == stof.STOF_ERR_INVALID_ARG, data
+    # a smaller set that begins inside one of the larger
+    assert lib.stof_cache_fork(a, caches((8 * FAKE, 2 * FAKE + size // 2), rows=32), FAKE, 2 * FAKE, None, None,
+                               None) == stof.STOF_ERR_INVALID_ARG
+    # side by side is no overlap: the next check answers
+    for data in ((FAKE + size, 2 * FAKE + size), (FAKE - size, 2 * FAKE - size)):
+        assert lib.stof_cache_fork(a, caches(data), FAKE + 2, 2 * FAKE, None, None, None) == stof.STOF_ERR_ALIGNMENT, data
+    # sizes whose product passes 64 bits
+    wide = dict(slots=(1 << 31) - 1, rows=(1 << 31) - 1)
+    assert lib.stof_cache_fork(caches(**wide), caches((8 * FAKE, 9 * FAKE), **wide), FAKE, 2 * FAKE, None, None,
+                               None) == stof.STOF_ERR_INVALID_ARG
+
+
 def test_binding_refuses_host_tensors(lib):
     with pytest.raises(stof.StofError) as e:
         stof.Caches([torch.zeros(2, 2, 8, 64, dtype=torch.float16)])

@@ -235,3 +235,16 @@ def test_caches_of_different_shapes_are_refused(gpu_lib):
     with pytest.raises(stof.StofError) as e:
         stof.stof_cache_keep(c, i32([0, 0, 0]), i32([[0], [0]]), i32([0, 0]))
     assert e.value.status == stof.STOF_ERR_SHAPE
+
+
+def test_overlapping_caches_are_refused(gpu_lib):
+    c = torch.zeros(6, 2, 8, 64, dtype=torch.float16, device="cuda")
+    d = torch.zeros_like(c)
+    with pytest.raises(stof.StofError) as e:
+        stof.Caches([c[:4], c[2:]])
+    assert e.value.status == stof.STOF_ERR_INVALID_ARG
+    stof.Caches([c[3:], c[:3]])  # side by side
+    src, lens = torch.zeros(6, dtype=torch.int32, device="cuda"), torch.ones(6, dtype=torch.int32, device="cuda")
+    with pytest.raises(stof.StofError) as e:
+        stof.stof_cache_fork(stof.Caches([c, d]), stof.Caches([d, c]), src, lens)
+    assert e.value.status == stof.STOF_ERR_INVALID_ARG
