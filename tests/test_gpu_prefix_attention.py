@@ -455,3 +455,52 @@ def test_copies_from_the_host_and_events_come_before_a_call(gpu_lib):
     torch.cuda.synchronize()
     for n, o in got:
         assert torch.equal(o, want[n])
+
+
+def test_captured_calls_between_copies_and_joined_streams(gpu_lib):
+    """In a graph: a copy node, or a copy and kernels of a joined stream, before the call; behind it a copy of its output
+    and then kernels that overwrite its inputs."""
+    c = Case(2, 8, 2, 2, 128, [700, 90], [30, 0, 5, 200], seed=34)
+    a = c.args()
+    for name in ("kp", "vp", "k", "v", "q"):
+        a[name][~torch.isfinite(a[name])] = 0.0
+    settings = [([700, 90], [30, 0, 5, 200]), ([3, 120], [100, 7, 230, 0]), ([0, 1], [0, 0, 64, 65])]
+    want = []
+    for plens, lens in settings:
+        a["plens"].copy_(i32(plens))
+        a["lens"].copy_(i32(lens))
+        want.append(torch.full(c.q.shape, 5.0, dtype=c.dtype, device="cuda"))
+        c.call(a, want[-1])
+    staged = [a["plens"].clone(), a["lens"].clone(), a["q"].clone()]
+    names = ("plens", "lens", "q")
+    big = torch.zeros(1 << 24, device="cuda")
+    o = torch.full(c.q.shape, 5.0, dtype=c.dtype, device="cuda")
+    out = torch.empty_like(o)
+    graphs = []
+    for joined in (False, True):
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            o.fill_(5.0)
+            if joined:
+                here, side = torch.cuda.current_stream(), torch.cuda.Stream()
+                side.wait_stream(here)
+                with torch.cuda.stream(side):
+                    big.add_(1.0)
+                    for name, x in zip(names, staged):
+                        a[name].copy_(x)
+                big.neg()  # beside it
+                here.wait_stream(side)
+            else:
+                for name, x in zip(names, staged):
+                    a[name].copy_(x)
+            c.call(a, o)
+            out.copy_(o)
+            for name in names:  # (after the call has read them)
+                a[name].fill_(-7)
+    for i in range(60):
+        n = i % 3
+        for x, y in zip(staged, settings[n]):
+            x.copy_(i32(y))
+        graphs[i // 3 % 2].replay()
+        assert torch.equal(out, want[n]), i
