@@ -201,9 +201,9 @@ struct PrefixSource : CacheSource {
         __syncthreads();  // the sums have been read
       }
       v = item_lengths(p, m, i);
-      if (blockIdx.x == 0) report(p, s, m, i);
       int2 total;
       at = both_prefixes(v, s.sums, total);
+      if (blockIdx.x == 0) report(p, s, m, i);  // behind a barrier: `bad` has been cleared by another warp
       at = make_int2(all.x + at.x, all.y + at.y);
       if (blockIdx.x == 0) {  // for merge_kernel
         if (i < p.NP) p.pline[i] = at.x;
