@@ -28,6 +28,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <type_traits>
@@ -237,18 +238,12 @@ bool rows_of(const Rows& r, int e) {
   return reinterpret_cast<uintptr_t>(r.data) % (2 * e) == 0 && r.sb % e == 0 && r.sh % e == 0 && r.st % e == 0;
 }
 
-template <bool BF16, bool INTER, int E, class PARAMS>
-cudaError_t launch(PARAMS& p, long long tokens, cudaStream_t s) {
-  constexpr int PAIRS = kPairs<E, INTER>;
-  const long long units = p.rot / 2 / PAIRS, heads = p.H + p.Hkv;
-  // Head slots per token: as few as come near the 1024 threads per SM that
-  // are resident (an angle is then computed for as many heads as can be), up
-  // to a thread per head when there are few tokens.  16384 tokens, 40 heads of
-  // 128: 1 slot 71.6 us, 2 slots 67.5, 4 slots 69.8, 8 slots 73.8.
-  // Accesses of 8 bytes want four times as many threads: 16384 tokens, 48 heads
-  // of 80, half of each turned, 2 slots 102 us, 8 slots 60; of 72, all turned, 2
-  // slots 49.2, 4 slots 51.4.
-  const long long want = (E == 4 ? 4 : 1) * 870ll * device_sm_count();
+// Head slots per token, one axis: as few as come near the 1024 threads per SM
+// that are resident (an angle is then computed for as many heads as can be), up
+// to a thread per head when there are few tokens.  16384 tokens, 40 heads of
+// 128: 1 slot 71.6 us, 2 slots 67.5, 4 slots 69.8, 8 slots 73.8.
+long long slots_of(const RopeParams& p, long long tokens, long long units, int) {
+  const long long want = 870ll * device_sm_count(), heads = p.H + p.Hkv;
   long long slots = (want + tokens * units - 1) / (tokens * units);
   if (slots > heads) slots = heads;
   // as many heads for every slot where a number up to twice as large divides them (3 slots for 32 heads: 41.5 us, 4: 36.2)
@@ -258,13 +253,44 @@ cudaError_t launch(PARAMS& p, long long tokens, cudaStream_t s) {
       break;
     }
   }
-  if (std::is_same<PARAMS, AxesParams>::value) {
-    // no second round of a few blocks behind the first (608 are resident): 9805
-    // tokens of 32 heads of 64, 4 slots on 613 blocks 28.0 us, 3 slots 25.3; 16384
-    // of 32 heads of 80, 2 slots on 640 blocks 55.3, one 53.5, 3 slots 48.8
-    const long long fit = static_cast<long long>(kThreadsRope) * kBlocksRope * device_sm_count(), n = tokens * units * slots;
-    if (n > fit && n < fit + fit / 16) slots += slots > 2 ? -1 : (slots < heads ? 1 : 0);
-  }
+  return slots;
+}
+
+// Several axes.  The most slots that the resident threads hold are best, and a
+// little more than that is a second round of a few blocks, the worst.  Over 161
+// calls of 16 to 65536 tokens, all access widths and parts of heads turned, each
+// timed with 1 to 32 slots, the rule is 4% over the best number of slots in the
+// mean and 30% at most (6000 tokens of 40 heads of 128, half turned: 7 slots 42.5
+// us, 6 32.7).
+// - One wave of the resident threads where it holds two slots or more: 9805
+//   tokens of 32 heads of 64, 3 slots (0.76 waves) 24.1 us, 4 (1.01) 27.3; 10500:
+//   25.1, (1.08) 28.2; 12500: 28.5, (1.28) 31.3; 4096 of 72, 4 (0.95) 15.2, 5
+//   (1.18) 19.6, 16 (3.8) 21.6; 14000 of 64, 2 (0.72) 31.3, 4 (1.44) 32.8.
+// - Else a wave and a half or more: 24000 of 64, 1 slot (0.62) 52.0, 2 (1.23)
+//   55.1, 3 (1.85) 50.5; 16384 of 128, 1 (0.84) 75.3, 2 (1.68) 68.3, 4 68.7; 16384
+//   of 72, 1 (0.95) 47.4, 2 47.4, 4 50.2.
+// - At most kCopiesMost copies a thread of what is not turned, 16: 24000 tokens
+//   of 40 heads of 128, half of each turned, 2 slots (56 copies) 139, 4 119, 8 109;
+//   16384 of 32 heads of 80, half turned, 4 (32) 67.9, 8 59.0, 16 62.3; V alone, 16384
+//   of 72, 1 slot (32) 47.4, 2 47.4, 3 50.5.
+// - No more slots than give a thread that many heads: 1000 tokens of 32 heads of
+//   72, 24 slots 9.9 us, 16 7.5.
+constexpr long long kCopiesMost = 16;
+long long slots_of(const AxesParams& p, long long tokens, long long units, int e) {
+  const long long wave = static_cast<long long>(kThreadsRope) * kBlocksRope * device_sm_count(), n = tokens * units;
+  const long long heads = p.H + p.Hkv;
+  const long long copies = (p.d - p.rot) / e * heads + (p.has_v ? p.d / e * static_cast<long long>(p.Hkv) : 0);
+  long long slots = wave / n;
+  if (slots < 2) slots = (3 * wave + 2 * n - 1) / (2 * n);
+  slots = std::max(slots, (copies + kCopiesMost * units - 1) / (kCopiesMost * units));
+  slots = std::max(1ll, std::min({slots, heads, ((1ll << 31) - 1) / n}));  // threads are counted in 32 bits
+  const long long each = (heads + slots - 1) / slots;
+  return (heads + each - 1) / each;
+}
+
+template <bool BF16, bool INTER, int E, class PARAMS>
+cudaError_t launch(PARAMS& p, long long tokens, cudaStream_t s) {
+  const long long units = p.rot / 2 / kPairs<E, INTER>, slots = slots_of(p, tokens, units, E);
   p.slots = static_cast<int>(slots);
   p.n_threads = static_cast<uint32_t>(tokens * units * slots);
   const unsigned grid = static_cast<unsigned>((tokens * units * slots + kThreadsRope - 1) / kThreadsRope);
