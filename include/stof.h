@@ -778,8 +778,8 @@ stof_status stof_rope_axes_bwd(const stof_rope_axes* axes, const stof_rope_rows*
 
 /* The K and V caches of some layers, all of one shape: data[i] is device
  * memory of [slots][heads][rows][d] 16-bit elements, contiguous, 16-byte
- * aligned, none of them overlapping another; slot b is request b's.  HOST
- * struct and array, copied at the call. */
+ * aligned, none of them overlapping another (STOF_ERR_INVALID_ARG); slot b is
+ * request b's.  HOST struct and array, copied at the call. */
 #define STOF_CACHES_MAX 256
 typedef struct {
   void* const* data;  /* [n] */

@@ -166,6 +166,12 @@ struct Sorted {
     for (int i = 0; i < n; ++i) at[i] = reinterpret_cast<uintptr_t>(c->data[i]);
     if (!std::is_sorted(at, at + n)) std::sort(at, at + n);
   }
+  // Whether two of the set share bytes: their rows would be moved by several threads in no order.
+  bool overlapping() const {
+    for (int i = 1; i < n; ++i)
+      if (at[i] - at[i - 1] < bytes) return true;
+    return false;
+  }
 };
 
 // Whether a cache of one set shares bytes with one of the other.  The one that
@@ -191,6 +197,7 @@ extern "C" stof_status stof_cache_keep(const stof_caches* caches, int T, const i
   if (st != STOF_OK) return st;
   if (!lens || !path || !kept || T < 1 || new_lens == lens || (new_lens && new_lens == kept)) return STOF_ERR_INVALID_ARG;
   if (T > STOF_TREE_MAX_TOKENS || caches->slots > 65535) return STOF_ERR_SHAPE;
+  if (Sorted(caches).overlapping()) return STOF_ERR_INVALID_ARG;
   const uintptr_t words = reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(path) |
                           reinterpret_cast<uintptr_t>(kept) | reinterpret_cast<uintptr_t>(new_lens);
   if (words % 4 || reinterpret_cast<uintptr_t>(device_error) % 8) return STOF_ERR_ALIGNMENT;
@@ -222,7 +229,12 @@ extern "C" stof_status stof_cache_fork(const stof_caches* from, const stof_cache
   int equal = 0;
   for (int i = 0; i < from->n; ++i) equal += from->data[i] == to->data[i];
   if (equal && (equal != from->n || from->slots != to->slots || from->rows != to->rows)) return STOF_ERR_INVALID_ARG;
-  if (!equal && (new_lens == lens || overlap(Sorted(from), Sorted(to)))) return STOF_ERR_INVALID_ARG;
+  const Sorted sources(from);
+  if (sources.overlapping()) return STOF_ERR_INVALID_ARG;
+  if (!equal) {
+    const Sorted places(to);
+    if (new_lens == lens || places.overlapping() || overlap(sources, places)) return STOF_ERR_INVALID_ARG;
+  }
   const uintptr_t words = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(lens) |
                           reinterpret_cast<uintptr_t>(new_lens);
   if (words % 4 || reinterpret_cast<uintptr_t>(device_error) % 8) return STOF_ERR_ALIGNMENT;

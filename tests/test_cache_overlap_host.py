@@ -40,6 +40,8 @@ def test_overlap_of_two_sets_is_that_of_some_pair(lib, seed):  # noqa: F811
     same = any(p == q for p, q in zip(a, b))  # equal sets of other sizes are refused too
     if a == b and more == 1:  # the very same caches, which a fork takes
         some = same = False
+    # a set that overlaps itself (the shifted ones may)
+    some |= any(p != q and p < q + BYTES * more and q < p + BYTES * more for p in b for q in b)
     want = stof.STOF_ERR_INVALID_ARG if some or same else stof.STOF_ERR_ALIGNMENT
     assert fork(lib, x, y) == want and fork(lib, y, x) == want
 
@@ -61,3 +63,19 @@ def test_the_check_does_not_take_all_pairs(lib, shuffled):  # noqa: F811
                 fork(lib, a, to)
             best[i] = min(best[i], time.perf_counter() - begin)
     assert best[1] < 15 * best[0], best
+
+
+@pytest.mark.parametrize("n", [2, 3, 24, 256])
+@pytest.mark.parametrize("by", [0, 16, BYTES - 16, BYTES])
+def test_caches_of_one_set_that_overlap_are_refused(lib, n, by):  # noqa: F811
+    """One given twice, or two that share bytes: in the set that is kept, copied from, copied to, or both."""
+    rng = random.Random(n + by)
+    bad, far = [FAKE + 3 * BYTES * i for i in range(n - 1)], [1 << 30, *(2 * FAKE + FAKE * (i + 600) for i in range(n - 1))]
+    bad.append(rng.choice(bad) + by)
+    rng.shuffle(bad)
+    x, y = caches(bad, **SIZES), caches(far, **SIZES)
+
+    want = stof.STOF_ERR_ALIGNMENT if by == BYTES else stof.STOF_ERR_INVALID_ARG
+    for a, b in ((x, y), (y, x), (x, x)):
+        assert fork(lib, a, b) == want
+    assert lib.stof_cache_keep(x, 4, FAKE + 2, 2 * FAKE, 3 * FAKE, None, None, None) == want  # lens is misaligned
