@@ -461,7 +461,8 @@ size_t stof_tree_attn_workspace_bytes(int B, int H, int Hkv, int T, int d);
  *              stof_tree_attn_fwd(), with the call's error bits in its first
  *              8 bytes.
  * Other arguments, sizes, finite V rows, precision and errors as
- * stof_tree_attn_fwd(); prefix_cap + cap below 2^31.  Asynchronous on stream;
+ * stof_tree_attn_fwd(); prefix_cap + cap (without own caches: + 1) below
+ * 2147480000, 3648 short of 2^31 (else STOF_ERR_SHAPE).  Asynchronous on stream;
  * all lengths are read on the device only.
  */
 stof_status stof_prefix_attn_fwd(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
