@@ -241,8 +241,9 @@ stof_status launch_blockwise(const AttnParams& p, bool bf16, cudaStream_t s);
 stof_status launch_blockwise_persist64(const AttnParams& p, bool bf16, cudaStream_t s);
 // TMA map of a [heads][L][D] 16-bit tensor, boxes of 64 columns x box_rows rows of
 // one head (zeros past row L), 128-byte swizzle.
-// Maps are kept in a small per-process cache keyed by (device, base, rows,
-// D, box_rows, type), so repeated calls on the same tensors do no driver call.
+// Maps are kept in a per-process cache of some thousand, keyed by all that they
+// hold (device, address, sizes of every dimension, box, type), so repeated calls
+// on the same tensors do no driver call.
 bool make_bw_map(CUtensorMap* m, const void* base, uint64_t heads, uint64_t L, int D, int box_rows, bool bf16);
 // The same of a [B][heads][L][D] tensor with boxes of box_rows rows of one head of box_requests requests.
 bool make_requests_map(CUtensorMap* m, const void* base, uint64_t B, uint64_t heads, uint64_t L, int D, int box_rows,

@@ -34,8 +34,8 @@
 // 64 requests with 100 to 1500 rows of their own behind one prefix of 16384, 32
 // heads of 128 on 8: 59.9 us, 70%, the main kernel 53 of them, the first tile's
 // arrival 4.2; 8 prefixes of 16 requests with cap and slopes, 12 heads of 64, 50.4
-// us, 56%; 16 requests of up to 16 tokens behind 131072 rows 433 us, 58%; 4 beams
-// of 24 sources, 16 heads of 64, 24.7 us, 50%.
+// us, 56%; 16 requests of up to 16 tokens behind 131072 rows 433 to 442 us, 57%; 4
+// beams of 24 sources, 16 heads of 64, 24.7 us, 50%.
 #include <cmath>
 
 #include "cache_source.cuh"

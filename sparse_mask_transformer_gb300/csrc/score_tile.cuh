@@ -185,6 +185,11 @@ __device__ __forceinline__ void lower_by_positions(uint32_t (&sr)[CHUNKS][32], f
     }
 }
 
+// P is rounded to the call's type, the one that the tensor cores take beside V
+// at their full rate and that leaves TMEM room for two workers: half a step of a
+// p_j each, beside the output's own.  (Measured over the shared prefix's calls,
+// the 2-norm of the error is 1.04 to 1.4 times that of the output's rounding
+// alone.)  Scores, maxima, sums and O stay in fp32.
 // The sum of P that O is divided by is that of the rounded values which the
 // tensor cores multiply: a rounding d of p_j then moves O by d (V_j - O), not
 // d V_j, so a key that has nearly all the weight is not rounded at all.
