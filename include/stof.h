@@ -441,7 +441,8 @@ size_t stof_tree_attn_workspace_bytes(int B, int H, int Hkv, int T, int d);
  * over the first prefix_lens[p] rows of prefix p and the rows of request b's
  * own cache that stof_tree_attn_fwd() gives it (lens[b] committed ones, then
  * drafted ones by its tree row).  A prefix is read once for its group, not
- * once per request.
+ * once per request.  (Groups of unequal size are filled up with requests whose
+ * counts[b] is 0.)
  *   q, o       device [B][H][T][d], dt; o is written and overlaps no input.
  *   k_prefix, v_prefix  device [n_prefixes][Hkv][prefix_cap][d], dt.  Rows
  *              from prefix_lens[p] on are not used, whatever they hold.
