@@ -472,14 +472,16 @@ extern "C" stof_status stof_rope_bwd(const stof_rope_plan* plan, const stof_rope
 extern "C" stof_status stof_rope_axes_init(stof_rope_axes* axes, const stof_rope_plan* plan, int n_axes,
                                            const int32_t* axis_of_pair) {
   if (!axes) return STOF_ERR_INVALID_ARG;
+  stof_rope_plan turn = {};  // the plan may be *axes' own
+  if (plan) turn = *plan;
   std::memset(axes, 0, sizeof(*axes));
-  if (!plan_ok(plan) || !axis_of_pair || n_axes < 1) return STOF_ERR_INVALID_ARG;
+  if (!plan || !plan_ok(&turn) || !axis_of_pair || n_axes < 1) return STOF_ERR_INVALID_ARG;
   if (n_axes > STOF_ROPE_MAX_AXES) return STOF_ERR_UNSUPPORTED;
-  for (int i = 0; i < plan->rot_dim / 2; ++i)
+  for (int i = 0; i < turn.rot_dim / 2; ++i)
     if (axis_of_pair[i] < 0 || axis_of_pair[i] >= n_axes) return STOF_ERR_INVALID_ARG;
-  axes->turn = *plan;
+  axes->turn = turn;
   axes->n_axes = n_axes;
-  for (int i = 0; i < plan->rot_dim / 2; ++i) axes->axis[i] = static_cast<uint8_t>(axis_of_pair[i]);
+  for (int i = 0; i < turn.rot_dim / 2; ++i) axes->axis[i] = static_cast<uint8_t>(axis_of_pair[i]);
   axes->made = 1;
   return STOF_OK;
 }
