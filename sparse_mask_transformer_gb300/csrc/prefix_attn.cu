@@ -33,7 +33,7 @@
 // Measured (a call among others; of the memory's copy rate, of the bf16 rate):
 // 64 requests with 100 to 1500 rows of their own behind one prefix of 16384, 32
 // heads of 128 on 8: 59.9 us, 70%, the main kernel 53 of them, the first tile's
-// arrival 4.2; 8 prefixes of 16 requests with cap and slopes, 12 heads of 64, 50.4
+// arrival 4.2; 8 prefixes of 16 requests with cap and slopes, 12 heads of 64, 50.8
 // us, 56%; 16 requests of up to 16 tokens behind 131072 rows 433 to 442 us, 57%; 4
 // beams of 24 sources, 16 heads of 64, 24.7 us, 50%.
 #include <cmath>
@@ -203,11 +203,11 @@ struct PrefixSource : CacheSource {
       v = item_lengths(p, m, i);
       int2 total;
       at = both_prefixes(v, s.sums, total);
-      if (blockIdx.x == 0) report(p, s, m, i);  // behind a barrier: `bad` has been cleared by another warp
       at = make_int2(all.x + at.x, all.y + at.y);
       if (blockIdx.x == 0) {  // for merge_kernel
         if (i < p.NP) p.pline[i] = at.x;
         if (i < p.B) p.line[i] = at.y;
+        report(p, s, m, i);  // behind a barrier: `bad` has been cleared by another warp
       }
       all = make_int2(all.x + total.x, all.y + total.y);
     }
